@@ -1,0 +1,308 @@
+"""What is measured of the row operators: RMS norm, linear and gated layers.
+
+They are the per-voxel ("1x1x1") half of a sparse network: between two sparse
+convolutions every active voxel's feature row is normalised, projected, gated
+and added back to the residual stream. Rows are the active voxels of a scene
+(1 to 95,000), channels those of the convolution stages.
+
+Three operators, each with a serving and a training form:
+
+- norm:   s = x + r;  y = s / sqrt(mean(s^2) + eps) * w, as 16 bits or as e4m3
+          with one float32 scale a row;
+- linear: y = act(x W + b) + r, x and W in 16 bits or e4m3 with scales;
+- gated:  h = act(x Wg + bg) * (x Wu + bu), W = [Wg | Wu] in one tensor.
+
+`run` takes them through elementary torch operations in float32 where `own` is
+false, and through the package's entry points where it is true.
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-6
+E4M3_MAX = 448.0
+TINY = 2.0 ** -126          # the smallest scale of a row
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+ACTIVATIONS = ("none", "relu", "silu", "gelu")
+
+
+def _case(name, op, form, dtype, n, c_in, c_out, act="none", bias=False, residual=False):
+    return dict(name=name, op=op, form=form, dtype=dtype, n=n, c_in=c_in, c_out=c_out, act=act,
+                bias=bias, residual=residual)
+
+
+def listed():
+    return [
+        # one voxel's row through the norm in front of a block: latency
+        _case("norm_single", "norm", "forward", "bf16", 1, 512, 512, residual=True),
+        # the 91k-voxel stage: residual stream in, normalised rows and the new stream out
+        _case("norm_stage", "norm", "forward", "bf16", 91000, 128, 128, residual=True),
+        # the deep stage served in 8 bits: the norm writes what an e4m3 product reads
+        _case("norm_e4m3_deep", "norm", "e4m3", "bf16", 15000, 512, 512, residual=True),
+        # training on the largest scene: the norm's gradients, the stream's gradient added
+        _case("norm_backward_wide", "norm", "backward", "bf16", 95000, 128, 128, residual=True),
+        # one row through a block's second projection: the weights are all the traffic
+        _case("linear_single", "linear", "forward", "bf16", 1, 2048, 512, bias=True, residual=True),
+        # the pointwise layer of a residual block on the 91k-voxel stage
+        _case("linear_stage", "linear", "forward", "bf16", 91000, 128, 128, "relu", True, True),
+        # odd channel counts and rows, half precision: a head on a LiDAR scene
+        _case("linear_ragged", "linear", "forward", "f16", 32371, 200, 72, "gelu", True, False),
+        # training the second projection of the deep stage's block
+        _case("linear_backward_deep", "linear", "backward", "bf16", 15000, 2048, 512, bias=True),
+        # one row through a gated layer whose width is no multiple of anything
+        _case("gated_single", "gated", "forward", "bf16", 1, 512, 1365, "silu"),
+        # the gated layer of the 91k-voxel stage (8/3 of the channels, in eights)
+        _case("gated_stage", "gated", "forward", "bf16", 91000, 128, 344, "silu"),
+        # the deep stage served in 8 bits, reading the norm's rows and scales
+        _case("gated_e4m3_deep", "gated", "e4m3", "bf16", 15000, 512, 2048, "silu"),
+        # training the deep stage's gated layer: the most work of all
+        _case("gated_backward_deep", "gated", "backward", "bf16", 15000, 512, 2048, "silu"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _channels(rng, lo, hi):
+    c = _log_int(rng, lo, hi)
+    u = rng.random()
+    if u < 0.5:                                     # half of them in sixteens
+        return max(16, c // 16 * 16)
+    return max(8, c // 8 * 8) if u < 0.75 else c    # then eights, then anything
+
+
+def draw(rng):
+    most = max((work(c) for c in listed()), key=lambda w: w["flops"])["flops"]
+    most_bytes = max(work(c)["bytes"] for c in listed())
+    while True:
+        op = rng.choice(("norm", "linear", "gated"))
+        form = rng.choice(("forward", "forward", "backward", "e4m3"))
+        c_in = _channels(rng, 16, 2048 if op == "linear" else 512)
+        c_out = c_in if op == "norm" else _channels(rng, 16, 2048)
+        if form == "e4m3" and op != "norm":
+            c_in = max(16, c_in // 16 * 16)         # e4m3 rows are 16-byte words
+        act = {"norm": "none", "linear": rng.choice(ACTIVATIONS),
+               "gated": rng.choice(ACTIVATIONS[1:])}[op]
+        case = dict(op=op, form=form, dtype=rng.choice(("bf16", "bf16", "f16")),
+                    n=_log_int(rng, 1, 95000), c_in=c_in, c_out=c_out, act=act,
+                    bias=op != "norm" and rng.random() < 0.5,
+                    residual=op == "norm" and rng.random() < 0.7
+                    or op == "linear" and form != "backward" and rng.random() < 0.5)
+        w = work(case)
+        if w["flops"] <= most and w["bytes"] <= most_bytes:
+            return case
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+    n, c_in, c_out, op, form = (case[k] for k in ("n", "c_in", "c_out", "op", "form"))
+    wide = 2 * c_out if op == "gated" else c_out
+
+    def normal(shape, std=1.0):
+        return torch.randn(shape, generator=g, device="cuda") * std
+
+    state = dict(case=case, x=normal((n, c_in)).to(dt))
+    if op == "norm":
+        state["w"] = (1.0 + normal(c_in, 0.1)).to(dt)
+        if case["residual"]:                        # backward: the stream's own gradient
+            state["residual"] = normal((n, c_in), 2.0).to(dt)
+        if form == "backward":
+            state["dy"] = normal((n, c_in), 0.1).to(dt)
+        return state
+    w = normal((c_in, wide), 1.0 / math.sqrt(c_in))
+    if form == "e4m3":                              # rows as the norm writes them, weights quantised once
+        state["x"], state["x_scale"] = _quantise(state["x"].float())
+        state["w"], state["w_scale"] = _quantise(w.t())
+    else:
+        state["w"] = w.to(dt)
+    if case["bias"]:
+        state["bias"] = normal(wide, 0.1).to(dt)
+    if case["residual"]:
+        state["residual"] = normal((n, c_out), 2.0).to(dt)
+    if form == "backward":
+        state["dy"] = normal((n, c_out), 0.1).to(dt)
+    return state
+
+
+# ---- the plain forms ----------------------------------------------------------
+
+
+def _quantise(y):
+    """float32 rows -> (e4m3 rows, float32 scale of each row)."""
+    scale = (y.abs().amax(1, keepdim=True) / E4M3_MAX).clamp(min=TINY)
+    return (y / scale).to(torch.float8_e4m3fn), scale.squeeze(1)
+
+
+def _act(z, act):
+    if act == "relu":
+        return torch.where(z < 0, torch.zeros_like(z), z)
+    if act == "silu":
+        return z / (1 + torch.exp(-z))
+    if act == "gelu":
+        return 0.5 * z * (1 + torch.erf(z * math.sqrt(0.5)))
+    return z
+
+
+def _act_slope(z, act):
+    if act == "relu":
+        return (z > 0).to(z.dtype)
+    if act == "silu":
+        sg = 1 / (1 + torch.exp(-z))
+        return sg * (1 + z * (1 - sg))
+    if act == "gelu":
+        return (0.5 * (1 + torch.erf(z * math.sqrt(0.5)))
+                + z * torch.exp(-0.5 * z * z) * (1 / math.sqrt(2 * math.pi)))
+    return torch.ones_like(z)
+
+
+def _plain_norm(st, dt, form):
+    x, w = st["x"].float(), st["w"].float()
+    if form == "backward":
+        dy = st["dy"].float()
+        rstd = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + EPS)
+        xhat = x * rstd
+        a = dy * w
+        dx = rstd * (a - xhat * (a * xhat).mean(1, keepdim=True))
+        if "residual" in st:
+            dx = dx + st["residual"].float()
+        return dx.to(dt), (dy * xhat).sum(0).to(dt)
+    s = x + st["residual"].float() if "residual" in st else x
+    y = s * (1 / torch.sqrt((s * s).mean(1, keepdim=True) + EPS)) * w
+    out = _quantise(y) if form == "e4m3" else (y.to(dt),)
+    return out + ((s.to(dt),) if "residual" in st else ())
+
+
+def _plain_product(st, form):
+    x, w = st["x"].float(), st["w"].float()
+    if form == "e4m3":
+        z = (x * st["x_scale"][:, None]) @ (w * st["w_scale"][:, None]).t()
+    else:
+        z = x @ w
+    return z + st["bias"].float() if "bias" in st else z
+
+
+def _plain_gradients(st, dz, dt):
+    out = ((dz @ st["w"].float().t()).to(dt), (st["x"].float().t() @ dz).to(dt))
+    return out + ((dz.sum(0).to(dt),) if "bias" in st else ())
+
+
+def _plain_linear(st, dt, form, act):
+    if form == "backward":
+        dz = st["dy"].float()
+        if act != "none":
+            dz = dz * _act_slope(_plain_product(st, form), act)
+        return _plain_gradients(st, dz, dt)
+    y = _act(_plain_product(st, form), act)
+    if "residual" in st:
+        y = y + st["residual"].float()
+    return y.to(dt)
+
+
+def _plain_gated(st, dt, form, act):
+    gate, up = _plain_product(st, form).chunk(2, 1)
+    if form == "backward":
+        dh = st["dy"].float()
+        dz = torch.cat((dh * up * _act_slope(gate, act), dh * _act(gate, act)), 1)
+        return _plain_gradients(st, dz, dt)
+    return (_act(gate, act) * up).to(dt)
+
+
+def run(state):
+    case = state["case"]
+    op, form, act, dt = case["op"], case["form"], case["act"], DTYPES[case["dtype"]]
+    if not own:
+        if op == "norm":
+            return _plain_norm(state, dt, form)
+        return (_plain_linear if op == "linear" else _plain_gated)(state, dt, form, act)
+    import submanifold_sparse_convolution_amd as smc
+    x, w, residual = state["x"], state["w"], state.get("residual")
+    if op == "norm":
+        if form == "backward":
+            return smc.rms_norm_backward(state["dy"], x, w, eps=EPS, ds=residual)
+        return smc.rms_norm(x, w, residual=residual, eps=EPS, e4m3=form == "e4m3")
+    bias = state.get("bias")
+    if form == "backward":
+        back = smc.linear_backward if op == "linear" else smc.gated_backward
+        grads = back(state["dy"], x, w, bias=bias, activation=act)
+        return grads if bias is not None else grads[:2]
+    scales = {k: state[k] for k in ("x_scale", "w_scale") if k in state}
+    if scales:
+        scales["dtype"] = dt
+    if op == "linear":
+        return smc.linear(x, w, bias=bias, residual=residual, activation=act, **scales)
+    return smc.gated(x, w, bias=bias, activation=act, **scales)
+
+
+def work(case):
+    """Each input read once, each output written once; 2 operations a product term."""
+    n, c, m, op, form = (case[k] for k in ("n", "c_in", "c_out", "op", "form"))
+    if op == "norm":
+        per = 4 + (4 if case["residual"] else 0)            # x in and y out, r in and s out
+        if form == "e4m3":
+            per -= 1
+        if form == "backward":
+            per = 6 + (2 if case["residual"] else 0)        # x, dy (and ds) in, dx out
+        return dict(bytes=n * c * per + (4 * n if form == "e4m3" else 0)
+                    + c * (4 if form == "backward" else 2), flops=8 * n * c)
+    wide = 2 * m if op == "gated" else m
+    vec = wide * 2 if case["bias"] else 0
+    product = 2 * n * c * wide
+    if form == "backward":
+        products = 2 if op == "linear" and case["act"] == "none" else 3
+        return dict(bytes=4 * n * c + 2 * n * m + 4 * c * wide + 2 * vec, flops=products * product)
+    size = 1 if form == "e4m3" else 2
+    extra = 4 * (n + wide) if form == "e4m3" else 0
+    return dict(bytes=size * c * (n + wide) + extra + vec
+                + 2 * n * m * (2 if case["residual"] else 1), flops=product)
+
+
+# ---- the definition, in 64 bits -----------------------------------------------
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    d = {k: v.double() for k, v in st.items() if k != "case"}
+    op, form, act = case["op"], case["form"], case["act"]
+    if op == "norm":
+        s = d["x"]
+        if form != "backward" and case["residual"]:
+            s = s + d["residual"]
+        c = s.shape[1]
+        norm = torch.sqrt(torch.linalg.vector_norm(s, dim=1) ** 2 / c + EPS).unsqueeze(1)
+        if form == "backward":
+            # y_j = w_j s_j / norm, d norm / d s_i = s_i / (c norm)
+            g = d["dy"] * d["w"]
+            dx = g / norm - s * (g * s).sum(1, keepdim=True) / (c * norm ** 3)
+            if case["residual"]:
+                dx = dx + d["residual"]
+            return dx, torch.einsum("nc,nc->c", d["dy"], s / norm)
+        y = s / norm * d["w"]
+        out = (y,)
+        if form == "e4m3":
+            scale = torch.clamp(y.abs().max(dim=1).values / E4M3_MAX, min=TINY)
+            out = ((y / scale[:, None]).float().to(torch.float8_e4m3fn).double(), scale)
+        return out + ((s,) if case["residual"] else ())
+    z = torch.mm(d["x"], d["w"].t() if form == "e4m3" else d["w"])
+    if form == "e4m3":
+        z *= d["x_scale"].unsqueeze(1) * d["w_scale"].unsqueeze(0)
+    if case["bias"]:
+        z += d["bias"]
+    f = {"none": lambda t: t, "relu": torch.relu, "silu": torch.nn.functional.silu,
+         "gelu": torch.nn.functional.gelu}[act]
+
+    def value(t):
+        return f(t[:, :case["c_out"]]) * t[:, case["c_out"]:] if op == "gated" else f(t)
+
+    if form != "backward":
+        y = value(z)
+        return y + d["residual"] if case["residual"] else y
+    z.requires_grad_(True)
+    with torch.enable_grad():
+        (dz,) = torch.autograd.grad(value(z), z, d["dy"])
+    out = (torch.mm(dz, d["w"].t()), torch.mm(d["x"].t(), dz))
+    return out + ((dz.sum(0),) if case["bias"] else ())
