@@ -174,7 +174,8 @@ def _plain_norm(st, dt, form):
     s = x + st["residual"].float() if "residual" in st else x
     y = s * (1 / torch.sqrt((s * s).mean(1, keepdim=True) + EPS)) * w
     out = _quantise(y) if form == "e4m3" else (y.to(dt),)
-    return out + ((s.to(dt),) if "residual" in st else ())
+    out += (s.to(dt),) if "residual" in st else ()
+    return out if len(out) > 1 else out[0]
 
 
 def _plain_product(st, form):
@@ -286,7 +287,8 @@ def exact(case, seed):
         if form == "e4m3":
             scale = torch.clamp(y.abs().max(dim=1).values / E4M3_MAX, min=TINY)
             out = ((y / scale[:, None]).float().to(torch.float8_e4m3fn).double(), scale)
-        return out + ((s,) if case["residual"] else ())
+        out += (s,) if case["residual"] else ()
+        return out if len(out) > 1 else out[0]
     z = torch.mm(d["x"], d["w"].t() if form == "e4m3" else d["w"])
     if form == "e4m3":
         z *= d["x_scale"].unsqueeze(1) * d["w_scale"].unsqueeze(0)
