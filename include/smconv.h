@@ -471,6 +471,155 @@ const char* smc_last_error(void);
 /* Library version, major*10000 + minor*100 + patch. */
 int smc_version(void);
 
+/* ---------------------------------------------------------------------------
+ * Row operators: what a network does to each active voxel's feature row
+ * between two sparse convolutions. All tensors are row-major device memory;
+ * ld* is the distance between rows in elements (at least the row's length, at
+ * most 2^21), so a view of some channels or every other row is accepted as it
+ * is. 16-byte loads are used where a tensor's address and row distance are
+ * multiples of 16 bytes, element loads otherwise: same results, slower.
+ * Nothing is kept between calls and nothing is allocated: calls that need
+ * scratch memory take it from the caller, and calls on several streams with
+ * their own scratch do not touch each other. n = 0 is valid (gradients of
+ * weights are then zeros). Outputs may not overlap inputs, except y = residual
+ * (smc_linear) and s = x or residual, y = x (smc_rms_norm) with equal
+ * addresses and row distances.
+ *
+ * Sums, norms and pre-activations are float32; every output is rounded once
+ * (to nearest, ties to even) from float32. The backward passes keep nothing of
+ * the forward pass but its inputs: pre-activations are computed again, and
+ * the gradient dz that reaches them is rounded to `dtype` in the scratch
+ * memory, as it is the operand of two MFMA products. Sums have a fixed order:
+ * equal inputs give equal bits.
+ * ------------------------------------------------------------------------- */
+enum {
+    SMC_DTYPE_BF16 = 0,
+    SMC_DTYPE_F16 = 1,
+    SMC_DTYPE_E4M3 = 2        /* 8-bit floats (4 exponent, 3 mantissa bits, no infinity), with scales */
+};
+
+enum {
+    SMC_ACT_NONE = 0,
+    SMC_ACT_RELU = 1,         /* z < 0 ? 0 : z; slope 0 at z = 0 */
+    SMC_ACT_SILU = 2,         /* z / (1 + exp(-z)) */
+    SMC_ACT_GELU = 3          /* z (1 + erf(z / sqrt 2)) / 2 */
+};
+
+/*
+ * RMS norm of each row, with the residual stream's addition:
+ *   s = x + residual (or x);  y = s / sqrt(mean(s^2) + eps) * weight.
+ * The norm is taken of the float32 sum, before s is rounded. With y_scale the
+ * rows go out as e4m3: y_scale[i] = max(max_c |y[i, c]| / 448, 2^-126) and
+ * y[i, c] = e4m3(y[i, c] / y_scale[i]), what smc_linear and smc_gated read. A
+ * row with a NaN gets a NaN scale; a row of zeros stays zeros.
+ */
+typedef struct smc_norm_s {
+    int64_t n;                /* rows */
+    int32_t c;                /* channels, 1 .. 2^21 */
+    int32_t dtype;            /* of every tensor but e4m3 y: SMC_DTYPE_BF16 or _F16 */
+    float eps;                /* >= 0 */
+    const void* x;            /* [n, c] */
+    int64_t ldx;
+    const void* residual;     /* [n, c] or NULL */
+    int64_t ld_residual;
+    const void* weight;       /* [c] */
+    void* y;                  /* [n, c]: dtype, or e4m3 with y_scale */
+    int64_t ldy;
+    float* y_scale;           /* [n] or NULL */
+    void* s;                  /* [n, c] or NULL: the new residual stream */
+    int64_t lds;
+} smc_norm_t;
+int smc_rms_norm(const smc_norm_t* args, void* stream);
+
+/*
+ * Gradients of y = s / sqrt(mean(s^2) + eps) * weight with x_hat = s rstd:
+ *   dx = rstd (dy weight - x_hat mean(dy weight x_hat)) + ds
+ *   dweight = sum over rows of dy x_hat
+ * dx is the gradient of s, so of x and of the residual alike; ds (or NULL) is
+ * the gradient that reaches s by other paths. workspace: device memory of
+ * smc_rms_norm_backward_workspace(n, c) bytes, 16-byte aligned.
+ */
+typedef struct smc_norm_backward_s {
+    int64_t n;
+    int32_t c;
+    int32_t dtype;
+    float eps;
+    const void* dy;           /* [n, c] */
+    int64_t ld_dy;
+    const void* s;            /* [n, c]: the rows that were normalised */
+    int64_t lds;
+    const void* weight;       /* [c] */
+    const void* ds;           /* [n, c] or NULL */
+    int64_t ld_ds;
+    void* dx;                 /* [n, c] */
+    int64_t ld_dx;
+    void* dweight;            /* [c] */
+    void* workspace;
+    size_t workspace_bytes;
+} smc_norm_backward_t;
+int smc_rms_norm_backward(const smc_norm_backward_t* args, void* stream);
+size_t smc_rms_norm_backward_workspace(int64_t n, int c);
+
+/*
+ * smc_linear: y = act(x w + bias) + residual, x [n, c_in], w [c_in, c_out].
+ * smc_gated:  y = act(x wg + bias_g) * (x wu + bias_u), w = [wg | wu]
+ *             [c_in, 2 c_out] and bias [2 c_out] (gate half first); both
+ *             projections, the activation and the product in one kernel.
+ * x_dtype SMC_DTYPE_E4M3: x is e4m3 with one scale a row, w is e4m3 with one
+ * scale an output column, and x w is the product of the scaled values; with
+ * w_transposed, w is stored as [c_out (gated: 2 c_out), c_in]
+ * (smc_weight_quantize writes that). w's last element lies within 2^31 bytes
+ * of its first (else SMC_ERR_UNSUPPORTED).
+ *
+ * Backward: dy is the gradient of y; dx [n, c_in], dw [c_in, c_out or 2 c_out]
+ * and db (or NULL) those of x, w and bias. The residual's gradient is dy. 16-bit
+ * types only. workspace: smc_linear_backward_workspace(args) or
+ * smc_gated_backward_workspace(args) bytes (they read n, c_in, c_out,
+ * activation, db), 16-byte aligned.
+ */
+typedef struct smc_product_s {
+    int64_t n;                /* rows */
+    int32_t c_in, c_out;      /* 1 .. 2^21 */
+    int32_t dtype;            /* of y, bias, residual, the gradients: SMC_DTYPE_BF16 or _F16 */
+    int32_t x_dtype;          /* of x and w: dtype, or SMC_DTYPE_E4M3 */
+    int32_t activation;       /* SMC_ACT_* */
+    const void* x;
+    int64_t ldx;
+    const float* x_scale;     /* e4m3: [n] */
+    const void* w;
+    int64_t ldw;
+    int32_t w_transposed;     /* e4m3 only: 1 for w^T */
+    const float* w_scale;     /* e4m3: [c_out] ([2 c_out]) */
+    const void* bias;         /* or NULL */
+    const void* residual;     /* smc_linear: [n, c_out] or NULL; smc_gated and backward: NULL */
+    int64_t ld_residual;
+    void* y;                  /* forward: [n, c_out] */
+    int64_t ldy;
+    const void* dy;           /* backward from here on */
+    int64_t ld_dy;
+    void* dx;
+    int64_t ld_dx;
+    void* dw;
+    int64_t ld_dw;
+    void* db;
+    void* workspace;
+    size_t workspace_bytes;
+} smc_product_t;
+int smc_linear(const smc_product_t* args, void* stream);
+int smc_gated(const smc_product_t* args, void* stream);
+int smc_linear_backward(const smc_product_t* args, void* stream);
+int smc_gated_backward(const smc_product_t* args, void* stream);
+size_t smc_linear_backward_workspace(const smc_product_t* args);
+size_t smc_gated_backward_workspace(const smc_product_t* args);
+
+/*
+ * w [c_in, c_out] (dtype, rows ldw apart) -> q [c_out, c_in] e4m3 (rows ldq
+ * apart) and scale [c_out]: scale[j] = max(max_k |w[k, j]| / 448, 2^-126),
+ * q[j, k] = e4m3(w[k, j] / scale[j]). For a gated layer c_out is both halves.
+ */
+int smc_weight_quantize(const void* w, int64_t ldw, int c_in, int c_out, int dtype, void* q,
+                        int64_t ldq, float* scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

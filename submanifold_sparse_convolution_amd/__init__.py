@@ -17,7 +17,8 @@ import os
 
 __all__ = ["KernelMap", "PackedWeights", "pack_weights", "subm_conv3d", "lib", "library_path",
            "SmconvError", "ROUTES", "EXPORTED_SYMBOLS", "use_torch_allocator", "probe_mfma_bf16",
-           "probe_copy"]
+           "probe_copy", "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated",
+           "gated_backward", "quantize_weight", "ACTIVATIONS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsmconv.so")
@@ -41,7 +42,10 @@ EXPORTED_SYMBOLS = [
     "smc_map_set_order", "smc_map_calibrate", "smc_map_build_strided",
     "smc_map_export_out_coords", "smc_set_allocator", "smc_probe_mfma_out_bytes",
     "smc_probe_mfma_bf16", "smc_probe_copy", "smc_conv_forward_noalloc",
-    "smc_test_force_lookback_timeout", "smc_map_rows",
+    "smc_test_force_lookback_timeout", "smc_map_rows", "smc_rms_norm", "smc_rms_norm_backward",
+    "smc_rms_norm_backward_workspace", "smc_linear", "smc_gated", "smc_linear_backward",
+    "smc_gated_backward", "smc_linear_backward_workspace", "smc_gated_backward_workspace",
+    "smc_weight_quantize",
 ]
 STAGES = ["map", "neighbours", "mask_sort", "compact", "gemm", "centre"]
 
@@ -62,6 +66,42 @@ class MapInfo(ctypes.Structure):
         ("n_groups", ctypes.c_int32), ("group_rows", ctypes.c_int64 * 4),
         ("kernel_size", ctypes.c_int32), ("taps", ctypes.c_int32),
         ("n_in", ctypes.c_int64), ("strided", ctypes.c_int32), ("out_extent", ctypes.c_int32 * 3),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("c", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("y_scale", ctypes.c_void_p), ("s", ctypes.c_void_p), ("lds", ctypes.c_int64),
+    ]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("c", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+        ("s", ctypes.c_void_p), ("lds", ctypes.c_int64), ("weight", ctypes.c_void_p),
+        ("ds", ctypes.c_void_p), ("ld_ds", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("dweight", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ProductArgs(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("c_in", ctypes.c_int32), ("c_out", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("w_transposed", ctypes.c_int32),
+        ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+        ("ld_residual", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("ld_dw", ctypes.c_int64),
+        ("db", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -123,6 +163,18 @@ def lib():
                  "smc_set_allocator", "smc_probe_mfma_bf16", "smc_probe_copy",
                  "smc_conv_forward_noalloc", "smc_test_force_lookback_timeout", "smc_map_rows"):
         getattr(L, name).restype = i32
+    for name, args in (("smc_rms_norm", NormArgs), ("smc_rms_norm_backward", NormBackwardArgs),
+                       ("smc_linear", ProductArgs), ("smc_gated", ProductArgs),
+                       ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
+        getattr(L, name).restype = i32
+    for name in ("smc_linear_backward_workspace", "smc_gated_backward_workspace"):
+        getattr(L, name).argtypes = [ctypes.POINTER(ProductArgs)]
+        getattr(L, name).restype = ctypes.c_size_t
+    L.smc_rms_norm_backward_workspace.argtypes = [i64, i32]
+    L.smc_rms_norm_backward_workspace.restype = ctypes.c_size_t
+    L.smc_weight_quantize.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp]
+    L.smc_weight_quantize.restype = i32
     _lib = L
     return L
 
@@ -423,6 +475,259 @@ def subm_conv3d(coords, x, w, spatial_shape=None, relu: bool = False, route: str
     m = KernelMap().build(coords, spatial_shape=spatial_shape, route=route,
                           kernel_size=wp.kernel_size)
     return m.forward(x, wp, relu=relu)
+
+
+# ---- row operators ------------------------------------------------------------
+
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _dtype_code(t, name):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1}.get(t.dtype if isinstance(t, torch.Tensor) else t)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return code
+
+
+def _rows(t, name, dtype, device, shape=None):
+    """A 2-D CUDA tensor's (address, row distance in elements): the elements of
+    a row must be adjacent, rows may lie any distance apart without overlap."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {list(shape) if shape else '2-dimensional'}, "
+                         f"got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    n, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    ld = t.stride(0) if n > 1 else c
+    if ld < c:
+        raise ValueError(f"{name}: rows overlap (row distance {ld} < {c})")
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, dtype, device, size):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != size or (size > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous [{size}], got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+class _Launch:
+    """The device and stream of a call: outputs and scratch memory allocated
+    inside belong to the stream that runs the kernels."""
+
+    def __init__(self, x, stream):
+        import torch
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError("x must be a CUDA (HIP) torch tensor")
+        if x.dim() != 2:
+            raise ValueError(f"x must be 2-dimensional, got {list(x.shape)}")
+        self._ctx = []
+        index = x.device.index
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"stream is on {stream.device}, x on {x.device}")
+            self._ctx.append(torch.cuda.stream(stream))     # switches the device too
+            self.raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != index:
+                self._ctx.append(torch.cuda.device(index))
+            self.raw = torch.cuda.current_stream(index).cuda_stream
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, e4m3: bool = False, stream=None):
+    """s = x + residual (or x); y = s / sqrt(mean(s^2) + eps) * weight, per row.
+
+    x, residual: bf16 or f16 [N, C] CUDA tensors (rows may be strided), weight
+    [C]. Returns y; with a residual (y, s), s the new residual stream. e4m3:
+    (q, scale) in y's place, q float8_e4m3fn [N, C] and scale float32 [N] with
+    y = q * scale[:, None], as linear and gated take them."""
+    import torch
+    with _Launch(x, stream) as on:
+        dev, dt = x.device, x.dtype
+        code = _dtype_code(x, "x")
+        n, c = x.shape
+        xp, ldx = _rows(x, "x", dt, dev)
+        rp, ldr, s = None, 0, None
+        wp = _vector(weight, "weight", dt, dev, c)
+        if residual is not None:
+            rp, ldr = _rows(residual, "residual", dt, dev, (n, c))
+            s = torch.empty((n, c), dtype=dt, device=dev)
+        y = torch.empty((n, c), dtype=torch.float8_e4m3fn if e4m3 else dt, device=dev)
+        scale = torch.empty(n, dtype=torch.float32, device=dev) if e4m3 else None
+        _check(lib().smc_rms_norm(NormArgs(
+            n, c, code, eps, xp, ldx, rp, ldr, wp, y.data_ptr(), c,
+            scale.data_ptr() if e4m3 and n else None, s.data_ptr() if s is not None else None, c),
+            on.raw))
+    out = ((y, scale) if e4m3 else (y,)) + ((s,) if s is not None else ())
+    return out if len(out) > 1 else y
+
+
+def rms_norm_backward(dy, s, weight, eps: float = 1e-6, ds=None, stream=None):
+    """Gradients of rms_norm: (dx, dweight). s: the rows that were normalised
+    (rms_norm's s, or x without a residual); ds: the gradient that reaches s by
+    other paths, added to dx. dx is the gradient of x and of the residual."""
+    import torch
+    with _Launch(s, stream) as on:
+        dev, dt = s.device, s.dtype
+        code = _dtype_code(s, "s")
+        n, c = s.shape
+        sp, lds = _rows(s, "s", dt, dev)
+        dyp, lddy = _rows(dy, "dy", dt, dev, (n, c))
+        wp = _vector(weight, "weight", dt, dev, c)
+        dsp, ldds = _rows(ds, "ds", dt, dev, (n, c)) if ds is not None else (None, 0)
+        L = lib()
+        dx = torch.empty((n, c), dtype=dt, device=dev)
+        dweight = torch.empty(c, dtype=dt, device=dev)
+        ws = torch.empty(L.smc_rms_norm_backward_workspace(n, c), dtype=torch.uint8, device=dev)
+        _check(L.smc_rms_norm_backward(NormBackwardArgs(
+            n, c, code, eps, dyp, lddy, sp, lds, wp, dsp, ldds, dx.data_ptr(), c,
+            dweight.data_ptr(), ws.data_ptr(), ws.numel()), on.raw))
+    return dx, dweight
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {[a for a in ACTIVATIONS if a]} or None")
+    return ACTIVATIONS[name]
+
+
+def _product_args(halves, x, w, bias, activation, x_scale, w_scale, dtype, backward=False):
+    """(args with the shared fields, output dtype, c_out) of a linear or gated layer."""
+    import torch
+    act = _activation(activation)
+    dev = x.device
+    e4m3 = x.dtype == torch.float8_e4m3fn
+    dt = (torch.bfloat16 if dtype is None else dtype) if e4m3 else x.dtype
+    if not e4m3 and (dtype not in (None, dt) or x_scale is not None or w_scale is not None):
+        raise ValueError("dtype and scales are for e4m3 rows")
+    code = _dtype_code(dt, "dtype" if e4m3 else "x")
+    n, c_in = x.shape
+    xp, ldx = _rows(x, "x", x.dtype, dev)
+    along = e4m3 and (w.dim() != 2 or w.stride(1) == 1)     # else [c_in, c_out] in memory
+    wp, ldw = _rows(w.t() if e4m3 and not along else w, "w", x.dtype, dev)
+    if w.shape[1 if e4m3 else 0] != c_in:
+        raise ValueError(f"w is {list(w.shape)}, x has {c_in} channels "
+                         f"(e4m3 weights are [c_out, c_in])")
+    wide = w.shape[0 if e4m3 else 1]
+    if wide % halves or wide == 0:
+        raise ValueError(f"a gated layer's w holds two halves, got {wide} columns")
+    xsp = wsp = None
+    if e4m3 and not backward:          # the library refuses gradients of e4m3 layers
+        xsp = _vector(x_scale, "x_scale", torch.float32, dev, n) if n else None
+        wsp = _vector(w_scale, "w_scale", torch.float32, dev, wide)
+    bp = _vector(bias, "bias", dt, dev, wide) if bias is not None else None
+    return ProductArgs(n, c_in, wide // halves, code, 2 if e4m3 else code, act, xp, ldx, xsp, wp, ldw,
+                       along, wsp, bp), dt, wide // halves
+
+
+def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scale=None, dtype=None,
+           out=None, stream=None):
+    """y = activation(x @ w + bias) + residual in one kernel.
+
+    x: bf16 or f16 [N, C_in] CUDA tensor, w: [C_in, C_out] (rows of both may be
+    strided), bias [C_out], residual [N, C_out]; activation None, "relu",
+    "silu" or "gelu" (erf). Served in 8 bits: x float8_e4m3fn with x_scale [N]
+    (rms_norm's e4m3 output), w float8_e4m3fn [C_out, C_in] with w_scale [C_out]
+    (quantize_weight; its transpose's memory order is taken too), y of `dtype`
+    (default bf16). out may be the residual."""
+    import torch
+    with _Launch(x, stream) as on:
+        a, dt, c_out = _product_args(1, x, w, bias, activation, x_scale, w_scale, dtype)
+        shape = (x.shape[0], c_out)
+        if residual is not None:
+            a.residual, a.ld_residual = _rows(residual, "residual", dt, x.device, shape)
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=x.device)
+        a.y, a.ldy = _rows(out, "out", dt, x.device, shape)
+        _check(lib().smc_linear(a, on.raw))
+    return out
+
+
+def gated(x, w, bias=None, activation="silu", x_scale=None, w_scale=None, dtype=None, out=None,
+          stream=None):
+    """h = activation(x @ wg + bias_g) * (x @ wu + bias_u) in one kernel, with
+    w = [wg | wu] [C_in, 2 C_out] and bias [2 C_out]. Types and the 8-bit form
+    as in linear (e4m3 w: [2 C_out, C_in], the gate's rows first)."""
+    import torch
+    with _Launch(x, stream) as on:
+        a, dt, c_out = _product_args(2, x, w, bias, activation, x_scale, w_scale, dtype)
+        shape = (x.shape[0], c_out)
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=x.device)
+        a.y, a.ldy = _rows(out, "out", dt, x.device, shape)
+        _check(lib().smc_gated(a, on.raw))
+    return out
+
+
+def _product_backward(halves, dy, x, w, bias, activation, stream):
+    import torch
+    with _Launch(x, stream) as on:
+        a, dt, c_out = _product_args(halves, x, w, bias, activation, None, None, None, True)
+        n, c_in = x.shape
+        a.dy, a.ld_dy = _rows(dy, "dy", dt, x.device, (n, c_out))
+        dx = torch.empty((n, c_in), dtype=dt, device=x.device)
+        dw = torch.empty((c_in, c_out * halves), dtype=dt, device=x.device)
+        db = torch.empty(c_out * halves, dtype=dt, device=x.device) if bias is not None else None
+        a.dx, a.ld_dx, a.dw, a.ld_dw = dx.data_ptr(), c_in, dw.data_ptr(), c_out * halves
+        a.db = db.data_ptr() if db is not None else None
+        L = lib()
+        need, call = ((L.smc_linear_backward_workspace, L.smc_linear_backward) if halves == 1 else
+                      (L.smc_gated_backward_workspace, L.smc_gated_backward))
+        ws = torch.empty(need(a), dtype=torch.uint8, device=x.device)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        _check(call(a, on.raw))
+    return dx, dw, db
+
+
+def linear_backward(dy, x, w, bias=None, activation=None, stream=None):
+    """(dx, dw, db) of linear for the gradient dy of its output (db None without
+    a bias); the residual's gradient is dy itself. The pre-activations are
+    computed again from x, w and bias: nothing of the forward pass is kept."""
+    return _product_backward(1, dy, x, w, bias, activation, stream)
+
+
+def gated_backward(dh, x, w, bias=None, activation="silu", stream=None):
+    """(dx, dw, db) of gated for the gradient dh of its output (db None without
+    a bias), from x, w and bias alone."""
+    return _product_backward(2, dh, x, w, bias, activation, stream)
+
+
+def quantize_weight(w, stream=None):
+    """bf16 or f16 w [C_in, C_out] -> (float8_e4m3fn [C_out, C_in], float32 scale
+    [C_out]) for linear and gated on e4m3 rows; scale[j] = max |w[:, j]| / 448."""
+    import torch
+    with _Launch(w, stream) as on:
+        code = _dtype_code(w, "w")
+        c_in, c_out = w.shape
+        wp, ldw = _rows(w, "w", w.dtype, w.device)
+        q = torch.empty((c_out, c_in), dtype=torch.float8_e4m3fn, device=w.device)
+        scale = torch.empty(c_out, dtype=torch.float32, device=w.device)
+        _check(lib().smc_weight_quantize(wp, ldw, c_in, c_out, code, q.data_ptr(), c_in,
+                                         scale.data_ptr(), on.raw))
+    return q, scale
 
 
 def probe_mfma_bf16(iters: int, stream=None) -> float:

@@ -1,0 +1,485 @@
+// RMS norm with the residual's addition, and its gradients; e4m3 weights.
+//
+//   s = x + r            (float32, rounded once into the new residual stream)
+//   y = s rstd w,        rstd = 1 / sqrt(mean(s^2) + eps), from the float32 s
+//   e4m3: y_scale = max(amax |y| / 448, 2^-126), q = e4m3(y / y_scale)
+//
+//   x_hat = s rstd, a = dy w
+//   dx = rstd (a - x_hat mean(a x_hat)) + ds,   dw = sum over rows of dy x_hat
+//
+// Bound by memory: every row is read once and kept in registers between its
+// sums and its outputs.
+#include <algorithm>
+
+#include "pointwise_gemm.h"
+
+namespace smc {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr float kE4m3Max = 448.f;
+constexpr float kTinyScale = 1.17549435e-38f;      // 2^-126
+
+// W consecutive elements (8: one 16-byte word) as float32.
+template <int DT, int W>
+__device__ __forceinline__ void load_f32(const void* p, int64_t i, float (&v)[W]) {
+    if constexpr (W == 8) {
+        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = to_f32<DT>((u[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+    } else {
+        v[0] = to_f32<DT>(static_cast<const uint16_t*>(p)[i]);
+    }
+}
+
+template <int DT, int W>
+__device__ __forceinline__ void store_16(void* p, int64_t i, const float (&v)[W]) {
+    if constexpr (W == 8)
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
+            (u32x4){pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                    pack2<DT>(v[6], v[7])};
+    else
+        static_cast<uint16_t*>(p)[i] = (uint16_t)from_f32<DT>(v[0]);
+}
+
+template <int W>
+__device__ __forceinline__ void store_e4m3(void* p, int64_t i, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        u32x2 u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
+            u[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w, true);
+        }
+        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(p) + i) = u;
+    } else {
+        static_cast<uint8_t*>(p)[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false);
+    }
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// Largest magnitude by its bits, in which order NaN is above infinity: a NaN
+// anywhere in the row makes the scale NaN.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
+}
+
+__device__ __forceinline__ float row_scale(uint32_t amax_bits) {
+    const float s = __uint_as_float(amax_bits) / kE4m3Max;
+    return s < kTinyScale ? kTinyScale : s;        // NaN stays
+}
+
+// L lanes a row, NV words of W elements a lane, the row in registers.
+template <int DT, int W, int L, int NV>
+__global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
+    const int lane = threadIdx.x % L;
+    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+    const bool ok = row < a.n;
+    float v[NV][W];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + lane) * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[j][e] = 0.f;
+        if (ok && c < a.c) {
+            load_f32<DT, W>(a.x, row * a.ldx + c, v[j]);
+            if (a.residual) {
+                float r[W];
+                load_f32<DT, W>(a.residual, row * a.ldr + c, r);
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[j][e] += r[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) ss += v[j][e] * v[j][e];
+    }
+    if (a.s) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * L + lane) * W;
+            if (ok && c < a.c) store_16<DT, W>(a.s, row * a.lds + c, v[j]);
+        }
+    }
+    const float rstd = 1.f / sqrtf(group_sum<L>(ss) / (float)a.c + a.eps);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + lane) * W;
+        if (c >= a.c) continue;
+        float w[W];
+        load_f32<DT, W>(a.weight, c, w);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            v[j][e] = v[j][e] * rstd * w[e];
+            amax = max(amax, __float_as_uint(v[j][e]) & 0x7fffffffu);
+        }
+        if (!a.y_scale && ok) store_16<DT, W>(a.y, row * a.ldy + c, v[j]);
+    }
+    if (!a.y_scale) return;
+    const float scale = row_scale(group_max<L>(amax));
+    if (ok && lane == 0) a.y_scale[row] = scale;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + lane) * W;
+        if (!ok || c >= a.c) continue;
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[j][e] = v[j][e] / scale;
+        store_e4m3<W>(a.y, row * a.ldy + c, v[j]);
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* s) {
+    v = group_sum<64>(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return s[0] + s[1] + s[2] + s[3];
+}
+
+// Rows too wide for a wave's registers: a block a row, the row read again (from
+// the caches) for each use.
+template <int DT, int W>
+__global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
+    __shared__ float s_sum[4];
+    __shared__ uint32_t s_max[4];
+    const int64_t row = blockIdx.x;
+    auto value = [&](int c, float (&v)[W]) {
+        load_f32<DT, W>(a.x, row * a.ldx + c, v);
+        if (a.residual) {
+            float r[W];
+            load_f32<DT, W>(a.residual, row * a.ldr + c, r);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] += r[e];
+        }
+    };
+    float ss = 0.f;
+    for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
+        float v[W];
+        value(c, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) ss += v[e] * v[e];
+    }
+    const float rstd = 1.f / sqrtf(block_sum(ss, s_sum) / (float)a.c + a.eps);
+    uint32_t amax = 0;
+    for (int pass = a.y_scale ? 0 : 1; pass < 2; ++pass) {
+        float scale = 1.f;
+        if (pass == 1 && a.y_scale) {
+            amax = group_max<64>(amax);
+            if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = amax;
+            __syncthreads();
+            scale = row_scale(max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3])));
+            if (threadIdx.x == 0) a.y_scale[row] = scale;
+        }
+        for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
+            float v[W], w[W];
+            value(c, v);
+            load_f32<DT, W>(a.weight, c, w);
+            if (pass == 1 && a.s) store_16<DT, W>(a.s, row * a.lds + c, v);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                v[e] = v[e] * rstd * w[e];
+                amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
+                if (a.y_scale) v[e] = v[e] / scale;
+            }
+            if (pass == 0) continue;
+            if (a.y_scale)
+                store_e4m3<W>(a.y, row * a.ldy + c, v);
+            else
+                store_16<DT, W>(a.y, row * a.ldy + c, v);
+        }
+    }
+}
+
+// dx of the rows blockIdx, + gridDim, ... and this block's sums of dy x_hat.
+template <int DT, int W, int L, int NV>
+__global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
+    constexpr int kRows = kNormThreads / L;
+    __shared__ float s_dw[L * NV * W];
+    const int lane = threadIdx.x % L;
+    float w[NV][W], dw[NV][W];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + lane) * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[j][e] = dw[j][e] = 0.f;
+        if (c < a.c) load_f32<DT, W>(a.weight, c, w[j]);
+    }
+    const int64_t first = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    // every lane of a wave walks the same number of rows: the sums below are
+    // exchanged across its lanes
+    const int64_t rounds = (a.n - (int64_t)blockIdx.x * kRows + (int64_t)gridDim.x * kRows - 1) /
+                           ((int64_t)gridDim.x * kRows);
+    for (int64_t it = 0; it < rounds; ++it) {
+        const int64_t row = first + it * gridDim.x * kRows;
+        const bool ok = row < a.n;
+        float x[NV][W], dy[NV][W];
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * L + lane) * W;
+#pragma unroll
+            for (int e = 0; e < W; ++e) x[j][e] = dy[j][e] = 0.f;
+            if (ok && c < a.c) {
+                load_f32<DT, W>(a.x, row * a.ldx + c, x[j]);
+                load_f32<DT, W>(a.dy, row * a.lddy + c, dy[j]);
+            }
+        }
+        float ds[NV][W];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * L + lane) * W;
+#pragma unroll
+            for (int e = 0; e < W; ++e) ds[j][e] = 0.f;
+            if (a.residual && ok && c < a.c) load_f32<DT, W>(a.residual, row * a.ldr + c, ds[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                ss += x[j][e] * x[j][e];
+                dot += dy[j][e] * w[j][e] * x[j][e];
+            }
+        ss = group_sum<L>(ss);
+        dot = group_sum<L>(dot);
+        const float rstd = 1.f / sqrtf(ss / (float)a.c + a.eps);
+        const float mean = dot * rstd / (float)a.c;        // mean(a x_hat)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * L + lane) * W;
+            float o[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float xh = x[j][e] * rstd;
+                o[e] = rstd * (dy[j][e] * w[j][e] - xh * mean) + ds[j][e];
+                if (ok) dw[j][e] += dy[j][e] * xh;
+            }
+            if (ok && c < a.c) store_16<DT, W>(a.y, row * a.ldy + c, o);
+        }
+    }
+    // the lane groups of a wave, then the waves in turn
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+#pragma unroll
+            for (int o = L; o < 64; o <<= 1) dw[j][e] += __shfl_xor(dw[j][e], o);
+    for (int wv = 0; wv < kNormThreads / 64; ++wv) {
+        if ((int)(threadIdx.x >> 6) == wv && (threadIdx.x & 63) < L) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    float* d = s_dw + (j * L + lane) * W + e;
+                    *d = wv == 0 ? dw[j][e] : *d + dw[j][e];
+                }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.c; c += kNormThreads) a.part[(int64_t)blockIdx.x * a.c + c] = s_dw[c];
+}
+
+template <int DT, int W>
+__global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a) {
+    __shared__ float s_sum[4];
+    float* part = a.part + (int64_t)blockIdx.x * a.c;      // each thread its own columns
+    for (int c = threadIdx.x; c < a.c; c += kNormThreads) part[c] = 0.f;
+    __syncthreads();
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        float ss = 0.f, dot = 0.f;
+        for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
+            float x[W], dy[W], w[W];
+            load_f32<DT, W>(a.x, row * a.ldx + c, x);
+            load_f32<DT, W>(a.dy, row * a.lddy + c, dy);
+            load_f32<DT, W>(a.weight, c, w);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                ss += x[e] * x[e];
+                dot += dy[e] * w[e] * x[e];
+            }
+        }
+        const float rstd = 1.f / sqrtf(block_sum(ss, s_sum) / (float)a.c + a.eps);
+        const float mean = block_sum(dot, s_sum) * rstd / (float)a.c;
+        for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
+            float x[W], dy[W], w[W], o[W], ds[W];
+            load_f32<DT, W>(a.x, row * a.ldx + c, x);
+            load_f32<DT, W>(a.dy, row * a.lddy + c, dy);
+            load_f32<DT, W>(a.weight, c, w);
+#pragma unroll
+            for (int e = 0; e < W; ++e) ds[e] = 0.f;
+            if (a.residual) load_f32<DT, W>(a.residual, row * a.ldr + c, ds);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float xh = x[e] * rstd;
+                o[e] = rstd * (dy[e] * w[e] - xh * mean) + ds[e];
+                part[c + e] += dy[e] * xh;
+            }
+            store_16<DT, W>(a.y, row * a.ldy + c, o);
+        }
+    }
+}
+
+// dw[c] = the blocks' sums in order: 32 columns a block, 32 runs of blocks,
+// the runs added by a tree.
+template <int DT>
+__global__ __launch_bounds__(1024) void k_norm_weight_sum(const float* __restrict__ part, int blocks,
+                                                          int c, uint16_t* dw) {
+    __shared__ float s[32][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    float v = 0.f;
+    if (col < c)
+        for (int b = g; b < blocks; b += 32) v += part[(int64_t)b * c + col];
+    s[g][threadIdx.x & 31] = v;
+    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) {
+        if (g < o) s[g][threadIdx.x & 31] += s[g + o][threadIdx.x & 31];
+        __syncthreads();
+    }
+    if (g == 0 && col < c) dw[col] = (uint16_t)from_f32<DT>(s[0][threadIdx.x]);
+}
+
+// W [c_in, c_out] -> q [c_out, c_in] e4m3, one scale a column of W. 32 columns
+// a block; W is read twice (once per weight and program, not a hot path).
+template <int DT>
+__global__ __launch_bounds__(256) void k_quantize_weight(const uint16_t* __restrict__ w, int64_t ldw,
+                                                         int c_in, int c_out, uint8_t* q,
+                                                         int64_t ldq, float* scale) {
+    __shared__ uint32_t s_max[8][32];
+    __shared__ float s_scale[32];
+    __shared__ float s_t[32][33];
+    const int x = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + x;
+    uint32_t amax = 0;
+    if (col < c_out)
+        for (int k = g; k < c_in; k += 8)
+            amax = max(amax, __float_as_uint(to_f32<DT>(w[k * ldw + col])) & 0x7fffffffu);
+    s_max[g][x] = amax;
+    __syncthreads();
+    if (g == 0) {
+        for (int i = 1; i < 8; ++i) amax = max(amax, s_max[i][x]);
+        s_scale[x] = row_scale(amax);
+        if (col < c_out) scale[col] = s_scale[x];
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < c_in; k0 += 32) {
+        for (int i = g; i < 32; i += 8)
+            s_t[i][x] = col < c_out && k0 + i < c_in ? to_f32<DT>(w[(k0 + i) * ldw + col]) / s_scale[x] : 0.f;
+        __syncthreads();
+        for (int i = g; i < 32; i += 8) {
+            const int oc = blockIdx.x * 32 + i;
+            if (oc < c_out && k0 + x < c_in)
+                q[oc * ldq + k0 + x] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(s_t[x][i], 0.f, 0, false);
+        }
+        __syncthreads();
+    }
+}
+
+// Lanes and words a row for c channels: the fewest lanes that hold the row in
+// one word each, up to a wave; wider rows take more words a lane, up to 8
+// words of 8 (4096 channels) or 16 single elements (1024).
+template <template <int, int, int, int> class K, int DT>
+bool by_shape(int c, int vec, const NormArgs& a, hipStream_t s) {
+    if (vec) {
+        const int words = (c + 7) / 8;
+        if (words <= 1) K<DT, 8, 1, 1>::go(a, s);
+        else if (words <= 2) K<DT, 8, 2, 1>::go(a, s);
+        else if (words <= 4) K<DT, 8, 4, 1>::go(a, s);
+        else if (words <= 8) K<DT, 8, 8, 1>::go(a, s);
+        else if (words <= 16) K<DT, 8, 16, 1>::go(a, s);
+        else if (words <= 32) K<DT, 8, 32, 1>::go(a, s);
+        else if (words <= 64) K<DT, 8, 64, 1>::go(a, s);
+        else if (words <= 128) K<DT, 8, 64, 2>::go(a, s);
+        else if (words <= 256) K<DT, 8, 64, 4>::go(a, s);
+        else if (words <= 512) K<DT, 8, 64, 8>::go(a, s);
+        else return false;
+        return true;
+    }
+    if (c <= 16) K<DT, 1, 16, 1>::go(a, s);
+    else if (c <= 64) K<DT, 1, 64, 1>::go(a, s);
+    else if (c <= 256) K<DT, 1, 64, 4>::go(a, s);
+    else if (c <= 1024) K<DT, 1, 64, 16>::go(a, s);
+    else return false;
+    return true;
+}
+
+template <int DT, int W, int L, int NV>
+struct Forward {
+    static void go(const NormArgs& a, hipStream_t s) {
+        constexpr int kRows = kNormThreads / L;
+        launch(k_norm<DT, W, L, NV>, dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kNormThreads), 0, s, a);
+    }
+};
+
+template <int DT, int W, int L, int NV>
+struct Backward {
+    static void go(const NormArgs& a, hipStream_t s) {
+        launch(k_norm_backward<DT, W, L, NV>, dim3((unsigned)norm_backward_blocks(a.n, a.c)),
+               dim3(kNormThreads), 0, s, a);
+    }
+};
+
+template <int DT>
+hipError_t norm_t(const NormArgs& a, hipStream_t s) {
+    if (!by_shape<Forward, DT>(a.c, a.vec, a, s)) {
+        if (a.vec)
+            launch(k_norm_wide<DT, 8>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+        else
+            launch(k_norm_wide<DT, 1>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
+    const int blocks = norm_backward_blocks(a.n, a.c);
+    if (blocks > 0 && !by_shape<Backward, DT>(a.c, a.vec, a, s)) {
+        if (a.vec)
+            launch(k_norm_backward_wide<DT, 8>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
+        else
+            launch(k_norm_backward_wide<DT, 1>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
+    }
+    launch(k_norm_weight_sum<DT>, dim3((unsigned)((a.c + 31) / 32)), dim3(1024), 0, s, a.part, blocks,
+           a.c, static_cast<uint16_t*>(a.dweight));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Blocks of the backward pass: each writes c sums, so no more than fill the
+// device (8 blocks a CU), and no more than there are rows.
+int norm_backward_blocks(int64_t n, int c) {
+    (void)c;
+    return (int)std::min<int64_t>(n, (int64_t)8 * device_cus());
+}
+
+hipError_t launch_norm(const NormArgs& a, int dt, hipStream_t s) {
+    if (a.n == 0) return hipSuccess;
+    return dt == kF16 ? norm_t<kF16>(a, s) : norm_t<kBF16>(a, s);
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, int dt, hipStream_t s) {
+    return dt == kF16 ? norm_backward_t<kF16>(a, s) : norm_backward_t<kBF16>(a, s);
+}
+
+hipError_t launch_quantize_weight(const void* w, int64_t ldw, int c_in, int c_out, void* q,
+                                  int64_t ldq, float* scale, int dt, hipStream_t s) {
+    const dim3 grid((unsigned)((c_out + 31) / 32));
+    if (dt == kF16)
+        launch(k_quantize_weight<kF16>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(w), ldw,
+               c_in, c_out, static_cast<uint8_t*>(q), ldq, scale);
+    else
+        launch(k_quantize_weight<kBF16>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(w), ldw,
+               c_in, c_out, static_cast<uint8_t*>(q), ldq, scale);
+    return hipGetLastError();
+}
+
+}  // namespace smc

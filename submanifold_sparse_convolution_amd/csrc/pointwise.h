@@ -1,0 +1,100 @@
+// Internal declarations of the row operators (RMS norm, linear and gated
+// layers): the operands their kernels take and the host functions that launch
+// them. The C entries are in pointwise_api.hip.
+#pragma once
+
+#include "smc_internal.h"
+
+namespace smc {
+
+// Element types (the C interface's SMC_DTYPE_* values).
+enum Dtype : int { kBF16 = 0, kF16 = 1, kE4M3 = 2 };
+enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+// What a product kernel does with its float32 accumulators.
+enum Epilogue : int {
+    kEpiStore = 0,      // y = act(z + bias) + residual
+    kEpiGated = 1,      // h = act(z_gate + bias) * (z_up + bias)
+    kEpiSlope = 2,      // dz = dy act'(z + bias)
+    kEpiGatedSlope = 3, // dz_gate = dh u act'(g), dz_up = dh act(g)
+    kEpiPartial = 4,    // the float32 sums of one range of the contraction
+};
+
+// How an operand lies in memory, seen from the product: its contraction index
+// is the contiguous one (kAlongK: rows of x, or W^T), or the other one is
+// (kAcrossK: W itself as [k, n], or both operands of x^T dz).
+enum Layout : int { kAlongK = 0, kAcrossK = 1 };
+
+// out[m, n] = sum over k of a(m, k) b(n, k), then the epilogue.
+struct ProductArgs {
+    const void* a = nullptr;    // rows of the output
+    const void* b = nullptr;    // columns of the output
+    int64_t lda = 0, ldb = 0;   // elements from one memory row to the next
+    int64_t m = 0, k = 0;
+    int n = 0;                  // columns of b (gated: both halves)
+    int half = 0;               // gated: columns of one half
+    const void* bias = nullptr; // [n]
+    const float* a_scale = nullptr;   // e4m3: one a row of a, of b
+    const float* b_scale = nullptr;
+    const void* extra = nullptr;      // residual, dy or dh: [m, n] ([m, half] gated)
+    int64_t ld_extra = 0;
+    void* out = nullptr;        // [m, n] ([m, half] for kEpiGated)
+    int64_t ldo = 0;
+    float* part = nullptr;      // kEpiPartial: [splits][m + colsum][n]
+    int64_t k_split = 0;        // contraction length of a split (all of k: one split)
+    int splits = 1;
+    int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
+    int act = 0;
+    int vec_a = 0, vec_b = 0;   // 16-byte loads are possible
+    int vec_o = 0;              // 16-byte stores (and loads of extra) are possible
+    // the tile walk
+    int tiles_m = 0, tiles_n = 0;
+    int xcds = 8;
+};
+
+// Tile shapes of the product kernel.
+enum TileShape : int { kTileLarge = 0, kTileMid = 1, kTileSmall = 2 };
+
+// Compute units of the current device (looked up once per device).
+int device_cus();
+
+// out = product (see ProductArgs); dt: type of out, bias and extra, and of a
+// and b unless e4m3 (whose b lies along k or across it). Fills in the tile walk.
+hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w_along, hipStream_t s);
+// dx = dz W^T: both operands along k.
+hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s);
+// dW = x^T dz (both operands across k) and, with colsum, db: float32 sums of
+// `splits` ranges of the rows, added and rounded by launch_sum_parts.
+int weight_gradient_splits(int64_t rows, int c_in, int n);
+hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s);
+hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
+                            void* db, int dt, hipStream_t s);
+
+// ---- norm (norm_kernels.hip) ----
+struct NormArgs {
+    int64_t n = 0;
+    int c = 0;
+    float eps = 0.f;
+    const void* x = nullptr;        // backward: s, the rows that were normalised
+    int64_t ldx = 0;
+    const void* residual = nullptr; // backward: the gradient that reaches s by other paths
+    int64_t ldr = 0;
+    const void* weight = nullptr;
+    void* y = nullptr;              // backward: dx
+    int64_t ldy = 0;
+    void* s = nullptr;
+    int64_t lds = 0;
+    float* y_scale = nullptr;       // e4m3 output
+    const void* dy = nullptr;
+    int64_t lddy = 0;
+    void* dweight = nullptr;
+    float* part = nullptr;          // backward: [blocks][c] sums of dy x_hat
+    int vec = 0;                    // 16-byte loads and stores are possible
+};
+hipError_t launch_norm(const NormArgs& a, int dt, hipStream_t s);
+int norm_backward_blocks(int64_t n, int c);
+hipError_t launch_norm_backward(const NormArgs& a, int dt, hipStream_t s);
+hipError_t launch_quantize_weight(const void* w, int64_t ldw, int c_in, int c_out, void* q,
+                                  int64_t ldq, float* scale, int dt, hipStream_t s);
+
+}  // namespace smc

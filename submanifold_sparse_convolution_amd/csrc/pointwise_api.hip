@@ -1,0 +1,326 @@
+// C entries of the row operators: argument checks, scratch layout and launches.
+// See include/smconv.h for the contract of each call.
+#include <cstdarg>
+#include <cstdio>
+
+#include "smconv.h"
+#include "pointwise.h"
+
+using namespace smc;
+
+namespace {
+
+constexpr int64_t kMaxDim = 1 << 21;           // channels and row distances: tile offsets fit 31 bits
+constexpr int64_t kMaxRows = (int64_t)1 << 36;
+constexpr size_t kAlign = 256;
+
+int bad(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int bad(int status, const char* fmt, ...) {
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return set_error(status, buf);
+}
+
+int hip_status(hipError_t e, const char* what) {
+    if (e == hipSuccess) return SMC_OK;
+    return bad(SMC_ERR_HIP, "%s failed: %s", what, hipGetErrorString(e));
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool words16(const void* p, int64_t ld) { return aligned16(p) && (ld & 7) == 0; }   // 16-bit rows
+size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// A [rows, cols] tensor: present where it has elements, row distance in range.
+int check_rows(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    if (!p && rows > 0) return bad(SMC_ERR_ARG, "%s is NULL", name);
+    if (ld < cols || ld > kMaxDim)
+        return bad(SMC_ERR_ARG, "row distance of %s is %lld, outside [%lld, 2^21]", name, (long long)ld,
+                   (long long)cols);
+    if (((uintptr_t)p & 1) != 0) return bad(SMC_ERR_ARG, "%s is not aligned to its elements", name);
+    return SMC_OK;
+}
+
+int check_common(int64_t n, int64_t c, const char* cname, int dtype) {
+    if (n < 0 || n > kMaxRows) return bad(SMC_ERR_ARG, "n = %lld", (long long)n);
+    if (c < 1 || c > kMaxDim) return bad(SMC_ERR_ARG, "%s = %lld outside [1, 2^21]", cname, (long long)c);
+    if (dtype != SMC_DTYPE_BF16 && dtype != SMC_DTYPE_F16)
+        return bad(SMC_ERR_ARG, "dtype %d (SMC_DTYPE_BF16 or SMC_DTYPE_F16)", dtype);
+    return SMC_OK;
+}
+
+#define CHECK(call)              \
+    do {                         \
+        const int rc_ = (call);  \
+        if (rc_) return rc_;     \
+    } while (0)
+
+// Checks of smc_linear, smc_gated (halves = 2) and their backward passes.
+int check_product(const smc_product_t* a, int halves, bool backward) {
+    if (!a) return bad(SMC_ERR_ARG, "args is NULL");
+    CHECK(check_common(a->n, a->c_in, "c_in", a->dtype));
+    if (a->c_out < 1 || a->c_out > kMaxDim / halves)
+        return bad(SMC_ERR_ARG, "c_out = %d outside [1, 2^21%s]", a->c_out, halves == 2 ? " / 2" : "");
+    const int64_t wide = (int64_t)a->c_out * halves;
+    const bool e4m3 = a->x_dtype == SMC_DTYPE_E4M3;
+    if (!e4m3 && a->x_dtype != a->dtype)
+        return bad(SMC_ERR_ARG, "x_dtype %d with dtype %d", a->x_dtype, a->dtype);
+    if (e4m3 && backward) return bad(SMC_ERR_UNSUPPORTED, "gradients of e4m3 layers");
+    if (a->activation < SMC_ACT_NONE || a->activation > SMC_ACT_GELU)
+        return bad(SMC_ERR_ARG, "activation %d", a->activation);
+    // the weights are addressed by 31-bit byte offsets from their first element
+    if (a->w_transposed && !e4m3) return bad(SMC_ERR_UNSUPPORTED, "w_transposed is for e4m3 weights");
+    const int64_t w_rows = a->w_transposed ? wide : a->c_in, w_cols = a->w_transposed ? a->c_in : wide;
+    if (!a->w) return bad(SMC_ERR_ARG, "w is NULL");
+    if (a->ldw < w_cols || a->ldw > kMaxDim)
+        return bad(SMC_ERR_ARG, "row distance of w is %lld, outside [%lld, 2^21]", (long long)a->ldw,
+                   (long long)w_cols);
+    if (w_rows * a->ldw * (e4m3 ? 1 : 2) >= ((int64_t)1 << 31))
+        return bad(SMC_ERR_UNSUPPORTED, "w spans 2^31 bytes or more");
+    if (e4m3) {
+        if (!a->w_scale || (!a->x_scale && a->n > 0)) return bad(SMC_ERR_ARG, "e4m3 operands need scales");
+        if (!a->x && a->n > 0) return bad(SMC_ERR_ARG, "x is NULL");
+        if (a->ldx < a->c_in || a->ldx > kMaxDim)
+            return bad(SMC_ERR_ARG, "row distance of x is %lld", (long long)a->ldx);
+    } else {
+        CHECK(check_rows("x", a->x, a->n, a->c_in, a->ldx));
+        if (((uintptr_t)a->w & 1) != 0) return bad(SMC_ERR_ARG, "w is not aligned to its elements");
+    }
+    if (((uintptr_t)a->bias & 1) != 0) return bad(SMC_ERR_ARG, "bias is not aligned to its elements");
+    if (a->residual && (halves == 2 || backward))
+        return bad(SMC_ERR_ARG, "residual is an argument of smc_linear only");
+    if (!backward) {
+        if (a->residual) CHECK(check_rows("residual", a->residual, a->n, a->c_out, a->ld_residual));
+        return check_rows("y", a->y, a->n, a->c_out, a->ldy);
+    }
+    CHECK(check_rows("dy", a->dy, a->n, a->c_out, a->ld_dy));
+    CHECK(check_rows("dx", a->dx, a->n, a->c_in, a->ld_dx));
+    if (!a->dw) return bad(SMC_ERR_ARG, "dw is NULL");
+    CHECK(check_rows("dw", a->dw, a->c_in, wide, a->ld_dw));
+    if (((uintptr_t)a->db & 1) != 0) return bad(SMC_ERR_ARG, "db is not aligned to its elements");
+    return SMC_OK;
+}
+
+ProductArgs forward_args(const smc_product_t* a, int halves) {
+    ProductArgs p;
+    const int es = a->x_dtype == SMC_DTYPE_E4M3 ? 1 : 2;
+    p.a = a->x;
+    p.lda = a->ldx;
+    p.b = a->w;
+    p.ldb = a->ldw;
+    p.m = a->n;
+    p.k = a->c_in;
+    p.n = a->c_out * halves;
+    p.half = a->c_out;
+    p.bias = a->bias;
+    p.a_scale = a->x_scale;
+    p.b_scale = a->w_scale;
+    p.act = a->activation;
+    // a row of x, and of w^T, is whole 16-byte words; of w, each half starts at one
+    const int per = 16 / es;
+    p.vec_a = aligned16(a->x) && a->ldx % per == 0 && a->c_in % per == 0;
+    p.vec_b = aligned16(a->w) && a->ldw % per == 0 &&
+              (a->w_transposed ? a->c_in % per == 0 : halves == 1 || a->c_out % per == 0);
+    return p;
+}
+
+int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
+    CHECK(check_product(a, halves, false));
+    if (a->n == 0) return SMC_OK;
+    ProductArgs p = forward_args(a, halves);
+    p.out = a->y;
+    p.ldo = a->ldy;
+    p.extra = a->residual;
+    p.ld_extra = a->ld_residual;
+    p.vec_o = words16(a->y, a->ldy) && (!a->residual || words16(a->residual, a->ld_residual));
+    return hip_status(launch_forward(p, epi, a->dtype, a->x_dtype == SMC_DTYPE_E4M3, a->w_transposed != 0,
+                                     (hipStream_t)stream),
+                      halves == 2 ? "smc_gated" : "smc_linear");
+}
+
+// Scratch of a backward pass: dz [n, ld_dz] (none where dz = dy), then the
+// weight gradient's float32 sums.
+struct Scratch {
+    int64_t ld_dz = 0;
+    size_t dz_bytes = 0;
+    int splits = 1;
+    size_t part_bytes = 0;
+    size_t total() const { return dz_bytes + part_bytes; }
+};
+
+Scratch scratch_of(const smc_product_t* a, int halves) {
+    Scratch s;
+    const int64_t wide = (int64_t)a->c_out * halves;
+    if (halves == 2 || a->activation != SMC_ACT_NONE) {
+        s.ld_dz = (wide + 7) / 8 * 8;
+        s.dz_bytes = round_up((size_t)a->n * s.ld_dz * 2);
+    }
+    s.splits = weight_gradient_splits(a->n, a->c_in, (int)wide);
+    s.part_bytes = round_up((size_t)s.splits * (a->c_in + (a->db ? 1 : 0)) * wide * 4);
+    return s;
+}
+
+size_t workspace_of(const smc_product_t* a, int halves) {
+    if (!a || a->n < 0 || a->n > kMaxRows || a->c_in < 1 || a->c_in > kMaxDim || a->c_out < 1 ||
+        a->c_out > kMaxDim / halves)
+        return 0;
+    return scratch_of(a, halves).total();
+}
+
+int backward(const smc_product_t* a, int halves, void* stream) {
+    const char* name = halves == 2 ? "smc_gated_backward" : "smc_linear_backward";
+    CHECK(check_product(a, halves, true));
+    const int64_t wide = (int64_t)a->c_out * halves;
+    const Scratch sc = scratch_of(a, halves);
+    if (a->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < sc.total()))
+        return bad(SMC_ERR_ARG, "workspace: %zu bytes at %p, %zu needed, 16-byte aligned",
+                   a->workspace_bytes, a->workspace, sc.total());
+    const hipStream_t s = (hipStream_t)stream;
+    if (a->n == 0)
+        return hip_status(launch_sum_parts(nullptr, 0, a->c_in, (int)wide, a->dw, a->ld_dw, a->db,
+                                           a->dtype, s), name);
+    const void* dz = a->dy;
+    int64_t ld_dz = a->ld_dy;
+    if (sc.dz_bytes) {
+        ProductArgs p = forward_args(a, halves);
+        p.extra = a->dy;
+        p.ld_extra = a->ld_dy;
+        p.out = a->workspace;
+        p.ldo = sc.ld_dz;
+        // gated: dz's second half starts at column c_out
+        p.vec_o = words16(a->dy, a->ld_dy) && (halves == 1 || a->c_out % 8 == 0);
+        CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false,
+                                        s), name));
+        dz = a->workspace;
+        ld_dz = sc.ld_dz;
+    }
+    {
+        ProductArgs p;                          // dx = dz W^T
+        p.a = dz;
+        p.lda = ld_dz;
+        p.b = a->w;
+        p.ldb = a->ldw;
+        p.m = a->n;
+        p.k = wide;
+        p.n = a->c_in;
+        p.out = a->dx;
+        p.ldo = a->ld_dx;
+        p.vec_a = words16(dz, ld_dz) && wide % 8 == 0;
+        p.vec_b = words16(a->w, a->ldw) && wide % 8 == 0;
+        p.vec_o = words16(a->dx, a->ld_dx);
+        CHECK(hip_status(launch_input_gradient(p, a->dtype, s), name));
+    }
+    ProductArgs p;                              // dW = x^T dz
+    p.a = a->x;
+    p.lda = a->ldx;
+    p.b = dz;
+    p.ldb = ld_dz;
+    p.m = a->c_in;
+    p.k = a->n;
+    p.n = (int)wide;
+    p.part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + sc.dz_bytes);
+    p.splits = sc.splits;
+    p.colsum = a->db != nullptr;
+    p.vec_a = words16(a->x, a->ldx);
+    p.vec_b = words16(dz, ld_dz);
+    CHECK(hip_status(launch_weight_gradient(p, a->dtype, s), name));
+    return hip_status(launch_sum_parts(p.part, sc.splits, a->c_in, (int)wide, a->dw, a->ld_dw, a->db,
+                                       a->dtype, s), name);
+}
+
+}  // namespace
+
+extern "C" {
+
+int smc_rms_norm(const smc_norm_t* a, void* stream) {
+    if (!a) return bad(SMC_ERR_ARG, "args is NULL");
+    CHECK(check_common(a->n, a->c, "c", a->dtype));
+    if (!(a->eps >= 0.f)) return bad(SMC_ERR_ARG, "eps = %g", (double)a->eps);
+    if (!a->weight || ((uintptr_t)a->weight & 1)) return bad(SMC_ERR_ARG, "weight is NULL or misaligned");
+    CHECK(check_rows("x", a->x, a->n, a->c, a->ldx));
+    if (a->residual) CHECK(check_rows("residual", a->residual, a->n, a->c, a->ld_residual));
+    if (a->s) CHECK(check_rows("s", a->s, a->n, a->c, a->lds));
+    if (!a->y && a->n > 0) return bad(SMC_ERR_ARG, "y is NULL");
+    if (a->ldy < a->c || a->ldy > kMaxDim)
+        return bad(SMC_ERR_ARG, "row distance of y is %lld, outside [%d, 2^21]", (long long)a->ldy, a->c);
+    if (!a->y_scale && ((uintptr_t)a->y & 1)) return bad(SMC_ERR_ARG, "y is not aligned to its elements");
+    NormArgs p;
+    p.n = a->n;
+    p.c = a->c;
+    p.eps = a->eps;
+    p.x = a->x;
+    p.ldx = a->ldx;
+    p.residual = a->residual;
+    p.ldr = a->ld_residual;
+    p.weight = a->weight;
+    p.y = a->y;
+    p.ldy = a->ldy;
+    p.y_scale = a->y_scale;
+    p.s = a->s;
+    p.lds = a->lds;
+    const bool y_ok = a->y_scale ? ((uintptr_t)a->y & 7) == 0 && a->ldy % 8 == 0 : words16(a->y, a->ldy);
+    p.vec = a->c % 8 == 0 && words16(a->x, a->ldx) && (!a->residual || words16(a->residual, a->ld_residual)) &&
+            (!a->s || words16(a->s, a->lds)) && aligned16(a->weight) && y_ok;
+    return hip_status(launch_norm(p, a->dtype, (hipStream_t)stream), "smc_rms_norm");
+}
+
+size_t smc_rms_norm_backward_workspace(int64_t n, int c) {
+    if (n < 0 || n > kMaxRows || c < 1 || c > kMaxDim) return 0;
+    return round_up((size_t)norm_backward_blocks(n, c) * c * 4);
+}
+
+int smc_rms_norm_backward(const smc_norm_backward_t* a, void* stream) {
+    if (!a) return bad(SMC_ERR_ARG, "args is NULL");
+    CHECK(check_common(a->n, a->c, "c", a->dtype));
+    if (!(a->eps >= 0.f)) return bad(SMC_ERR_ARG, "eps = %g", (double)a->eps);
+    if (!a->weight || ((uintptr_t)a->weight & 1)) return bad(SMC_ERR_ARG, "weight is NULL or misaligned");
+    if (!a->dweight || ((uintptr_t)a->dweight & 1)) return bad(SMC_ERR_ARG, "dweight is NULL or misaligned");
+    CHECK(check_rows("dy", a->dy, a->n, a->c, a->ld_dy));
+    CHECK(check_rows("s", a->s, a->n, a->c, a->lds));
+    if (a->ds) CHECK(check_rows("ds", a->ds, a->n, a->c, a->ld_ds));
+    CHECK(check_rows("dx", a->dx, a->n, a->c, a->ld_dx));
+    const size_t need = smc_rms_norm_backward_workspace(a->n, a->c);
+    if (a->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need))
+        return bad(SMC_ERR_ARG, "workspace: %zu bytes at %p, %zu needed, 16-byte aligned",
+                   a->workspace_bytes, a->workspace, need);
+    NormArgs p;
+    p.n = a->n;
+    p.c = a->c;
+    p.eps = a->eps;
+    p.x = a->s;
+    p.ldx = a->lds;
+    p.residual = a->ds;
+    p.ldr = a->ld_ds;
+    p.weight = a->weight;
+    p.y = a->dx;
+    p.ldy = a->ld_dx;
+    p.dy = a->dy;
+    p.lddy = a->ld_dy;
+    p.dweight = a->dweight;
+    p.part = static_cast<float*>(a->workspace);
+    p.vec = a->c % 8 == 0 && words16(a->s, a->lds) && words16(a->dy, a->ld_dy) &&
+            (!a->ds || words16(a->ds, a->ld_ds)) && words16(a->dx, a->ld_dx) && aligned16(a->weight);
+    return hip_status(launch_norm_backward(p, a->dtype, (hipStream_t)stream), "smc_rms_norm_backward");
+}
+
+int smc_linear(const smc_product_t* a, void* stream) { return forward(a, 1, kEpiStore, stream); }
+int smc_gated(const smc_product_t* a, void* stream) { return forward(a, 2, kEpiGated, stream); }
+int smc_linear_backward(const smc_product_t* a, void* stream) { return backward(a, 1, stream); }
+int smc_gated_backward(const smc_product_t* a, void* stream) { return backward(a, 2, stream); }
+size_t smc_linear_backward_workspace(const smc_product_t* a) { return workspace_of(a, 1); }
+size_t smc_gated_backward_workspace(const smc_product_t* a) { return workspace_of(a, 2); }
+
+int smc_weight_quantize(const void* w, int64_t ldw, int c_in, int c_out, int dtype, void* q,
+                        int64_t ldq, float* scale, void* stream) {
+    CHECK(check_common(0, c_in, "c_in", dtype));
+    if (c_out < 1 || c_out > kMaxDim) return bad(SMC_ERR_ARG, "c_out = %d outside [1, 2^21]", c_out);
+    CHECK(check_rows("w", w, c_in, c_out, ldw));
+    if (!q || !scale) return bad(SMC_ERR_ARG, "NULL pointer");
+    if (ldq < c_in || ldq > kMaxDim) return bad(SMC_ERR_ARG, "row distance of q is %lld", (long long)ldq);
+    return hip_status(launch_quantize_weight(w, ldw, c_in, c_out, q, ldq, scale, dtype, (hipStream_t)stream),
+                      "smc_weight_quantize");
+}
+
+}  // extern "C"

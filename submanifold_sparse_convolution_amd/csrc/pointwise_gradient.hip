@@ -1,0 +1,95 @@
+// Gradients of the linear and gated layers: dx = dz W^T, dW = x^T dz and
+// db = column sums of dz.
+#include <algorithm>
+#include <mutex>
+
+#include "pointwise_gemm.h"
+#include "pointwise_launch.h"
+
+namespace smc {
+
+int device_cus() {
+    static std::mutex mu;
+    static int known[64] = {};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+        int v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) v = 256;
+        known[dev] = v;
+    }
+    return known[dev];
+}
+
+hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w_along, hipStream_t s) {
+    p.k_split = p.k;
+    p.splits = 1;
+    if (e4m3)
+        return epi == kEpiGated ? launch_gated_e4m3(p, dt, w_along, s) : launch_store_e4m3(p, dt, w_along, s);
+    switch (epi) {
+        case kEpiGated: return launch_gated_16(p, dt, s);
+        case kEpiSlope: return launch_slope_16(p, dt, s);
+        case kEpiGatedSlope: return launch_gated_slope_16(p, dt, s);
+        default: return launch_store_16(p, dt, s);
+    }
+}
+
+hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s) {
+    p.k_split = p.k;
+    p.splits = 1;
+    return dt == kF16 ? launch_tiled<kF16, false, kAlongK, kAlongK, kEpiStore>(p, s)
+                      : launch_tiled<kBF16, false, kAlongK, kAlongK, kEpiStore>(p, s);
+}
+
+// Ranges of the rows: enough to give every CU two 128 x 128 tiles, none
+// shorter than 256 rows (4 steps), so that a tile's sums (64 KiB to memory and
+// back) stay small beside the rows it reads.
+int weight_gradient_splits(int64_t rows, int c_in, int n) {
+    const int64_t tiles = (int64_t)((c_in + 127) / 128) * ((n + 127) / 128);
+    const int64_t want = (2 * device_cus() + tiles - 1) / tiles;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, (rows + 255) / 256));
+}
+
+hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
+    const int64_t per = (p.k + p.splits - 1) / p.splits;
+    p.k_split = (per + 63) / 64 * 64;
+    return dt == kF16 ? launch_product<kF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s)
+                      : launch_product<kBF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s);
+}
+
+namespace {
+
+// dw[m, n] (and db[n], the row after) = the splits' float32 sums, added in
+// order and rounded once. Bound by reading them.
+template <int DT>
+__global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ part, int splits,
+                                                   int64_t m, int n, int64_t rows, uint16_t* dw,
+                                                   int64_t ldw, uint16_t* db) {
+    const int64_t total = rows * n;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    float v = 0.f;
+    for (int sp = 0; sp < splits; ++sp) v += part[(int64_t)sp * total + i];
+    const int64_t row = i / n;
+    const int col = (int)(i - row * n);
+    uint16_t* o = row < m ? dw + row * ldw + col : db + col;
+    *o = (uint16_t)from_f32<DT>(v);
+}
+
+}  // namespace
+
+hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
+                            void* db, int dt, hipStream_t s) {
+    const int64_t rows = m + (db ? 1 : 0);
+    const unsigned blocks = (unsigned)((rows * n + 255) / 256);
+    if (dt == kF16)
+        launch(k_sum_parts<kF16>, dim3(blocks), dim3(256), 0, s, part, splits, m, n, rows,
+               static_cast<uint16_t*>(dw), ldw, static_cast<uint16_t*>(db));
+    else
+        launch(k_sum_parts<kBF16>, dim3(blocks), dim3(256), 0, s, part, splits, m, n, rows,
+               static_cast<uint16_t*>(dw), ldw, static_cast<uint16_t*>(db));
+    return hipGetLastError();
+}
+
+}  // namespace smc

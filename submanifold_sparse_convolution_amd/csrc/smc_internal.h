@@ -7,6 +7,9 @@
 
 namespace smc {
 
+// Sets smc_last_error() and returns status; never throws (smconv_api.hip).
+int set_error(int status, const char* msg) noexcept;
+
 constexpr int kTaps = 27;           // 3 x 3 x 3 kernel (the mask-tile path, the fused lookup)
 constexpr int kCentre = 13;
 constexpr int kMaxTaps = 125;       // 5 x 5 x 5 kernel

@@ -37,6 +37,18 @@ int fail(int status, const char* fmt, ...) {
     return status;
 }
 
+}  // namespace
+
+int smc::set_error(int status, const char* msg) noexcept {
+    try {
+        g_last_error = msg;
+    } catch (...) {
+    }
+    return status;
+}
+
+namespace {
+
 #define SMC_HIP(call)                                                                          \
     do {                                                                                       \
         hipError_t e_ = (call);                                                                \
