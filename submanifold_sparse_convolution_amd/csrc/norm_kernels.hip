@@ -328,23 +328,26 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a)
     }
 }
 
-// dw[c] = the blocks' sums in order: 32 columns a block, 32 runs of blocks,
-// the runs added by a tree.
+// dw[c] = the blocks' sums: 8 columns a block, 128 runs of blocks (each a
+// strided sum, its loads independent), the runs added by a tree.
 template <int DT>
 __global__ __launch_bounds__(1024) void k_norm_weight_sum(const float* __restrict__ part, int blocks,
                                                           int c, uint16_t* dw) {
-    __shared__ float s[32][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    __shared__ float s[128][9];
+    const int x = threadIdx.x & 7, g = threadIdx.x >> 3;
+    const int col = blockIdx.x * 8 + x;
     float v = 0.f;
-    if (col < c)
-        for (int b = g; b < blocks; b += 32) v += part[(int64_t)b * c + col];
-    s[g][threadIdx.x & 31] = v;
+    if (col < c) {
+#pragma unroll 8
+        for (int b = g; b < blocks; b += 128) v += part[(int64_t)b * c + col];
+    }
+    s[g][x] = v;
     __syncthreads();
-    for (int o = 16; o > 0; o >>= 1) {
-        if (g < o) s[g][threadIdx.x & 31] += s[g + o][threadIdx.x & 31];
+    for (int o = 64; o > 0; o >>= 1) {
+        if (g < o) s[g][x] += s[g + o][x];
         __syncthreads();
     }
-    if (g == 0 && col < c) dw[col] = (uint16_t)from_f32<DT>(s[0][threadIdx.x]);
+    if (g == 0 && col < c) dw[col] = (uint16_t)from_f32<DT>(s[0][x]);
 }
 
 // W [c_in, c_out] -> q [c_out, c_in] e4m3, one scale a column of W. 32 columns
@@ -447,7 +450,7 @@ hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
         else
             launch(k_norm_backward_wide<DT, 1>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
     }
-    launch(k_norm_weight_sum<DT>, dim3((unsigned)((a.c + 31) / 32)), dim3(1024), 0, s, a.part, blocks,
+    launch(k_norm_weight_sum<DT>, dim3((unsigned)((a.c + 7) / 8)), dim3(1024), 0, s, a.part, blocks,
            a.c, static_cast<uint16_t*>(a.dweight));
     return hipGetLastError();
 }

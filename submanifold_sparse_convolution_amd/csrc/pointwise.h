@@ -30,7 +30,7 @@ struct ProductArgs {
     const void* a = nullptr;    // rows of the output
     const void* b = nullptr;    // columns of the output
     int64_t lda = 0, ldb = 0;   // elements from one memory row to the next
-    int64_t m = 0, k = 0;
+    int m = 0, k = 0;
     int n = 0;                  // columns of b (gated: both halves)
     int half = 0;               // gated: columns of one half
     const void* bias = nullptr; // [n]
@@ -41,7 +41,7 @@ struct ProductArgs {
     void* out = nullptr;        // [m, n] ([m, half] for kEpiGated)
     int64_t ldo = 0;
     float* part = nullptr;      // kEpiPartial: [splits][m + colsum][n]
-    int64_t k_split = 0;        // contraction length of a split (all of k: one split)
+    int k_split = 0;            // contraction length of a split (all of k: one split)
     int splits = 1;
     int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
     int act = 0;
@@ -49,6 +49,7 @@ struct ProductArgs {
     int vec_o = 0;              // 16-byte stores (and loads of extra) are possible
     // the tile walk
     int tiles_m = 0, tiles_n = 0;
+    int group_log = 0;          // row tiles walked together (log2)
     int xcds = 8;
 };
 

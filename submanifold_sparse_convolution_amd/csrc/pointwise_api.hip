@@ -11,7 +11,7 @@ using namespace smc;
 namespace {
 
 constexpr int64_t kMaxDim = 1 << 21;           // channels and row distances: tile offsets fit 31 bits
-constexpr int64_t kMaxRows = (int64_t)1 << 36;
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1024;   // row numbers are 32-bit
 constexpr size_t kAlign = 256;
 
 int bad(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -110,7 +110,7 @@ ProductArgs forward_args(const smc_product_t* a, int halves) {
     p.lda = a->ldx;
     p.b = a->w;
     p.ldb = a->ldw;
-    p.m = a->n;
+    p.m = (int)a->n;
     p.k = a->c_in;
     p.n = a->c_out * halves;
     p.half = a->c_out;
@@ -134,7 +134,7 @@ int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
     p.ldo = a->ldy;
     p.extra = a->residual;
     p.ld_extra = a->ld_residual;
-    p.vec_o = words16(a->y, a->ldy) && (!a->residual || words16(a->residual, a->ld_residual));
+    p.vec_o = a->c_out >= 8 && words16(a->y, a->ldy) && (!a->residual || words16(a->residual, a->ld_residual));
     return hip_status(launch_forward(p, epi, a->dtype, a->x_dtype == SMC_DTYPE_E4M3, a->w_transposed != 0,
                                      (hipStream_t)stream),
                       halves == 2 ? "smc_gated" : "smc_linear");
@@ -190,7 +190,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.out = a->workspace;
         p.ldo = sc.ld_dz;
         // gated: dz's second half starts at column c_out
-        p.vec_o = words16(a->dy, a->ld_dy) && (halves == 1 || a->c_out % 8 == 0);
+        p.vec_o = a->c_out >= 8 && words16(a->dy, a->ld_dy) && (halves == 1 || a->c_out % 8 == 0);
         CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false,
                                         s), name));
         dz = a->workspace;
@@ -202,8 +202,8 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.lda = ld_dz;
         p.b = a->w;
         p.ldb = a->ldw;
-        p.m = a->n;
-        p.k = wide;
+        p.m = (int)a->n;
+        p.k = (int)wide;
         p.n = a->c_in;
         p.out = a->dx;
         p.ldo = a->ld_dx;
@@ -218,7 +218,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
     p.b = dz;
     p.ldb = ld_dz;
     p.m = a->c_in;
-    p.k = a->n;
+    p.k = (int)a->n;
     p.n = (int)wide;
     p.part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + sc.dz_bytes);
     p.splits = sc.splits;

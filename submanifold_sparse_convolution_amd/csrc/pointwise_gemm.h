@@ -26,6 +26,8 @@
 // write zeros to LDS, so every edge multiplies by exact zeros on both sides.
 #pragma once
 
+#include <type_traits>
+
 #include "pointwise.h"
 
 namespace smc {
@@ -36,11 +38,16 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define SMC_LDS __attribute__((address_space(3)))
+// for lambdas over register arrays: a call that is not inlined puts them in memory
+#define SMC_INLINE __attribute__((always_inline))
 
 constexpr uint32_t kOutside = 0x80000000u;      // beyond every buffer's end
 
@@ -61,7 +68,9 @@ __device__ __forceinline__ uint32_t from_f32(float f) {
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return from_f32<DT>(a) | (from_f32<DT>(b) << 16);
+    const f32x2 v = {a, b};
+    if (DT == kF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 template <int DT>
@@ -89,37 +98,81 @@ __device__ __forceinline__ f32x4 mfma_e4m3(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
-__device__ __forceinline__ float act_value(float z, int act) {
-    switch (act) {
-        case kActRelu: return z < 0.f ? 0.f : z;
-        case kActSilu: return z * sigmoid(z);
-        case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        default: return z;
-    }
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2). erf by formula 7.1.26 of
+// Abramowitz and Stegun (error below 1.5e-7, what float32 leaves of 1 + erf
+// anyway), whose exponential is the Gaussian that the slope needs too.
+__device__ __forceinline__ float normal_cdf(float z, float& gauss) {
+    gauss = __expf(-0.5f * z * z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+    const float tail = 0.5f * gauss * t *
+                       fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f),
+                                    -0.284496736f), 0.254829592f);
+    return z < 0.f ? tail : 1.f - tail;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if (ACT == kActRelu) return z < 0.f ? 0.f : z;
+    if (ACT == kActSilu) return z * sigmoid(z);
+    if (ACT == kActGelu) {
+        float g;
+        return z * normal_cdf(z, g);
+    }
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
+    if (ACT == kActSilu) {
+        const float g = sigmoid(z);
+        return g * (1.f + z * (1.f - g));
+    }
+    if (ACT == kActGelu) {
+        float g;
+        const float c = normal_cdf(z, g);
+        return c + z * 0.39894228040143268f * g;
+    }
+    return 1.f;
+}
+
+// f(integral constant of the activation): one copy of f for each, so that the
+// choice is made once and not for every element.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
     switch (act) {
-        case kActRelu: return z > 0.f ? 1.f : 0.f;
-        case kActSilu: {
-            const float g = sigmoid(z);
-            return g * (1.f + z * (1.f - g));
-        }
-        case kActGelu:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-                   z * 0.39894228040143268f * __expf(-0.5f * z * z);
-        default: return 1.f;
+        case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+        case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+        case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+        default: f(std::integral_constant<int, kActNone>());
     }
 }
 
 // ---- staging one operand --------------------------------------------------------
 
-// 16 bytes a lane from the buffer to LDS, lane l's at lds + 16 l. (Kept out of
-// the templates: the host pass drops a template that calls this builtin with a
-// size of 16 without a word.)
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SMC_LDS void*)lds, 16, off, 0, 0, 0);
+// 16 bytes from any element's address.
+__device__ __forceinline__ u32x4 load_unaligned(const void* p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
 }
+
+// 16 bytes a lane from the buffer to LDS, lane l's at lds + 16 l. In assembly
+// (it has no output register) because the compiler, where it knows of such
+// loads, waits for all of them before every transposing LDS read, and so for
+// the next step's; the kernel waits for them itself (wait_vm).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"     // m0 is a reserved register, and it is clobbered
+__device__ __forceinline__ void load_to_lds(u32x4 descriptor, uint32_t lds, uint32_t off) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(off), "s"(descriptor)
+        : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // Word permutations of the kAcrossK images: over the k rows that one
 // transposing read touches (see frag_across, frag_across_e4m3).
@@ -178,17 +231,24 @@ struct Stager {
     }
 
     // base: the step's first element (kAlongK: of the tile's first row; else of
-    // column 0); bytes: from there to the operand's end; k_left: contraction left
-    __device__ void load(const char* base, uint32_t bytes, int k_left, char* lds, int wave) const {
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(base), 0, (int)bytes, 0x00020000);
-        const uint32_t dead = LAYOUT == kAlongK && (int)src >= k_left ? kOutside : 0u;
+    // column 0); bytes: from there to the operand's end; k_left: contraction left,
+    // WHOLE where that is known to be a whole step
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const char* base, uint32_t bytes, int k_left, char* lds, int wave) const {
+        // (the same in every lane, which the compiler does not always see)
+        const uint64_t b = (uint64_t)base;
+        const u32x4 descriptor = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                                  (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)),
+                                  (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+        const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane(
+            (int)(uint32_t)(uintptr_t)(SMC_LDS char*)lds + wave * 1024);
+        const uint32_t dead = !WHOLE && LAYOUT == kAlongK && (int)src >= k_left ? kOutside : 0u;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            load_to_lds(r, lds + (i * THREADS + wave * 64) * 16, off[i] | dead);
+        for (int i = 0; i < kLoads; ++i) load_to_lds(descriptor, first + i * THREADS * 16, off[i] | dead);
     }
 
-    // The same step by element loads, for operands that 16-byte words do not fit.
+    // The same step through registers, for operands whose rows are not made of
+    // 16-byte words: unaligned words, and element by element at the row ends.
     __device__ void load_elements(const char* base, uint32_t bytes, int k_left, int tid, char* lds,
                                   int row0, int count, int half) const {
 #pragma unroll 1
@@ -207,6 +267,9 @@ struct Stager {
             }
             if (o == kOutside) left = 0;
             u32x4 w;
+            if (left >= kPer16 && o + 16 <= bytes) {
+                w = load_unaligned(base + o);
+            } else
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 uint32_t u = 0;
@@ -261,15 +324,19 @@ __device__ __forceinline__ u32x4 frag_across_e4m3(const char* tile, int piece, i
 
 // ---- the kernel -----------------------------------------------------------------
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int BLOCKS_>
+// UNALIGNED: operands that are not whole 16-byte words too.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int BLOCKS_, bool UNALIGNED_ = false>
 struct Tile {
+    static constexpr bool kUnaligned = UNALIGNED_;
     static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
     static constexpr int kThreads = 64 * WAVES_M * WAVES_N;
     static constexpr int MT = BM / (16 * WAVES_M);
-    static constexpr int kBlocks = BLOCKS_;             // blocks a CU (register budget)
+    static constexpr int kBlocks = BLOCKS_;             // blocks a CU (LDS and register budget)
     static constexpr int kStepBytes = (BM + BN) * 128;
     static constexpr int kLdsBytes = kStepBytes * STAGES;
+    static constexpr int kLoads = (BM + BN) * 8 / kThreads;     // loads a lane and step
     static_assert(BN == 64 * WAVES_N, "a wave owns 64 columns");
+    static_assert(kLdsBytes * BLOCKS_ <= 160 * 1024, "LDS");
 };
 
 // 8 consecutive values <-> a lane's two 4-value groups: lanes of odd 16-lane
@@ -280,261 +347,515 @@ __device__ __forceinline__ void swap_rows(uint32_t& lo, uint32_t& hi) {
     hi = r.y;
 }
 
+// The first `count` (at most 8) elements of a row's end, zeros after them.
+__device__ __forceinline__ u32x4 load_tail(const uint16_t* p, int count) {
+    u32x4 w;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t lo = 2 * d < count ? p[2 * d] : 0u, hi = 2 * d + 1 < count ? p[2 * d + 1] : 0u;
+        w[d] = lo | (hi << 16);
+    }
+    return w;
+}
+
+// ---- the epilogue of 16 rows x 64 columns ------------------------------------------
+// acc[j] holds row r, columns 16 j + 4 q .. + 3 of the wave's 64; gated: the gate
+// half's 32 columns, then the same of the up half. Outputs (and `extra`) are read
+// and written as 8 consecutive columns a lane, `kPairs` of them.
+
+template <int EPI>
+struct Shape {
+    static constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
+    static constexpr bool kHasExtra = EPI == kEpiStore || EPI == kEpiSlope || EPI == kEpiGatedSlope;
+    static constexpr int kPairs = kGated ? 1 : 2;                   // 8-value words of extra
+    static constexpr int kOut = EPI == kEpiGated ? 1 : 2;           // 8-value words of out
+    // columns of a half (or of out) from column nw on: accumulator (j, e) and word h
+    __device__ static int column(int nw, int j, int q, int e) { return nw + (kGated ? (j & 1) : j) * 16 + q * 4 + e; }
+    __device__ static int word(int nw, int h, int q) { return nw + (kGated ? 0 : h * 32) + (q & 1) * 16 + (q >> 1) * 8; }
+};
+
+// What depends on the columns alone, kept in LDS for the tile (in registers it
+// would be 32 of them through the whole contraction): bias and, for e4m3, the
+// columns' scales, for virtual column v of the block at [v].
+template <int BN, bool E4M3>
+struct ColumnTable {
+    float bias[BN];
+    float scale[E4M3 ? BN : 1];
+};
+
+template <int DT, bool E4M3, int EPI, int BN>
+__device__ __forceinline__ void fill_columns(ColumnTable<BN, E4M3>& t, const ProductArgs& p, int n0, int width, int v) {
+    using Sh = Shape<EPI>;
+    if (v >= BN) return;
+    const int c = Sh::kGated ? n0 + (v >> 6) * 32 + (v & 31) : n0 + v;
+    const int cc = c < width ? c : width - 1;       // past the last column the last one (not stored)
+    const int b = Sh::kGated && (v & 32) ? cc + p.half : cc;
+    t.bias[v] = p.bias ? to_f32<DT>(static_cast<const uint16_t*>(p.bias)[b]) : 0.f;
+    if (E4M3) t.scale[v] = p.b_scale[b];
+}
+
+template <int EPI>
+__device__ __forceinline__ u32x4 load_extra(const ProductArgs& p, int row, int nw, int h, int q, int width) {
+    const int col = Shape<EPI>::word(nw, h, q);
+    const uint16_t* e0 = static_cast<const uint16_t*>(p.extra) + (int64_t)(row < p.m ? row : p.m - 1) * p.ld_extra;
+    if (!p.vec_o) return load_tail(e0 + col, width - col);
+    u32x4 x = *reinterpret_cast<const u32x4*>(e0 + (col + 8 <= width ? col : 0));
+    if (col < width && col + 8 > width) x = load_tail(e0 + col, width - col);
+    return x;
+}
+
+// The values, in place of the sums.
+template <int DT, int EPI, int ACT, bool EXTRA>
+__device__ __forceinline__ void row_values(f32x4 (&acc)[4], const u32x4 (&extra)[Shape<EPI>::kPairs]) {
+    using Sh = Shape<EPI>;
+    u32x4 x[Sh::kPairs];
+    if constexpr (EXTRA) {
+#pragma unroll
+        for (int h = 0; h < Sh::kPairs; ++h) {
+            // (opaque: else all rows' values are unpacked at once, into too many registers)
+            x[h] = extra[h];
+            asm volatile("" : "+v"(x[h]));
+            uint32_t l0 = x[h].x, l1 = x[h].y, h0 = x[h].z, h1 = x[h].w;
+            swap_rows(l0, h0);
+            swap_rows(l1, h1);
+            x[h] = (u32x4){l0, l1, h0, h1};         // the accumulators' order
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < (Sh::kGated ? 2 : 4); ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float z = acc[j][e], u = acc[(j + 2) & 3][e];
+            float ex = 0.f;
+            if constexpr (EXTRA) {
+                const uint32_t w = x[j >> 1][(j & 1) * 2 + (e >> 1)];
+                ex = to_f32<DT>(e & 1 ? w >> 16 : w & 0xffffu);
+            }
+            if (EPI == kEpiStore) acc[j][e] = EXTRA ? act_value<ACT>(z) + ex : act_value<ACT>(z);
+            if (EPI == kEpiSlope) acc[j][e] = ex * act_slope<ACT>(z);
+            if (EPI == kEpiGated) acc[j][e] = act_value<ACT>(z) * u;
+            if (EPI == kEpiGatedSlope) {
+                acc[j][e] = ex * u * act_slope<ACT>(z);
+                acc[(j + 2) & 3][e] = ex * act_value<ACT>(z);
+            }
+        }
+}
+
+// Rounds and stores them. FULL: the row and its columns exist and words are
+// aligned: one store for each word.
+template <int DT, int EPI, bool FULL>
+__device__ __forceinline__ void row_store(const ProductArgs& p, const f32x4 (&acc)[4], int row, int nw, int q, int width) {
+    using Sh = Shape<EPI>;
+#pragma unroll
+    for (int h = 0; h < Sh::kOut; ++h) {
+        const int col = Sh::word(nw, h, q);     // the second word of a gated pair is the up half's
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)row * p.ldo + col + (Sh::kGated && h ? p.half : 0);
+        uint32_t l0 = pack2<DT>(acc[2 * h][0], acc[2 * h][1]), l1 = pack2<DT>(acc[2 * h][2], acc[2 * h][3]);
+        uint32_t h0 = pack2<DT>(acc[2 * h + 1][0], acc[2 * h + 1][1]);
+        uint32_t h1 = pack2<DT>(acc[2 * h + 1][2], acc[2 * h + 1][3]);
+        swap_rows(l0, h0);
+        swap_rows(l1, h1);
+        if (FULL || (row < p.m && p.vec_o && col + 8 <= width)) {
+            *reinterpret_cast<u32x4*>(dst) = (u32x4){l0, l1, h0, h1};
+        } else if (row < p.m) {
+            const uint32_t w[4] = {l0, l1, h0, h1};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e < width) dst[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+        }
+    }
+}
+
+// At most N of this wave's memory operations are still in flight.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N < 64, "a 6-bit counter");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// One tile of the walk. Tiles are numbered split by split (kEpiPartial), within
+// a split group by group of 2^group_log row tiles, within a group column tile by
+// column tile, its row tiles in turn.
+template <class T, int EPI>
+struct Place {
+    int t, in_group, group, tn, tm, n0, split, steps;
+    int m0, k0, k_len;
+    __device__ int group_rows(const ProductArgs& p) const {
+        const int left = p.tiles_m - (group << p.group_log);
+        return left < (1 << p.group_log) ? left : 1 << p.group_log;
+    }
+    __device__ void start(const ProductArgs& p, int tile, int step_k) {
+        t = tile;
+        split = 0;
+        int rest = t;
+        if (EPI == kEpiPartial) {
+            split = t / (p.tiles_m * p.tiles_n);
+            rest = t - split * p.tiles_m * p.tiles_n;
+        }
+        group = rest / (p.tiles_n << p.group_log);
+        in_group = rest - group * (p.tiles_n << p.group_log);
+        derive(p, step_k);
+    }
+    __device__ void advance(const ProductArgs& p, int by, int step_k) {
+        t += by;
+        in_group += by;
+        for (int size = group_rows(p) * p.tiles_n; in_group >= size; size = group_rows(p) * p.tiles_n) {
+            in_group -= size;
+            ++group;
+            if (EPI == kEpiPartial && (group << p.group_log) >= p.tiles_m) {
+                group = 0;
+                ++split;
+            }
+        }
+        derive(p, step_k);
+    }
+    __device__ void derive(const ProductArgs& p, int step_k) {
+        constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
+        const int rows = group_rows(p);
+        tn = rows == 1 << p.group_log ? in_group >> p.group_log : in_group / rows;
+        tm = (group << p.group_log) + in_group - tn * rows;
+        n0 = tn * (kGated ? T::BN / 2 : T::BN);         // gated: column of a half
+        m0 = tm * T::BM;
+        k0 = split * p.k_split;
+        k_len = p.k - k0 < p.k_split ? p.k - k0 : p.k_split;
+        steps = k_len > 0 ? (k_len + step_k - 1) / step_k : 0;
+    }
+};
+
 template <int DT, bool E4M3, int LA, int LB, int EPI, class T, bool ALIGNED>
 __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_product(ProductArgs p) {
     constexpr int MT = T::MT;
     constexpr int ESIZE = E4M3 ? 1 : 2;
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
+    constexpr bool kHasExtra = EPI == kEpiStore || EPI == kEpiSlope || EPI == kEpiGatedSlope;
+    constexpr int kPairs = kGated ? 1 : 2;
     constexpr int kStep = 128 / ESIZE;
+    constexpr int S = T::STAGES;
     extern __shared__ __align__(1024) char s_tile[];
+    __shared__ __align__(16) ColumnTable<T::BN, E4M3> s_columns;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, r = lane & 15;
     const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
 
     // Blocks are dealt to the XCDs in turn; each XCD walks a contiguous run of
-    // tiles, columns fastest, so a row panel is read into one L2.
+    // tiles, its blocks side by side: at any time they read a group of row
+    // panels of a that stays in the XCD's L2 and a few column tiles of b.
     const int total = p.tiles_m * p.tiles_n * p.splits;
-    int t;
-    {
-        const int x = blockIdx.x % p.xcds, i = blockIdx.x / p.xcds;
-        const int per = total / p.xcds, more = total % p.xcds;
-        t = x * per + (x < more ? x : more) + i;
-    }
-    const int tn = t % p.tiles_n;
-    const int tm = (t / p.tiles_n) % p.tiles_m;
-    const int split = t / (p.tiles_n * p.tiles_m);
-    const int64_t m0 = (int64_t)tm * T::BM;
-    const int n0 = kGated ? tn * (T::BN / 2) : tn * T::BN;      // gated: column of a half
-    const int64_t k0 = split * p.k_split;
-    const int64_t k_len = (p.k - k0 < p.k_split ? p.k - k0 : p.k_split);
-    const int steps = (int)((k_len + kStep - 1) / kStep);
+    const int xcd = blockIdx.x % p.xcds, slot = blockIdx.x / p.xcds;
+    const int per = total / p.xcds, more = total % p.xcds;
+    const int t_end = (xcd + 1) * per + (xcd + 1 < more ? xcd + 1 : more);
+    const int t_step = ((int)gridDim.x - xcd + p.xcds - 1) / p.xcds;
+    const int t_first = xcd * per + (xcd < more ? xcd : more) + slot;
+    if (t_first >= t_end) return;
 
+    // ---- loads: the step that is issued next, S - 1 steps ahead ----
+    Place<T, EPI> ahead;
     Stager<T::BM, LA, T::kThreads, ESIZE, false> sa;
     Stager<T::BN, LB, T::kThreads, ESIZE, kGated> sb;
-    sa.setup(tid, (int)(LA == kAlongK ? 0 : m0), p.lda, (int)p.m, 0);
-    sb.setup(tid, LB == kAlongK && !kGated ? 0 : n0, p.ldb, p.n, p.half);
-    const int rows_a = (int)(p.m - m0 < T::BM ? p.m - m0 : T::BM);
-    const int rows_b = kGated ? p.n : (p.n - n0 < T::BN ? p.n - n0 : T::BN);
-    const char* base_a = static_cast<const char*>(p.a) +
-                         (LA == kAlongK ? m0 * p.lda + k0 : k0 * p.lda) * ESIZE;
-    const char* base_b = static_cast<const char*>(p.b) +
-                         (LB == kAlongK ? (kGated ? 0 : n0) * p.ldb + k0 : k0 * p.ldb) * ESIZE;
-
-    auto issue = [&](int step) {
-        const int kd = step * kStep;
-        const int64_t left64 = k_len - kd;
-        const int left = (int)(left64 < kStep ? left64 : kStep);
-        char* dst = s_tile + (step % T::STAGES) * T::kStepBytes;
-        const int64_t k_rest = p.k - k0 - kd;       // along k the row goes on past a split's end
-        const char* pa = base_a + (LA == kAlongK ? (int64_t)kd : kd * p.lda) * ESIZE;
-        const char* pb = base_b + (LB == kAlongK ? (int64_t)kd : kd * p.ldb) * ESIZE;
-        const uint32_t ba = (uint32_t)((LA == kAlongK ? (rows_a - 1) * p.lda + k_rest
-                                                      : (left - 1) * p.lda + p.m) * ESIZE);
-        const uint32_t bb = (uint32_t)((LB == kAlongK ? (rows_b - 1) * p.ldb + k_rest
-                                                      : (left - 1) * p.ldb + p.n) * ESIZE);
-        // the range check is by 4-byte words: a last element that fills one
-        // only partly needs the whole word in range (aligned, so on its page)
-        const uint32_t wa = (ba + 3) & ~3u, wb = (bb + 3) & ~3u;
+    const char *next_a, *next_b;        // first element of the next step
+    uint32_t bytes_a, bytes_b;          // from there to the operand's end (for a whole step)
+    int ahead_step = 0;
+    int ahead_buf = 0;                  // byte offset of the buffer it goes to
+    // along k a step is 128 bytes further in every row; across k, 128 / ESIZE rows on
+    const int64_t by_a = LA == kAlongK ? 128 : (int64_t)kStep * p.lda * ESIZE;
+    const int64_t by_b = LB == kAlongK ? 128 : (int64_t)kStep * p.ldb * ESIZE;
+    // The range check is by 4-byte words: a last element that fills one only
+    // partly needs the whole word in range (aligned, so on its page).
+    auto whole_words = [](int64_t bytes) SMC_INLINE { return (uint32_t)(bytes + 3) & ~3u; };
+    auto enter = [&](bool first, bool new_rows, bool new_columns) SMC_INLINE {
+        ahead_step = 0;
+        // along k a tile's rows are told by the base alone
+        if (first || (LA == kAcrossK && new_rows))
+            sa.setup(tid, LA == kAlongK ? 0 : ahead.m0, p.lda, p.m, 0);
+        if (first || ((LB == kAcrossK || kGated) && new_columns))
+            sb.setup(tid, LB == kAlongK && !kGated ? 0 : ahead.n0, p.ldb, p.n, p.half);
+        const int rows_a = p.m - ahead.m0 < T::BM ? p.m - ahead.m0 : T::BM;
+        const int rows_b = kGated ? p.n : (p.n - ahead.n0 < T::BN ? p.n - ahead.n0 : T::BN);
+        next_a = static_cast<const char*>(p.a) +
+                 (LA == kAlongK ? (int64_t)ahead.m0 * p.lda + ahead.k0 : (int64_t)ahead.k0 * p.lda) * ESIZE;
+        next_b = static_cast<const char*>(p.b) +
+                 (LB == kAlongK ? (int64_t)(kGated ? 0 : ahead.n0) * p.ldb + ahead.k0 : (int64_t)ahead.k0 * p.ldb) * ESIZE;
+        bytes_a = whole_words((LA == kAlongK ? (rows_a - 1) * p.lda + p.k - ahead.k0
+                                             : (kStep - 1) * p.lda + p.m) * ESIZE);
+        bytes_b = whole_words((LB == kAlongK ? (rows_b - 1) * p.ldb + p.k - ahead.k0
+                                             : (kStep - 1) * p.ldb + p.n) * ESIZE);
+    };
+    auto issued = [&]() SMC_INLINE {
+        next_a += by_a;
+        next_b += by_b;
+        if (LA == kAlongK) bytes_a -= 128;
+        if (LB == kAlongK) bytes_b -= 128;
+        ++ahead_step;
+        ahead_buf = ahead_buf == (S - 1) * T::kStepBytes ? 0 : ahead_buf + T::kStepBytes;
+    };
+    // a step that is known to exist and to be whole
+    auto issue_whole = [&]() SMC_INLINE {
+        char* dst = s_tile + ahead_buf;
+        sa.template load<true>(next_a, bytes_a, kStep, dst, wave);
+        sb.template load<true>(next_b, bytes_b, kStep, dst + T::BM * 128, wave);
+        issued();
+    };
+    // any step; false when the walk is over
+    auto issue = [&]() SMC_INLINE {
+        while (ahead_step >= ahead.steps) {             // (a split may be empty)
+            if (ahead.t + t_step >= t_end) return false;
+            const int tm = ahead.tm, tn = ahead.tn;
+            ahead.advance(p, t_step, kStep);
+            enter(false, ahead.tm != tm, ahead.tn != tn);
+        }
+        const int rest = ahead.k_len - ahead_step * kStep;
+        const int left = rest < kStep ? rest : kStep;
+        char* dst = s_tile + ahead_buf;
+        const uint32_t wa = LA == kAlongK ? bytes_a : whole_words(((left - 1) * p.lda + p.m) * ESIZE);
+        const uint32_t wb = LB == kAlongK ? bytes_b : whole_words(((left - 1) * p.ldb + p.n) * ESIZE);
         if (ALIGNED || p.vec_a)
-            sa.load(pa, wa, left, dst, wave);
+            sa.template load<false>(next_a, wa, left, dst, wave);
         else
-            sa.load_elements(pa, ba, left, tid, dst, (int)m0, (int)p.m, 0);
+            sa.load_elements(next_a, wa, left, tid, dst, ahead.m0, p.m, 0);
         if (ALIGNED || p.vec_b)
-            sb.load(pb, wb, left, dst + T::BM * 128, wave);
+            sb.template load<false>(next_b, wb, left, dst + T::BM * 128, wave);
         else
-            sb.load_elements(pb, bb, left, tid, dst + T::BM * 128, n0, p.n, p.half);
+            sb.load_elements(next_b, wb, left, tid, dst + T::BM * 128, ahead.n0, p.n, p.half);
+        issued();
+        return true;
     };
 
-    f32x4 acc[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    f32x4 sum[4];                                   // column sums of b (kEpiPartial)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    const bool colsum = EPI == kEpiPartial && p.colsum && tm == 0 && wm == 0;
+    ahead.start(p, t_first, kStep);
+    Place<T, EPI> here = ahead;
+    enter(true, true, true);
+    bool over = false;                                  // every step has been issued
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) over = !issue();
 
+    int buf = 0;                        // byte offset of the step's buffer
+    int after_stores = 0;               // steps to come that were issued before a full tile's stores
 #pragma unroll 1
-    for (int st = 0; st < T::STAGES - 1 && st < steps; ++st) issue(st);
-#pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-        // this step's words have landed, and every wave is done with the buffer
-        // that the next loads will overwrite
-        if (ALIGNED)
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (step + T::STAGES - 1 < steps) issue(step + T::STAGES - 1);
-        const char* ta = s_tile + (step % T::STAGES) * T::kStepBytes;
-        const char* tb = ta + T::BM * 128;
-        if constexpr (E4M3) {
-            u32x4 fb[4][2];
+    for (;; here.advance(p, t_step, kStep)) {
+        // What the epilogue reads: columns of this lane's pair of 4-value groups
+        // and of its 8 stored values. Past the last row or column the last one
+        // is read (and not stored), so that the loads need no branches.
+        const int width = kGated ? p.half : p.n;        // columns of out (and extra)
+        const int nw = here.n0 + wn * (kGated ? 32 : 64);
+        const int row_base = here.m0 + wm * MT * 16 + r;
+        u32x4 extra[MT][kPairs];
+        float ascale[MT];
+        auto load_epilogue = [&]() SMC_INLINE {
+            if constexpr (EPI != kEpiPartial) {
+                if (E4M3 || p.bias) fill_columns<DT, E4M3, EPI, T::BN>(s_columns, p, here.n0, width, tid);
+                if (E4M3) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    fb[j][h] = LB == kAlongK ? frag_along(tb, wn * 64 + j * 16 + r, 4 * h + q)
-                                             : frag_across_e4m3<T::BN>(tb, wn * 4 + j, h, lane);
+                    for (int i = 0; i < MT; ++i) {
+                        const int row = row_base + i * 16;
+                        ascale[i] = p.a_scale[row < p.m ? row : p.m - 1];
+                    }
+                }
             }
+            if constexpr (kHasExtra) {
+                if (p.extra) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const u32x4 a0 = frag_along(ta, (wm * MT + i) * 16 + r, q);
-                const u32x4 a1 = frag_along(ta, (wm * MT + i) * 16 + r, 4 + q);
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma_e4m3(fb[j][0], fb[j][1], a0, a1, acc[i][j]);
+                        for (int h = 0; h < kPairs; ++h)
+                            extra[i][h] = load_extra<EPI>(p, row_base + i * 16, nw, h, q, width);
+                }
             }
-        } else {
+        };
+
+        f32x4 acc[MT][4];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                u32x4 fb[4];
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    fb[j] = LB == kAlongK ? frag_along(tb, wn * 64 + j * 16 + r, kk * 4 + q)
-                                          : frag_across<T::BN>(tb, wn * 4 + j, kk, lane);
-                u32x4 fa[MT];
+            for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        f32x4 sum[4];                           // column sums of b (kEpiPartial)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        const bool colsum = EPI == kEpiPartial && p.colsum && here.tm == 0 && wm == 0;
+
+        // One step: the products of the buffer at `buf`.
+        auto compute = [&]() SMC_INLINE {
+            const char* ta = s_tile + buf;
+            const char* tb = ta + T::BM * 128;
+            buf = buf == (S - 1) * T::kStepBytes ? 0 : buf + T::kStepBytes;
+            if constexpr (E4M3) {
+                u32x4 fb[4][2], fa[MT][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        fb[j][h] = LB == kAlongK ? frag_along(tb, wn * 64 + j * 16 + r, 4 * h + q)
+                                                 : frag_across_e4m3<T::BN>(tb, wn * 4 + j, h, lane);
+                }
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
-                    fa[i] = LA == kAlongK ? frag_along(ta, (wm * MT + i) * 16 + r, kk * 4 + q)
-                                          : frag_across<T::BM>(ta, wm * MT + i, kk, lane);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) fa[i][h] = frag_along(ta, (wm * MT + i) * 16 + r, 4 * h + q);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = mfma_e4m3(fb[j][0], fb[j][1], fa[i][0], fa[i][1], acc[i][j]);
+                __builtin_amdgcn_s_setprio(0);
+            } else {
+                u32x4 fb[2][4], fa[2][MT];
+                auto read = [&](int kk) SMC_INLINE {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        fb[kk][j] = LB == kAlongK ? frag_along(tb, wn * 64 + j * 16 + r, kk * 4 + q)
+                                                  : frag_across<T::BN>(tb, wn * 4 + j, kk, lane);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        fa[kk][i] = LA == kAlongK ? frag_along(ta, (wm * MT + i) * 16 + r, kk * 4 + q)
+                                                  : frag_across<T::BM>(ta, wm * MT + i, kk, lane);
+                };
+                auto multiply = [&](int kk) SMC_INLINE {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(fb[kk][j], fa[kk][i], acc[i][j]);
+                };
+                // the second half's reads go out between the first half's products
+                read(0);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+                multiply(0);
+                read(1);
+                constexpr int kReads = (LB == kAlongK ? 4 : 8) + (LA == kAlongK ? MT : 2 * MT);
+                constexpr int kBetween = MT * 4 / kReads > 0 ? MT * 4 / kReads : 1;
+#pragma unroll
+                for (int i = 0; i < kReads; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, kBetween, 0);   // MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // LDS read
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(1);
+                __builtin_amdgcn_s_setprio(0);
                 if (EPI == kEpiPartial && colsum) {
                     constexpr uint32_t one = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
                     const u32x4 ones = {one, one, one, one};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sum[j] = mfma16<DT>(fb[j], ones, sum[j]);
+                    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum[j] = mfma16<DT>(fb[kk][j], ones, sum[j]);
                 }
             }
-        }
-    }
+        };
 
-    // ---- epilogue: acc[i][j] holds row 16 i + r, columns 16 j + 4 q .. + 3 ----
-    const int64_t row_base = m0 + wm * MT * 16 + r;
-    if constexpr (EPI == kEpiPartial) {
-        float* part = p.part + (int64_t)split * (p.m + p.colsum) * p.n;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int col = n0 + wn * 64 + j * 16 + q * 4;
-            if (col >= p.n) continue;
-            const bool whole = col + 4 <= p.n && (p.n & 3) == 0;
-#pragma unroll
-            for (int i = 0; i <= MT; ++i) {
-                const bool is_sum = i == MT;
-                const int64_t row = is_sum ? p.m : row_base + i * 16;
-                if (is_sum ? !(colsum && r == 0) : row >= p.m) continue;
-                const f32x4 v = is_sum ? sum[j] : acc[i < MT ? i : 0][j];
-                float* o = part + row * p.n + col;
-                if (whole) {
-                    *reinterpret_cast<f32x4*>(o) = v;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < p.n) o[e] = v[e];
-                }
+        // At a step's start its words have landed (all but the loads of later
+        // steps, and stores issued after them, may still be in flight), and
+        // every wave is done with the buffer that the next loads overwrite.
+        constexpr int kLater = (S - 2) * T::kLoads;
+        constexpr int kStores = MT * (EPI == kEpiGated ? 1 : 2);
+        auto arrive = [&]() SMC_INLINE {
+            if (after_stores > 0)
+                wait_vm<kLater + kStores>();
+            else
+                wait_vm<kLater>();
+            --after_stores;
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+        int step = 0;
+        if constexpr (ALIGNED) {
+            // the step issued is a whole one of this tile
+            const int main_steps = here.k_len / kStep - (S - 1);
+#pragma unroll 1
+            for (; step < main_steps; ++step) {
+                arrive();
+                issue_whole();
+                if (step == 0) load_epilogue();     // with the next step's loads: waited for with them
+                compute();
             }
         }
-    } else {
-        // columns of this lane's pair of 4-value groups, and of its 8 stored values
-        constexpr int kPairs = kGated ? 1 : 2;
-        const int width = kGated ? p.half : p.n;            // columns of out (and extra)
-        const int nw = n0 + wn * (kGated ? 32 : 64);
-        float bias[4][4], bscale[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = nw + (kGated ? (j & 1) : j) * 16 + q * 4 + e;
-                const int b = kGated && j >= 2 ? c + p.half : c;
-                bias[j][e] = p.bias && c < width ? to_f32<DT>(static_cast<const uint16_t*>(p.bias)[b]) : 0.f;
-                if (E4M3) bscale[j][e] = c < width ? p.b_scale[b] : 0.f;
+#pragma unroll 1
+        for (; step < here.steps; ++step) {
+            if (!ALIGNED || over) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            } else {
+                arrive();
             }
+            if (kHasExtra && step > 0) {
+                // The compiler's wait for them belongs here, before the next
+                // tile's loads go out: it does not count those.
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int64_t row = row_base + i * 16;
-            const bool row_ok = row < p.m;
-            if (E4M3) {
-                const float as = row_ok ? p.a_scale[row] : 0.f;
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= as * bscale[j][e];
+                    for (int h = 0; h < kPairs; ++h) asm volatile("" : "+v"(extra[i][h]));
             }
+            if (!over) over = !issue();
+            if (step == 0) load_epilogue();
+            compute();
+        }
+
+        // ---- epilogue: acc[i][j] holds row 16 i + r, columns 16 j + 4 q .. + 3 ----
+        if constexpr (EPI == kEpiPartial) {
+            float* part = p.part + (int64_t)here.split * (p.m + p.colsum) * p.n;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                const int col = here.n0 + wn * 64 + j * 16 + q * 4;
+                if (col >= p.n) continue;
+                const bool whole = col + 4 <= p.n && (p.n & 3) == 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] += bias[j][e];
-#pragma unroll
-            for (int h = 0; h < kPairs; ++h) {
-                const int col = nw + h * 32 + (q & 1) * 16 + (q >> 1) * 8;   // 8 values stored
-                const bool whole = row_ok && p.vec_o && col + 8 <= width;
-                // extra's 8 values, then exchanged to the accumulators' order
-                float ex[2][4];
-                if (EPI == kEpiSlope || EPI == kEpiGatedSlope || (EPI == kEpiStore && p.extra)) {
-                    u32x4 x = {0u, 0u, 0u, 0u};
-                    const uint16_t* e0 = static_cast<const uint16_t*>(p.extra) + row * p.ld_extra + col;
+                for (int i = 0; i <= MT; ++i) {
+                    const bool is_sum = i == MT;
+                    const int row = is_sum ? p.m : row_base + i * 16;
+                    if (is_sum ? !(colsum && r == 0) : row >= p.m) continue;
+                    const f32x4 v = is_sum ? sum[j] : acc[i < MT ? i : 0][j];
+                    float* o = part + (int64_t)row * p.n + col;
                     if (whole) {
-                        x = *reinterpret_cast<const u32x4*>(e0);
-                    } else if (row_ok) {
-                        uint32_t v[8];
+                        *reinterpret_cast<f32x4*>(o) = v;
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = col + e < width ? e0[e] : 0u;
-                        x = (u32x4){v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16),
-                                    v[6] | (v[7] << 16)};
+                        for (int e = 0; e < 4; ++e)
+                            if (col + e < p.n) o[e] = v[e];
                     }
-                    uint32_t l0 = x.x, l1 = x.y, h0 = x.z, h1 = x.w;
-                    swap_rows(l0, h0);
-                    swap_rows(l1, h1);
-                    ex[0][0] = to_f32<DT>(l0 & 0xffffu); ex[0][1] = to_f32<DT>(l0 >> 16);
-                    ex[0][2] = to_f32<DT>(l1 & 0xffffu); ex[0][3] = to_f32<DT>(l1 >> 16);
-                    ex[1][0] = to_f32<DT>(h0 & 0xffffu); ex[1][1] = to_f32<DT>(h0 >> 16);
-                    ex[1][2] = to_f32<DT>(h1 & 0xffffu); ex[1][3] = to_f32<DT>(h1 >> 16);
+                }
+            }
+        } else {
+            if (E4M3 || p.bias) {
+                if (here.steps == 1) __syncthreads();       // else a later step's barrier has shown the table
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int v = wn * 64 + j * 16 + q * 4;
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(&s_columns.bias[v]);
+                    if constexpr (E4M3) {
+                        const f32x4 sc = *reinterpret_cast<const f32x4*>(&s_columns.scale[v]);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) acc[i][j] = acc[i][j] * (ascale[i] * sc) + b;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) acc[i][j] += b;
+                    }
+                }
+            }
+            with_act(p.act, [&](auto act_c) SMC_INLINE {
+                constexpr int ACT = decltype(act_c)::value;
+                if (EPI == kEpiStore && !p.extra) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        row_values<DT, EPI, ACT, false>(acc[i], extra[i]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ex[e >> 2][e & 3] = 0.f;
+                    for (int i = 0; i < MT; ++i)
+                        row_values<DT, EPI, ACT, kHasExtra>(acc[i], extra[i]);
                 }
-                float v[2][2][4];                   // [output part][group][value]
+            });
+            // in a full tile as many stores as the waits above rely on
+            const bool full = p.vec_o && here.m0 + T::BM <= p.m &&
+                              here.n0 + (kGated ? T::BN / 2 : T::BN) <= width;
+            if (full) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int i = 0; i < MT; ++i) row_store<DT, EPI, true>(p, acc[i], row_base + i * 16, nw, q, width);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float z = acc[i][h * 2 + g][e];
-                        if (EPI == kEpiStore) {
-                            v[0][g][e] = act_value(z, p.act) + ex[g][e];
-                        } else if (EPI == kEpiSlope) {
-                            v[0][g][e] = ex[g][e] * act_slope(z, p.act);
-                        } else {
-                            const float u = acc[i][2 + g][e];
-                            if (EPI == kEpiGated) {
-                                v[0][g][e] = act_value(z, p.act) * u;
-                            } else {
-                                v[0][g][e] = ex[g][e] * u * act_slope(z, p.act);
-                                v[1][g][e] = ex[g][e] * act_value(z, p.act);
-                            }
-                        }
-                    }
-#pragma unroll
-                for (int o = 0; o < (EPI == kEpiGatedSlope ? 2 : 1); ++o) {
-                    uint32_t l0 = pack2<DT>(v[o][0][0], v[o][0][1]), l1 = pack2<DT>(v[o][0][2], v[o][0][3]);
-                    uint32_t h0 = pack2<DT>(v[o][1][0], v[o][1][1]), h1 = pack2<DT>(v[o][1][2], v[o][1][3]);
-                    swap_rows(l0, h0);
-                    swap_rows(l1, h1);
-                    uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.ldo + col + (o ? p.half : 0);
-                    if (whole) {
-                        *reinterpret_cast<u32x4*>(dst) = (u32x4){l0, l1, h0, h1};
-                    } else if (row_ok) {
-                        const uint32_t w[4] = {l0, l1, h0, h1};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (col + e < width) dst[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
-                    }
-                }
+                for (int i = 0; i < MT; ++i) row_store<DT, EPI, false>(p, acc[i], row_base + i * 16, nw, q, width);
             }
+            after_stores = full ? S - 1 : 0;
         }
+        if (here.t + t_step >= t_end) return;
     }
 }
 
@@ -546,10 +867,12 @@ hipError_t allow_lds(K kernel, size_t bytes) {
 }
 
 template <int DT, bool E4M3, int LA, int LB, int EPI, class T, bool ALIGNED>
-hipError_t launch_aligned(const ProductArgs& p, unsigned blocks, hipStream_t s) {
+hipError_t launch_aligned(const ProductArgs& p, int64_t total, hipStream_t s) {
     static const hipError_t ok = allow_lds(k_product<DT, E4M3, LA, LB, EPI, T, ALIGNED>, T::kLdsBytes);
     if (ok != hipSuccess) return ok;
-    launch(k_product<DT, E4M3, LA, LB, EPI, T, ALIGNED>, dim3(blocks), dim3(T::kThreads), T::kLdsBytes, s, p);
+    const int64_t resident = (int64_t)T::kBlocks * device_cus();    // each walks several tiles
+    launch(k_product<DT, E4M3, LA, LB, EPI, T, ALIGNED>, dim3((unsigned)(total < resident ? total : resident)),
+           dim3(T::kThreads), T::kLdsBytes, s, p);
     return hipGetLastError();
 }
 
@@ -561,13 +884,23 @@ hipError_t launch_product(ProductArgs p, hipStream_t s) {
     const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     if (total <= 0) return hipSuccess;
     if (total > 0x7fffffff) return hipErrorInvalidValue;
-    if (p.vec_a && p.vec_b) return launch_aligned<DT, E4M3, LA, LB, EPI, T, true>(p, (unsigned)total, s);
-    return launch_aligned<DT, E4M3, LA, LB, EPI, T, false>(p, (unsigned)total, s);
+    // row tiles a group: 1 MiB of a at most, a quarter of an XCD's L2 (columns
+    // fastest over single row tiles, b was read from memory again for nearly
+    // every row tile: 15,000 x 512 -> 4096 backward 380 MB of fetches)
+    p.group_log = 0;
+    while (p.group_log < 6 && ((int64_t)T::BM * p.k * (E4M3 ? 1 : 2) << (p.group_log + 1)) <= (1 << 20))
+        ++p.group_log;
+    if (EPI == kEpiPartial) p.group_log = 0;
+    if (p.vec_a && p.vec_b) return launch_aligned<DT, E4M3, LA, LB, EPI, T, true>(p, total, s);
+    if constexpr (T::kUnaligned) return launch_aligned<DT, E4M3, LA, LB, EPI, T, false>(p, total, s);
+    return hipErrorInvalidValue;                    // (launch_tiled picks a tile that takes them)
 }
 
-typedef Tile<256, 256, 2, 4, 2, 1> TileLarge;
-typedef Tile<128, 128, 2, 2, 2, 2> TileMid;
-typedef Tile<32, 64, 2, 1, 2, 4> TileSmall;
+typedef Tile<128, 128, 2, 2, 2, 2> TileMid;     // 64 x 64 a wave
+typedef Tile<128, 128, 4, 2, 2, 2> TileWide;    // 32 x 64 a wave, twice the waves
+typedef Tile<64, 128, 2, 2, 2, 3> TileRows;     // three blocks a CU
+typedef Tile<32, 64, 2, 1, 3, 4, true> TileSmall;
+typedef Tile<128, 128, 2, 2, 2, 2, true> TileWeight;    // x^T dz
 
 }  // namespace
 }  // namespace smc

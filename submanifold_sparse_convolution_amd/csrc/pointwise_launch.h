@@ -13,15 +13,24 @@ hipError_t launch_slope_16(const ProductArgs& p, int dt, hipStream_t s);
 hipError_t launch_gated_slope_16(const ProductArgs& p, int dt, hipStream_t s);
 hipError_t launch_store_e4m3(const ProductArgs& p, int dt, bool along, hipStream_t s);
 hipError_t launch_gated_e4m3(const ProductArgs& p, int dt, bool along, hipStream_t s);
+// Up to kFewRows rows (kEpiStore, kEpiGated; 16-bit operands).
+constexpr int kFewRows = 8;
+hipError_t launch_few_rows(const ProductArgs& p, Epilogue epi, int dt, hipStream_t s);
 
 namespace {
 
 template <int DT, bool E4M3, int LA, int LB, int EPI>
 hipError_t launch_tiled(const ProductArgs& p, hipStream_t s) {
-    const int64_t cus = device_cus();
-    const int64_t mid = ((p.m + 127) / 128) * ((p.n + 127) / 128) * p.splits;
-    if (mid >= cus) return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
-    return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
+    constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
+    // Half the CUs without a 128 x 128 tile: small tiles (33 x 512 -> 1365: ... us).
+    const int64_t mid = ((p.m + 127) / 128) * ((p.n + 127) / 128);
+    if (!(p.vec_a && p.vec_b) || mid < device_cus() / 2)
+        return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
+    if constexpr (kGated) return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
+    else {
+        if (p.n <= 128) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
+        return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
+    }
 }
 
 }  // namespace
