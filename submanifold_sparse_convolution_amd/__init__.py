@@ -484,77 +484,71 @@ ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 def _dtype_code(t, name):
     import torch
-    code = {torch.bfloat16: 0, torch.float16: 1}.get(t.dtype if isinstance(t, torch.Tensor) else t)
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16 or float16")
-    return code
+    dtype = t.dtype if isinstance(t, torch.Tensor) else t
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float16:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
+
+
+def _of(t, name, dtype, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _rows(t, name, dtype, device, shape=None):
     """A 2-D CUDA tensor's (address, row distance in elements): the elements of
     a row must be adjacent, rows may lie any distance apart without overlap."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    _of(t, name, dtype, device)
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{name} must be {list(shape) if shape else '2-dimensional'}, "
-                         f"got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    n, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+                         f"got {list(size)}")
+    n, c = size
+    ld, step = t.stride()
+    if c > 1 and step != 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
-    ld = t.stride(0) if n > 1 else c
-    if ld < c:
+    if n <= 1:
+        ld = c
+    elif ld < c:
         raise ValueError(f"{name}: rows overlap (row distance {ld} < {c})")
     return t.data_ptr(), ld
 
 
 def _vector(t, name, dtype, device, size):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != size or (size > 1 and t.stride(0) != 1):
+    _of(t, name, dtype, device)
+    if t.shape != (size,) or (size > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous [{size}], got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
     return t.data_ptr()
 
 
-class _Launch:
-    """The device and stream of a call: outputs and scratch memory allocated
-    inside belong to the stream that runs the kernels."""
+def _elsewhere(x, stream):
+    """None where a call runs as it stands, on x's device and its current
+    stream; else the context to run it in, so that outputs and scratch memory
+    belong to the stream that runs the kernels."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA (HIP) torch tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-dimensional, got {list(x.shape)}")
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, x on {x.device}")
+        return torch.cuda.stream(stream)                    # switches the device too
+    if torch._C._cuda_getDevice() != x.device.index:
+        return torch.cuda.device(x.device.index)
+    return None
 
-    def __init__(self, x, stream):
-        import torch
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise TypeError("x must be a CUDA (HIP) torch tensor")
-        if x.dim() != 2:
-            raise ValueError(f"x must be 2-dimensional, got {list(x.shape)}")
-        self._ctx = []
-        index = x.device.index
-        if stream is not None:
-            if stream.device != x.device:
-                raise ValueError(f"stream is on {stream.device}, x on {x.device}")
-            self._ctx.append(torch.cuda.stream(stream))     # switches the device too
-            self.raw = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != index:
-                self._ctx.append(torch.cuda.device(index))
-            self.raw = torch.cuda.current_stream(index).cuda_stream
 
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
+def _raw_stream(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, e4m3: bool = False, stream=None):
@@ -565,22 +559,25 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, e4m3: bool = False, st
     (q, scale) in y's place, q float8_e4m3fn [N, C] and scale float32 [N] with
     y = q * scale[:, None], as linear and gated take them."""
     import torch
-    with _Launch(x, stream) as on:
-        dev, dt = x.device, x.dtype
-        code = _dtype_code(x, "x")
-        n, c = x.shape
-        xp, ldx = _rows(x, "x", dt, dev)
-        rp, ldr, s = None, 0, None
-        wp = _vector(weight, "weight", dt, dev, c)
-        if residual is not None:
-            rp, ldr = _rows(residual, "residual", dt, dev, (n, c))
-            s = torch.empty((n, c), dtype=dt, device=dev)
-        y = torch.empty((n, c), dtype=torch.float8_e4m3fn if e4m3 else dt, device=dev)
-        scale = torch.empty(n, dtype=torch.float32, device=dev) if e4m3 else None
-        _check(lib().smc_rms_norm(NormArgs(
-            n, c, code, eps, xp, ldx, rp, ldr, wp, y.data_ptr(), c,
-            scale.data_ptr() if e4m3 and n else None, s.data_ptr() if s is not None else None, c),
-            on.raw))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return rms_norm(x, weight, residual, eps, e4m3)
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x, "x")
+    n, c = x.shape
+    xp, ldx = _rows(x, "x", dt, dev)
+    rp, ldr, s = None, 0, None
+    wp = _vector(weight, "weight", dt, dev, c)
+    if residual is not None:
+        rp, ldr = _rows(residual, "residual", dt, dev, (n, c))
+        s = torch.empty((n, c), dtype=dt, device=dev)
+    y = torch.empty((n, c), dtype=torch.float8_e4m3fn if e4m3 else dt, device=dev)
+    scale = torch.empty(n, dtype=torch.float32, device=dev) if e4m3 else None
+    _check(lib().smc_rms_norm(NormArgs(
+        n, c, code, eps, xp, ldx, rp, ldr, wp, y.data_ptr(), c,
+        scale.data_ptr() if e4m3 and n else None, s.data_ptr() if s is not None else None, c),
+        _raw_stream(dev)))
     out = ((y, scale) if e4m3 else (y,)) + ((s,) if s is not None else ())
     return out if len(out) > 1 else y
 
@@ -590,21 +587,25 @@ def rms_norm_backward(dy, s, weight, eps: float = 1e-6, ds=None, stream=None):
     (rms_norm's s, or x without a residual); ds: the gradient that reaches s by
     other paths, added to dx. dx is the gradient of x and of the residual."""
     import torch
-    with _Launch(s, stream) as on:
-        dev, dt = s.device, s.dtype
-        code = _dtype_code(s, "s")
-        n, c = s.shape
-        sp, lds = _rows(s, "s", dt, dev)
-        dyp, lddy = _rows(dy, "dy", dt, dev, (n, c))
-        wp = _vector(weight, "weight", dt, dev, c)
-        dsp, ldds = _rows(ds, "ds", dt, dev, (n, c)) if ds is not None else (None, 0)
-        L = lib()
-        dx = torch.empty((n, c), dtype=dt, device=dev)
-        dweight = torch.empty(c, dtype=dt, device=dev)
-        ws = torch.empty(L.smc_rms_norm_backward_workspace(n, c), dtype=torch.uint8, device=dev)
-        _check(L.smc_rms_norm_backward(NormBackwardArgs(
-            n, c, code, eps, dyp, lddy, sp, lds, wp, dsp, ldds, dx.data_ptr(), c,
-            dweight.data_ptr(), ws.data_ptr(), ws.numel()), on.raw))
+    ctx = _elsewhere(s, stream)
+    if ctx is not None:
+        with ctx:
+            return rms_norm_backward(dy, s, weight, eps, ds)
+    dev, dt = s.device, s.dtype
+    code = _dtype_code(s, "s")
+    n, c = s.shape
+    sp, lds = _rows(s, "s", dt, dev)
+    dyp, lddy = _rows(dy, "dy", dt, dev, (n, c))
+    wp = _vector(weight, "weight", dt, dev, c)
+    dsp, ldds = _rows(ds, "ds", dt, dev, (n, c)) if ds is not None else (None, 0)
+    L = lib()
+    dx = torch.empty((n, c), dtype=dt, device=dev)
+    dweight = torch.empty(c, dtype=dt, device=dev)
+    nbytes = L.smc_rms_norm_backward_workspace(n, c)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(L.smc_rms_norm_backward(NormBackwardArgs(
+        n, c, code, eps, dyp, lddy, sp, lds, wp, dsp, ldds, dx.data_ptr(), c,
+        dweight.data_ptr(), ws.data_ptr(), nbytes), _raw_stream(dev)))
     return dx, dweight
 
 
@@ -615,7 +616,7 @@ def _activation(name):
 
 
 def _product_args(halves, x, w, bias, activation, x_scale, w_scale, dtype, backward=False):
-    """(args with the shared fields, output dtype, c_out) of a linear or gated layer."""
+    """(args with the shared fields, output dtype, output shape) of a linear or gated layer."""
     import torch
     act = _activation(activation)
     dev = x.device
@@ -640,7 +641,17 @@ def _product_args(halves, x, w, bias, activation, x_scale, w_scale, dtype, backw
         wsp = _vector(w_scale, "w_scale", torch.float32, dev, wide)
     bp = _vector(bias, "bias", dt, dev, wide) if bias is not None else None
     return ProductArgs(n, c_in, wide // halves, code, 2 if e4m3 else code, act, xp, ldx, xsp, wp, ldw,
-                       along, wsp, bp), dt, wide // halves
+                       along, wsp, bp), dt, (n, wide // halves)
+
+
+def _product_out(a, out, dt, device, shape):
+    if out is None:
+        import torch
+        out = torch.empty(shape, dtype=dt, device=device)
+        a.y, a.ldy = out.data_ptr(), shape[1]
+    else:
+        a.y, a.ldy = _rows(out, "out", dt, device, shape)
+    return out
 
 
 def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scale=None, dtype=None,
@@ -653,16 +664,15 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     (rms_norm's e4m3 output), w float8_e4m3fn [C_out, C_in] with w_scale [C_out]
     (quantize_weight; its transpose's memory order is taken too), y of `dtype`
     (default bf16). out may be the residual."""
-    import torch
-    with _Launch(x, stream) as on:
-        a, dt, c_out = _product_args(1, x, w, bias, activation, x_scale, w_scale, dtype)
-        shape = (x.shape[0], c_out)
-        if residual is not None:
-            a.residual, a.ld_residual = _rows(residual, "residual", dt, x.device, shape)
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=x.device)
-        a.y, a.ldy = _rows(out, "out", dt, x.device, shape)
-        _check(lib().smc_linear(a, on.raw))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return linear(x, w, bias, residual, activation, x_scale, w_scale, dtype, out)
+    a, dt, shape = _product_args(1, x, w, bias, activation, x_scale, w_scale, dtype)
+    if residual is not None:
+        a.residual, a.ld_residual = _rows(residual, "residual", dt, x.device, shape)
+    out = _product_out(a, out, dt, x.device, shape)
+    _check(lib().smc_linear(a, _raw_stream(x.device)))
     return out
 
 
@@ -671,34 +681,37 @@ def gated(x, w, bias=None, activation="silu", x_scale=None, w_scale=None, dtype=
     """h = activation(x @ wg + bias_g) * (x @ wu + bias_u) in one kernel, with
     w = [wg | wu] [C_in, 2 C_out] and bias [2 C_out]. Types and the 8-bit form
     as in linear (e4m3 w: [2 C_out, C_in], the gate's rows first)."""
-    import torch
-    with _Launch(x, stream) as on:
-        a, dt, c_out = _product_args(2, x, w, bias, activation, x_scale, w_scale, dtype)
-        shape = (x.shape[0], c_out)
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=x.device)
-        a.y, a.ldy = _rows(out, "out", dt, x.device, shape)
-        _check(lib().smc_gated(a, on.raw))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return gated(x, w, bias, activation, x_scale, w_scale, dtype, out)
+    a, dt, shape = _product_args(2, x, w, bias, activation, x_scale, w_scale, dtype)
+    out = _product_out(a, out, dt, x.device, shape)
+    _check(lib().smc_gated(a, _raw_stream(x.device)))
     return out
 
 
 def _product_backward(halves, dy, x, w, bias, activation, stream):
     import torch
-    with _Launch(x, stream) as on:
-        a, dt, c_out = _product_args(halves, x, w, bias, activation, None, None, None, True)
-        n, c_in = x.shape
-        a.dy, a.ld_dy = _rows(dy, "dy", dt, x.device, (n, c_out))
-        dx = torch.empty((n, c_in), dtype=dt, device=x.device)
-        dw = torch.empty((c_in, c_out * halves), dtype=dt, device=x.device)
-        db = torch.empty(c_out * halves, dtype=dt, device=x.device) if bias is not None else None
-        a.dx, a.ld_dx, a.dw, a.ld_dw = dx.data_ptr(), c_in, dw.data_ptr(), c_out * halves
-        a.db = db.data_ptr() if db is not None else None
-        L = lib()
-        need, call = ((L.smc_linear_backward_workspace, L.smc_linear_backward) if halves == 1 else
-                      (L.smc_gated_backward_workspace, L.smc_gated_backward))
-        ws = torch.empty(need(a), dtype=torch.uint8, device=x.device)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-        _check(call(a, on.raw))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return _product_backward(halves, dy, x, w, bias, activation, None)
+    a, dt, (n, c_out) = _product_args(halves, x, w, bias, activation, None, None, None, True)
+    dev, c_in, wide = x.device, x.shape[1], c_out * halves
+    a.dy, a.ld_dy = _rows(dy, "dy", dt, dev, (n, c_out))
+    dx = torch.empty((n, c_in), dtype=dt, device=dev)
+    dw = torch.empty((c_in, wide), dtype=dt, device=dev)
+    db = torch.empty(wide, dtype=dt, device=dev) if bias is not None else None
+    a.dx, a.ld_dx, a.dw, a.ld_dw = dx.data_ptr(), c_in, dw.data_ptr(), wide
+    a.db = db.data_ptr() if db is not None else None
+    L = lib()
+    need, call = ((L.smc_linear_backward_workspace, L.smc_linear_backward) if halves == 1 else
+                  (L.smc_gated_backward_workspace, L.smc_gated_backward))
+    nbytes = need(a)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _check(call(a, _raw_stream(dev)))
     return dx, dw, db
 
 
@@ -719,14 +732,17 @@ def quantize_weight(w, stream=None):
     """bf16 or f16 w [C_in, C_out] -> (float8_e4m3fn [C_out, C_in], float32 scale
     [C_out]) for linear and gated on e4m3 rows; scale[j] = max |w[:, j]| / 448."""
     import torch
-    with _Launch(w, stream) as on:
-        code = _dtype_code(w, "w")
-        c_in, c_out = w.shape
-        wp, ldw = _rows(w, "w", w.dtype, w.device)
-        q = torch.empty((c_out, c_in), dtype=torch.float8_e4m3fn, device=w.device)
-        scale = torch.empty(c_out, dtype=torch.float32, device=w.device)
-        _check(lib().smc_weight_quantize(wp, ldw, c_in, c_out, code, q.data_ptr(), c_in,
-                                         scale.data_ptr(), on.raw))
+    ctx = _elsewhere(w, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_weight(w)
+    code = _dtype_code(w, "w")
+    c_in, c_out = w.shape
+    wp, ldw = _rows(w, "w", w.dtype, w.device)
+    q = torch.empty((c_out, c_in), dtype=torch.float8_e4m3fn, device=w.device)
+    scale = torch.empty(c_out, dtype=torch.float32, device=w.device)
+    _check(lib().smc_weight_quantize(wp, ldw, c_in, c_out, code, q.data_ptr(), c_in,
+                                     scale.data_ptr(), _raw_stream(w.device)))
     return q, scale
 
 

@@ -57,22 +57,8 @@ __device__ __forceinline__ void store_e4m3(void* p, int64_t i, const float (&v)[
     }
 }
 
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
-}
-
-// Largest magnitude by its bits, in which order NaN is above infinity: a NaN
-// anywhere in the row makes the scale NaN.
-template <int L>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    return v;
-}
-
+// From the row's largest magnitude by its bits, in which order NaN is above
+// infinity: a NaN anywhere in the row makes the scale NaN.
 __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     const float s = __uint_as_float(amax_bits) / kE4m3Max;
     return s < kTinyScale ? kTinyScale : s;        // NaN stays
@@ -110,7 +96,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
             if (ok && c < a.c) store_16<DT, W>(a.s, row * a.lds + c, v[j]);
         }
     }
-    const float rstd = 1.f / sqrtf(group_sum<L>(ss) / (float)a.c + a.eps);
+    const float rstd = 1.f / sqrtf(lane_sum<L>(ss) / (float)a.c + a.eps);
     uint32_t amax = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -126,7 +112,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
         if (!a.y_scale && ok) store_16<DT, W>(a.y, row * a.ldy + c, v[j]);
     }
     if (!a.y_scale) return;
-    const float scale = row_scale(group_max<L>(amax));
+    const float scale = row_scale(lane_max<L>(amax));
     if (ok && lane == 0) a.y_scale[row] = scale;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -139,7 +125,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
 }
 
 __device__ __forceinline__ float block_sum(float v, float* s) {
-    v = group_sum<64>(v);
+    v = lane_sum<64>(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -174,7 +160,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
     for (int pass = a.y_scale ? 0 : 1; pass < 2; ++pass) {
         float scale = 1.f;
         if (pass == 1 && a.y_scale) {
-            amax = group_max<64>(amax);
+            amax = lane_max<64>(amax);
             if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = amax;
             __syncthreads();
             scale = row_scale(max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3])));
@@ -249,8 +235,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
                 ss += x[j][e] * x[j][e];
                 dot += dy[j][e] * w[j][e] * x[j][e];
             }
-        ss = group_sum<L>(ss);
-        dot = group_sum<L>(dot);
+        ss = lane_sum<L>(ss);
+        dot = lane_sum<L>(dot);
         const float rstd = 1.f / sqrtf(ss / (float)a.c + a.eps);
         const float mean = dot * rstd / (float)a.c;        // mean(a x_hat)
 #pragma unroll

@@ -148,6 +148,46 @@ __device__ __forceinline__ void with_act(int act, F f) {
     }
 }
 
+// ---- sums and maxima over the lanes ----------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+
+// v combined over aligned groups of L lanes (1 .. 64), the result in every lane,
+// by vector instructions alone (a shuffle through the LDS unit costs more than
+// the rest of a small kernel: one row of 512 -> 1365 gated 12.0 us with them).
+// f is commutative, so lanes may be mirrored once the smaller groups are equal.
+template <int L, class F>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t v, F f) {
+    if (L >= 2) v = f(v, dpp<0xB1>(v));             // lane ^ 1
+    if (L >= 4) v = f(v, dpp<0x4E>(v));             // lane ^ 2
+    if (L >= 8) v = f(v, dpp<0x141>(v));            // mirrored in 8
+    if (L >= 16) v = f(v, dpp<0x140>(v));           // mirrored in 16
+    if (L >= 32) {
+        const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+        v = f(r.x, r.y);
+    }
+    if (L >= 64) {
+        const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+        v = f(r.x, r.y);
+    }
+    return v;
+}
+
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+    return __uint_as_float(over_lanes<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) SMC_INLINE {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t lane_max(uint32_t v) {
+    return over_lanes<L>(v, [](uint32_t a, uint32_t b) SMC_INLINE { return a > b ? a : b; });
+}
+
 // ---- staging one operand --------------------------------------------------------
 
 // 16 bytes from any element's address.
@@ -623,12 +663,26 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
     ahead.start(p, t_first, kStep);
     Place<T, EPI> here = ahead;
     enter(true, true, true);
+    // The vector memory counter is in order: the oldest step in flight has landed
+    // when no more operations are left than were issued after it. `ops` counts the
+    // operations that are certain (a step's loads, the loads of extra in words,
+    // the stores of a full tile); others only make a wait longer.
+    int ops = 0, mark[S] = {}, in_flight = 0;           // mark: ops when a step had been issued
     bool over = false;                                  // every step has been issued
+    auto issued_one = [&]() SMC_INLINE {
+        ops += T::kLoads;
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (i == in_flight) mark[i] = ops;
+        ++in_flight;
+    };
 #pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) over = !issue();
+    for (int i = 0; i < S; ++i) {
+        over = !issue();
+        if (!over) issued_one();
+    }
 
     int buf = 0;                        // byte offset of the step's buffer
-    int after_stores = 0;               // steps to come that were issued before a full tile's stores
 #pragma unroll 1
     for (;; here.advance(p, t_step, kStep)) {
         // What the epilogue reads: columns of this lane's pair of 4-value groups
@@ -742,21 +796,42 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             }
         };
 
-        // At a step's start its words have landed (all but the loads of later
-        // steps, and stores issued after them, may still be in flight), and
-        // every wave is done with the buffer that the next loads overwrite.
-        constexpr int kLater = (S - 2) * T::kLoads;
-        constexpr int kStores = MT * (EPI == kEpiGated ? 1 : 2);
+        // At a step's start its words have landed, and every wave is done with the
+        // buffer that the next loads overwrite.
         auto arrive = [&]() SMC_INLINE {
-            if (after_stores > 0)
-                wait_vm<kLater + kStores>();
+            constexpr int kSteady = (S - 2) * T::kLoads;
+            const int newer = ops - mark[0];
+            if (!ALIGNED)
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            else if (newer == kSteady)
+                wait_vm<kSteady>();
+            else if (newer >= 16)
+                wait_vm<16>();
+            else if (newer >= 12)
+                wait_vm<12>();
+            else if (newer >= 8)
+                wait_vm<8>();
+            else if (newer >= 4)
+                wait_vm<4>();
             else
-                wait_vm<kLater>();
-            --after_stores;
+                wait_vm<0>();
+#pragma unroll
+            for (int i = 0; i + 1 < S; ++i) mark[i] = mark[i + 1];
+            --in_flight;
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
         };
+        // S steps are in flight at a tile's start: its first step issues none.
+        // What the epilogue reads is loaded beside it, two steps before a wait
+        // includes it.
         int step = 0;
+        if (here.steps > 0) {
+            arrive();
+            load_epilogue();
+            if (kHasExtra && p.extra && p.vec_o) ops += MT * kPairs;
+            compute();
+            ++step;
+        }
         if constexpr (ALIGNED) {
             // the step issued is a whole one of this tile
             const int main_steps = here.k_len / kStep - (S - 1);
@@ -764,30 +839,33 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             for (; step < main_steps; ++step) {
                 arrive();
                 issue_whole();
-                if (step == 0) load_epilogue();     // with the next step's loads: waited for with them
+                issued_one();
                 compute();
             }
         }
 #pragma unroll 1
         for (; step < here.steps; ++step) {
-            if (!ALIGNED || over) {
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
-            } else {
-                arrive();
+            arrive();
+            if (!over) {
+                over = !issue();
+                if (!over) issued_one();
             }
-            if (kHasExtra && step > 0) {
-                // The compiler's wait for them belongs here, before the next
-                // tile's loads go out: it does not count those.
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < kPairs; ++h) asm volatile("" : "+v"(extra[i][h]));
-            }
-            if (!over) over = !issue();
-            if (step == 0) load_epilogue();
             compute();
+        }
+        if (kHasExtra && p.extra) {
+            // the compiler's own wait for them belongs here, before the next
+            // tile's loads, which it does not count
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < kPairs; ++h) asm volatile("" : "+v"(extra[i][h]));
+        }
+        // The last step's buffer is free once every wave has read it.
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (!over) {
+            over = !issue();
+            if (!over) issued_one();
         }
 
         // ---- epilogue: acc[i][j] holds row 16 i + r, columns 16 j + 4 q .. + 3 ----
@@ -816,7 +894,6 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             }
         } else {
             if (E4M3 || p.bias) {
-                if (here.steps == 1) __syncthreads();       // else a later step's barrier has shown the table
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int v = wn * 64 + j * 16 + q * 4;
@@ -853,7 +930,7 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
 #pragma unroll
                 for (int i = 0; i < MT; ++i) row_store<DT, EPI, false>(p, acc[i], row_base + i * 16, nw, q, width);
             }
-            after_stores = full ? S - 1 : 0;
+            if (full) ops += MT * Shape<EPI>::kOut;
         }
         if (here.t + t_step >= t_end) return;
     }

@@ -62,20 +62,45 @@ hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
 namespace {
 
 // dw[m, n] (and db[n], the row after) = the splits' float32 sums, added in
-// order and rounded once. Bound by reading them.
-template <int DT>
+// order and rounded once; W consecutive elements a thread, each split's read
+// independent of the others. Bound by reading them.
+template <int DT, int W>
 __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ part, int splits,
                                                    int64_t m, int n, int64_t rows, uint16_t* dw,
                                                    int64_t ldw, uint16_t* db) {
     const int64_t total = rows * n;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
     if (i >= total) return;
-    float v = 0.f;
-    for (int sp = 0; sp < splits; ++sp) v += part[(int64_t)sp * total + i];
+    float v[W] = {};
+#pragma unroll 4
+    for (int sp = 0; sp < splits; ++sp) {
+        const float* src = part + (int64_t)sp * total + i;
+        if constexpr (W == 4) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += u[e];
+        } else {
+            v[0] += *src;
+        }
+    }
     const int64_t row = i / n;
     const int col = (int)(i - row * n);
     uint16_t* o = row < m ? dw + row * ldw + col : db + col;
-    *o = (uint16_t)from_f32<DT>(v);
+#pragma unroll
+    for (int e = 0; e < W; ++e) o[e] = (uint16_t)from_f32<DT>(v[e]);
+}
+
+template <int DT>
+void sum_parts(const float* part, int splits, int64_t m, int n, int64_t rows, void* dw, int64_t ldw,
+               void* db, hipStream_t s) {
+    uint16_t* w = static_cast<uint16_t*>(dw);
+    uint16_t* b = static_cast<uint16_t*>(db);
+    if (n % 4 == 0)                             // a row's elements in whole 16-byte words of sums
+        launch(k_sum_parts<DT, 4>, dim3((unsigned)((rows * n + 1023) / 1024)), dim3(256), 0, s, part, splits, m,
+               n, rows, w, ldw, b);
+    else
+        launch(k_sum_parts<DT, 1>, dim3((unsigned)((rows * n + 255) / 256)), dim3(256), 0, s, part, splits, m, n,
+               rows, w, ldw, b);
 }
 
 }  // namespace
@@ -83,13 +108,10 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ par
 hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
                             void* db, int dt, hipStream_t s) {
     const int64_t rows = m + (db ? 1 : 0);
-    const unsigned blocks = (unsigned)((rows * n + 255) / 256);
     if (dt == kF16)
-        launch(k_sum_parts<kF16>, dim3(blocks), dim3(256), 0, s, part, splits, m, n, rows,
-               static_cast<uint16_t*>(dw), ldw, static_cast<uint16_t*>(db));
+        sum_parts<kF16>(part, splits, m, n, rows, dw, ldw, db, s);
     else
-        launch(k_sum_parts<kBF16>, dim3(blocks), dim3(256), 0, s, part, splits, m, n, rows,
-               static_cast<uint16_t*>(dw), ldw, static_cast<uint16_t*>(db));
+        sum_parts<kBF16>(part, splits, m, n, rows, dw, ldw, db, s);
     return hipGetLastError();
 }
 

@@ -3,29 +3,33 @@
 // launch.
 //
 // A block owns CB output columns (gated: of both halves) and the whole
-// contraction: lane l reads 8 consecutive columns of weight row k as one 16-byte
-// word (unaligned where the rows are), the block's 256 lanes cover CB columns
-// of 2048 / CB weight rows at a time, and their partial sums are added across
-// the lanes, then across the waves through LDS, in a fixed order. Few columns a
-// block give many blocks, each with few loads in turn.
+// contraction: a lane reads 8 consecutive columns of weight row k as one 16-byte
+// word (unaligned where the rows are), the block's 1024 lanes cover CB columns
+// of 8192 / CB weight rows at a time, up to four such rounds in flight, and their
+// partial sums are added across the lanes, then across the waves through LDS,
+// in a fixed order. Few columns a block give many blocks, and 1024 lanes a
+// short chain of loads in each.
 #include "pointwise_gemm.h"
 #include "pointwise_launch.h"
 
 namespace smc {
 namespace {
 
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 1024;
+constexpr int kFewWaves = kFewThreads / 64;
 
 template <int DT, int EPI, int R, int CB>
 __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
     constexpr bool kGated = EPI == kEpiGated;
     constexpr int kHalves = kGated ? 2 : 1;
-    constexpr int kWide = CB / 8;                       // lanes side by side
+    constexpr int kWide = CB / 8;                       // words side by side
+    constexpr int kLanes = 64 / kWide;                  // lanes of a wave on one word's column
     constexpr int kDeep = kFewThreads / kWide;          // weight rows at a time
-    __shared__ float s_sum[4][R][kHalves][CB];
+    constexpr int kFewRounds = R <= 2 ? 4 / R : 1;      // (registers)
+    __shared__ float s_sum[kFewWaves][R][kHalves][CB];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int width = kGated ? p.half : p.n;
-    const int c0 = blockIdx.x * CB, col = c0 + (tid % kWide) * 8;
+    const int c0 = blockIdx.x * CB, col = c0 + lane / kLanes * 8;
     const uint16_t* x = static_cast<const uint16_t*>(p.a);
     const uint16_t* w = static_cast<const uint16_t*>(p.b);
     const int cols = width - col;                       // of this lane's 8 that exist (or more)
@@ -37,44 +41,62 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[r][h][e] = 0.f;
-    if (cols > 0) {
-#pragma unroll 4
-        for (int k = tid / kWide; k < p.k; k += kDeep) {
-            float xv[R];
+    // `word` reads 8 columns of a weight row; past the last row it is read again
+    // and counted as zeros, so that a round's loads need no branches
+    auto walk = [&](auto word, auto rounds_c) SMC_INLINE {
+        constexpr int kRounds = decltype(rounds_c)::value;
+        for (int k0 = wave * kLanes + lane % kLanes; k0 < p.k; k0 += kRounds * kDeep) {
+            u32x4 v[kRounds][kHalves];
+            float xv[kRounds][R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) xv[r] = to_f32<DT>(x[(int64_t)(r < p.m ? r : 0) * p.lda + k]);
+            for (int i = 0; i < kRounds; ++i) {
+                const int k = k0 + i * kDeep, kc = k < p.k ? k : p.k - 1;
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                const uint16_t* wr = w + (int64_t)k * p.ldb + col + (h ? p.half : 0);
-                const u32x4 v = cols >= 8 ? load_unaligned(wr) : load_tail(wr, cols);
+                for (int h = 0; h < kHalves; ++h) v[i][h] = word(w + (int64_t)kc * p.ldb + col + (h ? p.half : 0));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float wv = to_f32<DT>((v[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+                for (int r = 0; r < R; ++r) xv[i][r] = to_f32<DT>(x[(int64_t)(r < p.m ? r : 0) * p.lda + kc]);
+            }
 #pragma unroll
-                    for (int r = 0; r < R; ++r) acc[r][h][e] = fmaf(xv[r], wv, acc[r][h][e]);
-                }
+            for (int i = 0; i < kRounds; ++i) {
+                if (k0 + i * kDeep >= p.k) continue;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float wv = to_f32<DT>((v[i][h][e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[r][h][e] = fmaf(xv[i][r], wv, acc[r][h][e]);
+                    }
             }
         }
-    }
+    };
+    auto words = [](const uint16_t* wr) SMC_INLINE { return load_unaligned(wr); };
+    if (cols >= 8 && p.k <= kDeep)
+        walk(words, std::integral_constant<int, 1>());
+    else if (cols >= 8)
+        walk(words, std::integral_constant<int, kFewRounds>());
+    else if (cols > 0)
+        walk([cols](const uint16_t* wr) SMC_INLINE { return load_tail(wr, cols); }, std::integral_constant<int, 1>());
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float v = acc[r][h][e];
-#pragma unroll
-                for (int o = kWide; o < 64; o <<= 1) v += __shfl_xor(v, o);
-                if (lane < kWide) s_sum[wave][r][h][lane * 8 + e] = v;
+                const float v = lane_sum<kLanes>(acc[r][h][e]);
+                if (lane % kLanes == 0) s_sum[wave][r][h][lane / kLanes * 8 + e] = v;
             }
     __syncthreads();
-    for (int i = tid; i < R * CB; i += kFewThreads) {
-        const int r = i / CB, c = i - r * CB;
-        if (r >= p.m || c0 + c >= width) continue;
+    static_assert(R * CB <= kFewThreads, "a thread an output");
+    {
+        const int r = tid / CB, c = tid - r * CB;
+        if (r >= p.m || r >= R || c0 + c >= width) return;
         float z[kHalves];
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
-            z[h] = s_sum[0][r][h][c] + s_sum[1][r][h][c] + s_sum[2][r][h][c] + s_sum[3][r][h][c];
+            z[h] = 0.f;
+#pragma unroll
+            for (int wv = 0; wv < kFewWaves; ++wv) z[h] += s_sum[wv][r][h][c];
             if (p.bias) z[h] += to_f32<DT>(static_cast<const uint16_t*>(p.bias)[c0 + c + (h ? p.half : 0)]);
         }
         float y = 0.f;
@@ -89,7 +111,10 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
 template <int DT, int EPI, int R>
 hipError_t few_t(const ProductArgs& p, hipStream_t s) {
     const int width = EPI == kEpiGated ? p.half : p.n;
-    // the widest blocks (whole 128-byte lines of a weight row) that still give 128 of them
+    // The widest blocks (whole 128-byte lines of a weight row) that still give
+    // 128 of them, else 16 columns. One row, 2048 -> 512 and gated 512 -> 1365:
+    // 8.4 and 7.3 us with 8 columns a block, 5.0 and 7.6 with 16, 7.1 and 10.3
+    // with 32, 10.7 and 11.7 with 64.
     if (width >= 128 * 64)
         launch(k_few_rows<DT, EPI, R, 64>, dim3((unsigned)((width + 63) / 64)), dim3(kFewThreads), 0, s, p);
     else if (width >= 128 * 32)
