@@ -20,40 +20,50 @@ constexpr int kNormThreads = 256;
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;      // 2^-126
 
-// W consecutive elements (8: one 16-byte word) as float32.
-template <int DT, int W>
-__device__ __forceinline__ void load_f32(const void* p, int64_t i, float (&v)[W]) {
-    if constexpr (W == 8) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+constexpr int W = 8;        // elements of a word
+
+// A word of a row as float32: elements i .. i + 7, of which `left` exist (all of
+// them where ALIGNED, which also means that the address is a multiple of 16).
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void load_f32(const void* p, int64_t i, int left, float (&v)[W]) {
+    const uint16_t* e0 = static_cast<const uint16_t*>(p) + i;
+    const u32x4 u = ALIGNED ? *reinterpret_cast<const u32x4*>(e0) : left >= W ? load_unaligned(e0) : load_tail(e0, left);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = to_f32<DT>((u[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+    for (int e = 0; e < W; ++e) v[e] = to_f32<DT>((u[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+}
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void store_16(void* p, int64_t i, int left, const float (&v)[W]) {
+    uint16_t* e0 = static_cast<uint16_t*>(p) + i;
+    const u32x4 u = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+    if (ALIGNED) {
+        *reinterpret_cast<u32x4*>(e0) = u;
+    } else if (left >= W) {
+        __builtin_memcpy(e0, &u, 16);
     } else {
-        v[0] = to_f32<DT>(static_cast<const uint16_t*>(p)[i]);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < left) e0[e] = (uint16_t)(u[e >> 1] >> ((e & 1) * 16));
     }
 }
 
-template <int DT, int W>
-__device__ __forceinline__ void store_16(void* p, int64_t i, const float (&v)[W]) {
-    if constexpr (W == 8)
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
-            (u32x4){pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
-                    pack2<DT>(v[6], v[7])};
-    else
-        static_cast<uint16_t*>(p)[i] = (uint16_t)from_f32<DT>(v[0]);
-}
-
-template <int W>
-__device__ __forceinline__ void store_e4m3(void* p, int64_t i, const float (&v)[W]) {
-    if constexpr (W == 8) {
-        u32x2 u;
+template <bool ALIGNED>
+__device__ __forceinline__ void store_e4m3(void* p, int64_t i, int left, const float (&v)[W]) {
+    uint8_t* e0 = static_cast<uint8_t*>(p) + i;
+    u32x2 u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
-            u[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w, true);
-        }
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(p) + i) = u;
+    for (int h = 0; h < 2; ++h) {
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
+        u[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w, true);
+    }
+    if (ALIGNED) {
+        *reinterpret_cast<u32x2*>(e0) = u;
+    } else if (left >= W) {
+        __builtin_memcpy(e0, &u, 8);
     } else {
-        static_cast<uint8_t*>(p)[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < left) e0[e] = (uint8_t)(u[e >> 2] >> ((e & 3) * 8));
     }
 }
 
@@ -65,7 +75,7 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
 }
 
 // L lanes a row, NV words of W elements a lane, the row in registers.
-template <int DT, int W, int L, int NV>
+template <int DT, bool A, int L, int NV>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
     const int lane = threadIdx.x % L;
     const int64_t row = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
@@ -78,10 +88,10 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < W; ++e) v[j][e] = 0.f;
         if (ok && c < a.c) {
-            load_f32<DT, W>(a.x, row * a.ldx + c, v[j]);
+            load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, v[j]);
             if (a.residual) {
                 float r[W];
-                load_f32<DT, W>(a.residual, row * a.ldr + c, r);
+                load_f32<DT, A>(a.residual, row * a.ldr + c, a.c - c, r);
 #pragma unroll
                 for (int e = 0; e < W; ++e) v[j][e] += r[e];
             }
@@ -93,7 +103,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * L + lane) * W;
-            if (ok && c < a.c) store_16<DT, W>(a.s, row * a.lds + c, v[j]);
+            if (ok && c < a.c) store_16<DT, A>(a.s, row * a.lds + c, a.c - c, v[j]);
         }
     }
     const float rstd = 1.f / sqrtf(lane_sum<L>(ss) / (float)a.c + a.eps);
@@ -103,13 +113,13 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
         const int c = (j * L + lane) * W;
         if (c >= a.c) continue;
         float w[W];
-        load_f32<DT, W>(a.weight, c, w);
+        load_f32<DT, A>(a.weight, c, a.c - c, w);
 #pragma unroll
         for (int e = 0; e < W; ++e) {
             v[j][e] = v[j][e] * rstd * w[e];
             amax = max(amax, __float_as_uint(v[j][e]) & 0x7fffffffu);
         }
-        if (!a.y_scale && ok) store_16<DT, W>(a.y, row * a.ldy + c, v[j]);
+        if (!a.y_scale && ok) store_16<DT, A>(a.y, row * a.ldy + c, a.c - c, v[j]);
     }
     if (!a.y_scale) return;
     const float scale = row_scale(lane_max<L>(amax));
@@ -120,7 +130,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
         if (!ok || c >= a.c) continue;
 #pragma unroll
         for (int e = 0; e < W; ++e) v[j][e] = v[j][e] / scale;
-        store_e4m3<W>(a.y, row * a.ldy + c, v[j]);
+        store_e4m3<A>(a.y, row * a.ldy + c, a.c - c, v[j]);
     }
 }
 
@@ -134,16 +144,16 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
 
 // Rows too wide for a wave's registers: a block a row, the row read again (from
 // the caches) for each use.
-template <int DT, int W>
+template <int DT, bool A>
 __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
     __shared__ float s_sum[4];
     __shared__ uint32_t s_max[4];
     const int64_t row = blockIdx.x;
     auto value = [&](int c, float (&v)[W]) {
-        load_f32<DT, W>(a.x, row * a.ldx + c, v);
+        load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, v);
         if (a.residual) {
             float r[W];
-            load_f32<DT, W>(a.residual, row * a.ldr + c, r);
+            load_f32<DT, A>(a.residual, row * a.ldr + c, a.c - c, r);
 #pragma unroll
             for (int e = 0; e < W; ++e) v[e] += r[e];
         }
@@ -169,8 +179,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
         for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
             float v[W], w[W];
             value(c, v);
-            load_f32<DT, W>(a.weight, c, w);
-            if (pass == 1 && a.s) store_16<DT, W>(a.s, row * a.lds + c, v);
+            load_f32<DT, A>(a.weight, c, a.c - c, w);
+            if (pass == 1 && a.s) store_16<DT, A>(a.s, row * a.lds + c, a.c - c, v);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 v[e] = v[e] * rstd * w[e];
@@ -179,15 +189,15 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
             }
             if (pass == 0) continue;
             if (a.y_scale)
-                store_e4m3<W>(a.y, row * a.ldy + c, v);
+                store_e4m3<A>(a.y, row * a.ldy + c, a.c - c, v);
             else
-                store_16<DT, W>(a.y, row * a.ldy + c, v);
+                store_16<DT, A>(a.y, row * a.ldy + c, a.c - c, v);
         }
     }
 }
 
 // dx of the rows blockIdx, + gridDim, ... and this block's sums of dy x_hat.
-template <int DT, int W, int L, int NV>
+template <int DT, bool A, int L, int NV>
 __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
     constexpr int kRows = kNormThreads / L;
     __shared__ float s_dw[L * NV * W];
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
         const int c = (j * L + lane) * W;
 #pragma unroll
         for (int e = 0; e < W; ++e) w[j][e] = dw[j][e] = 0.f;
-        if (c < a.c) load_f32<DT, W>(a.weight, c, w[j]);
+        if (c < a.c) load_f32<DT, A>(a.weight, c, a.c - c, w[j]);
     }
     const int64_t first = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
     // every lane of a wave walks the same number of rows: the sums below are
@@ -216,8 +226,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < W; ++e) x[j][e] = dy[j][e] = 0.f;
             if (ok && c < a.c) {
-                load_f32<DT, W>(a.x, row * a.ldx + c, x[j]);
-                load_f32<DT, W>(a.dy, row * a.lddy + c, dy[j]);
+                load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, x[j]);
+                load_f32<DT, A>(a.dy, row * a.lddy + c, a.c - c, dy[j]);
             }
         }
         float ds[NV][W];
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
             const int c = (j * L + lane) * W;
 #pragma unroll
             for (int e = 0; e < W; ++e) ds[j][e] = 0.f;
-            if (a.residual && ok && c < a.c) load_f32<DT, W>(a.residual, row * a.ldr + c, ds[j]);
+            if (a.residual && ok && c < a.c) load_f32<DT, A>(a.residual, row * a.ldr + c, a.c - c, ds[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -249,7 +259,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
                 o[e] = rstd * (dy[j][e] * w[j][e] - xh * mean) + ds[j][e];
                 if (ok) dw[j][e] += dy[j][e] * xh;
             }
-            if (ok && c < a.c) store_16<DT, W>(a.y, row * a.ldy + c, o);
+            if (ok && c < a.c) store_16<DT, A>(a.y, row * a.ldy + c, a.c - c, o);
         }
     }
     // the lane groups of a wave, then the waves in turn
@@ -274,7 +284,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
     for (int c = threadIdx.x; c < a.c; c += kNormThreads) a.part[(int64_t)blockIdx.x * a.c + c] = s_dw[c];
 }
 
-template <int DT, int W>
+template <int DT, bool A>
 __global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a) {
     __shared__ float s_sum[4];
     float* part = a.part + (int64_t)blockIdx.x * a.c;      // each thread its own columns
@@ -284,9 +294,9 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a)
         float ss = 0.f, dot = 0.f;
         for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
             float x[W], dy[W], w[W];
-            load_f32<DT, W>(a.x, row * a.ldx + c, x);
-            load_f32<DT, W>(a.dy, row * a.lddy + c, dy);
-            load_f32<DT, W>(a.weight, c, w);
+            load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, x);
+            load_f32<DT, A>(a.dy, row * a.lddy + c, a.c - c, dy);
+            load_f32<DT, A>(a.weight, c, a.c - c, w);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 ss += x[e] * x[e];
@@ -297,19 +307,19 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a)
         const float mean = block_sum(dot, s_sum) * rstd / (float)a.c;
         for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
             float x[W], dy[W], w[W], o[W], ds[W];
-            load_f32<DT, W>(a.x, row * a.ldx + c, x);
-            load_f32<DT, W>(a.dy, row * a.lddy + c, dy);
-            load_f32<DT, W>(a.weight, c, w);
+            load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, x);
+            load_f32<DT, A>(a.dy, row * a.lddy + c, a.c - c, dy);
+            load_f32<DT, A>(a.weight, c, a.c - c, w);
 #pragma unroll
             for (int e = 0; e < W; ++e) ds[e] = 0.f;
-            if (a.residual) load_f32<DT, W>(a.residual, row * a.ldr + c, ds);
+            if (a.residual) load_f32<DT, A>(a.residual, row * a.ldr + c, a.c - c, ds);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 const float xh = x[e] * rstd;
                 o[e] = rstd * (dy[e] * w[e] - xh * mean) + ds[e];
-                part[c + e] += dy[e] * xh;
+                if (c + e < a.c) part[c + e] += dy[e] * xh;
             }
-            store_16<DT, W>(a.y, row * a.ldy + c, o);
+            store_16<DT, A>(a.y, row * a.ldy + c, a.c - c, o);
         }
     }
 }
@@ -373,56 +383,53 @@ __global__ __launch_bounds__(256) void k_quantize_weight(const uint16_t* __restr
 }
 
 // Lanes and words a row for c channels: the fewest lanes that hold the row in
-// one word each, up to a wave; wider rows take more words a lane, up to 8
-// words of 8 (4096 channels) or 16 single elements (1024).
-template <template <int, int, int, int> class K, int DT>
-bool by_shape(int c, int vec, const NormArgs& a, hipStream_t s) {
-    if (vec) {
-        const int words = (c + 7) / 8;
-        if (words <= 1) K<DT, 8, 1, 1>::go(a, s);
-        else if (words <= 2) K<DT, 8, 2, 1>::go(a, s);
-        else if (words <= 4) K<DT, 8, 4, 1>::go(a, s);
-        else if (words <= 8) K<DT, 8, 8, 1>::go(a, s);
-        else if (words <= 16) K<DT, 8, 16, 1>::go(a, s);
-        else if (words <= 32) K<DT, 8, 32, 1>::go(a, s);
-        else if (words <= 64) K<DT, 8, 64, 1>::go(a, s);
-        else if (words <= 128) K<DT, 8, 64, 2>::go(a, s);
-        else if (words <= 256) K<DT, 8, 64, 4>::go(a, s);
-        else if (words <= 512) K<DT, 8, 64, 8>::go(a, s);
-        else return false;
-        return true;
-    }
-    if (c <= 16) K<DT, 1, 16, 1>::go(a, s);
-    else if (c <= 64) K<DT, 1, 64, 1>::go(a, s);
-    else if (c <= 256) K<DT, 1, 64, 4>::go(a, s);
-    else if (c <= 1024) K<DT, 1, 64, 16>::go(a, s);
+// one word each, up to a wave; wider rows take up to 8 words a lane (4096
+// channels).
+template <template <int, bool, int, int> class K, int DT, bool A>
+bool by_shape(const NormArgs& a, hipStream_t s) {
+    const int words = (a.c + W - 1) / W;
+    if (words <= 1) K<DT, A, 1, 1>::go(a, s);
+    else if (words <= 2) K<DT, A, 2, 1>::go(a, s);
+    else if (words <= 4) K<DT, A, 4, 1>::go(a, s);
+    else if (words <= 8) K<DT, A, 8, 1>::go(a, s);
+    else if (words <= 16) K<DT, A, 16, 1>::go(a, s);
+    else if (words <= 32) K<DT, A, 32, 1>::go(a, s);
+    else if (words <= 64) K<DT, A, 64, 1>::go(a, s);
+    else if (words <= 128) K<DT, A, 64, 2>::go(a, s);
+    else if (words <= 256) K<DT, A, 64, 4>::go(a, s);
+    else if (words <= 512) K<DT, A, 64, 8>::go(a, s);
     else return false;
     return true;
 }
 
-template <int DT, int W, int L, int NV>
+template <template <int, bool, int, int> class K, int DT>
+bool by_shape(const NormArgs& a, hipStream_t s) {
+    return a.vec ? by_shape<K, DT, true>(a, s) : by_shape<K, DT, false>(a, s);
+}
+
+template <int DT, bool A, int L, int NV>
 struct Forward {
     static void go(const NormArgs& a, hipStream_t s) {
         constexpr int kRows = kNormThreads / L;
-        launch(k_norm<DT, W, L, NV>, dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kNormThreads), 0, s, a);
+        launch(k_norm<DT, A, L, NV>, dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kNormThreads), 0, s, a);
     }
 };
 
-template <int DT, int W, int L, int NV>
+template <int DT, bool A, int L, int NV>
 struct Backward {
     static void go(const NormArgs& a, hipStream_t s) {
-        launch(k_norm_backward<DT, W, L, NV>, dim3((unsigned)norm_backward_blocks(a.n, a.c)),
+        launch(k_norm_backward<DT, A, L, NV>, dim3((unsigned)norm_backward_blocks(a.n, a.c)),
                dim3(kNormThreads), 0, s, a);
     }
 };
 
 template <int DT>
 hipError_t norm_t(const NormArgs& a, hipStream_t s) {
-    if (!by_shape<Forward, DT>(a.c, a.vec, a, s)) {
+    if (!by_shape<Forward, DT>(a, s)) {
         if (a.vec)
-            launch(k_norm_wide<DT, 8>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_wide<DT, true>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
         else
-            launch(k_norm_wide<DT, 1>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_wide<DT, false>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
     }
     return hipGetLastError();
 }
@@ -430,11 +437,11 @@ hipError_t norm_t(const NormArgs& a, hipStream_t s) {
 template <int DT>
 hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
     const int blocks = norm_backward_blocks(a.n, a.c);
-    if (blocks > 0 && !by_shape<Backward, DT>(a.c, a.vec, a, s)) {
+    if (blocks > 0 && !by_shape<Backward, DT>(a, s)) {
         if (a.vec)
-            launch(k_norm_backward_wide<DT, 8>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_backward_wide<DT, true>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
         else
-            launch(k_norm_backward_wide<DT, 1>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_backward_wide<DT, false>, dim3((unsigned)blocks), dim3(kNormThreads), 0, s, a);
     }
     launch(k_norm_weight_sum<DT>, dim3((unsigned)((a.c + 7) / 8)), dim3(1024), 0, s, a.part, blocks,
            a.c, static_cast<uint16_t*>(a.dweight));

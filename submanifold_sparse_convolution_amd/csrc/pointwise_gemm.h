@@ -289,43 +289,44 @@ struct Stager {
 
     // The same step through registers, for operands whose rows are not made of
     // 16-byte words: unaligned words, and element by element at the row ends.
-    __device__ void load_elements(const char* base, uint32_t bytes, int k_left, int tid, char* lds,
-                                  int row0, int count, int half) const {
-#pragma unroll 1
-        for (int i = 0; i < kLoads; ++i) {
-            const int id = i * THREADS + tid;
-            uint32_t o = off[0];                // selected without a register array index
+    // Every load goes out before the first is waited for.
+    __device__ __forceinline__ void fetch(const char* base, uint32_t bytes, int k_left, int tid, int row0,
+                                          int count, int half, u32x4 (&w)[kLoads]) const {
+        int left[kLoads];                           // elements of the words that exist
 #pragma unroll
-            for (int j = 1; j < kLoads; ++j) o = i == j ? off[j] : o;
-            int left;                           // elements of this word that exist
+        for (int i = 0; i < kLoads; ++i) {
             if (LAYOUT == kAlongK) {
-                left = k_left - (int)src;
+                left[i] = k_left - (int)src;
             } else {
                 int k, v;
-                across_word(id, k, v);
-                left = k < k_left ? (GATED ? half - (row0 + (v >> 6) * 32 + (v & 31)) : count - row0 - v) : 0;
+                across_word(i * THREADS + tid, k, v);
+                left[i] = k >= k_left ? 0 : GATED ? half - (row0 + (v >> 6) * 32 + (v & 31)) : count - row0 - v;
             }
-            if (o == kOutside) left = 0;
-            u32x4 w;
-            if (left >= kPer16 && o + 16 <= bytes) {
-                w = load_unaligned(base + o);
-            } else
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                uint32_t u = 0;
-#pragma unroll
-                for (int e = 0; e < 4 / ESIZE; ++e) {
-                    const int el = d * (4 / ESIZE) + e;
-                    const uint32_t at = o + el * ESIZE;
-                    if (el < left && at + ESIZE <= bytes)
-                        u |= (ESIZE == 2 ? (uint32_t)*reinterpret_cast<const uint16_t*>(base + at)
-                                         : (uint32_t)*reinterpret_cast<const uint8_t*>(base + at))
-                             << (8 * ESIZE * e);
-                }
-                w[d] = u;
-            }
-            *reinterpret_cast<u32x4*>(lds + id * 16) = w;
+            if (off[i] == kOutside || off[i] + (LAYOUT == kAlongK ? ESIZE : 0) > bytes) left[i] = 0;
+            w[i] = (u32x4){0u, 0u, 0u, 0u};
+            if (left[i] >= kPer16 && off[i] + 16 <= bytes) w[i] = load_unaligned(base + off[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if (left[i] <= 0 || (left[i] >= kPer16 && off[i] + 16 <= bytes)) continue;
+#pragma unroll 1
+            for (int e = 0; e < kPer16 && e < left[i]; ++e) {
+                const uint32_t at = off[i] + e * ESIZE;
+                if (at + ESIZE > bytes) break;
+                const uint32_t v = ESIZE == 2 ? (uint32_t)*reinterpret_cast<const uint16_t*>(base + at)
+                                              : (uint32_t)*reinterpret_cast<const uint8_t*>(base + at);
+                const int d = e / (4 / ESIZE);
+                const uint32_t placed = v << (8 * ESIZE * (e % (4 / ESIZE)));
+                w[i].x |= d == 0 ? placed : 0u;
+                w[i].y |= d == 1 ? placed : 0u;
+                w[i].z |= d == 2 ? placed : 0u;
+                w[i].w |= d == 3 ? placed : 0u;
+            }
+        }
+    }
+    __device__ __forceinline__ void commit(char* lds, int tid, const u32x4 (&w)[kLoads]) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(lds + (i * THREADS + tid) * 16) = w[i];
     }
 };
 
@@ -593,6 +594,7 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
     Stager<T::BM, LA, T::kThreads, ESIZE, false> sa;
     Stager<T::BN, LB, T::kThreads, ESIZE, kGated> sb;
     const char *next_a, *next_b;        // first element of the next step
+    const char *end_a = nullptr, *end_b = nullptr;      // along k: the end of the tile's rows
     uint32_t bytes_a, bytes_b;          // from there to the operand's end (for a whole step)
     int ahead_step = 0;
     int ahead_buf = 0;                  // byte offset of the buffer it goes to
@@ -615,6 +617,8 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
                  (LA == kAlongK ? (int64_t)ahead.m0 * p.lda + ahead.k0 : (int64_t)ahead.k0 * p.lda) * ESIZE;
         next_b = static_cast<const char*>(p.b) +
                  (LB == kAlongK ? (int64_t)(kGated ? 0 : ahead.n0) * p.ldb + ahead.k0 : (int64_t)ahead.k0 * p.ldb) * ESIZE;
+        if (LA == kAlongK) end_a = next_a + ((int64_t)(rows_a - 1) * p.lda + p.k - ahead.k0) * ESIZE;
+        if (LB == kAlongK) end_b = next_b + ((int64_t)(rows_b - 1) * p.ldb + p.k - ahead.k0) * ESIZE;
         bytes_a = whole_words((LA == kAlongK ? (rows_a - 1) * p.lda + p.k - ahead.k0
                                              : (kStep - 1) * p.lda + p.m) * ESIZE);
         bytes_b = whole_words((LB == kAlongK ? (rows_b - 1) * p.ldb + p.k - ahead.k0
@@ -635,29 +639,49 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
         sb.template load<true>(next_b, bytes_b, kStep, dst + T::BM * 128, wave);
         issued();
     };
-    // any step; false when the walk is over
-    auto issue = [&]() SMC_INLINE {
+    // moves on to a step that exists; false when the walk is over
+    auto next_step = [&]() SMC_INLINE {
         while (ahead_step >= ahead.steps) {             // (a split may be empty)
             if (ahead.t + t_step >= t_end) return false;
             const int tm = ahead.tm, tn = ahead.tn;
             ahead.advance(p, t_step, kStep);
             enter(false, ahead.tm != tm, ahead.tn != tn);
         }
+        return true;
+    };
+    auto step_left = [&]() SMC_INLINE {                 // contraction elements of it
         const int rest = ahead.k_len - ahead_step * kStep;
-        const int left = rest < kStep ? rest : kStep;
+        return rest < kStep ? rest : kStep;
+    };
+    // any step, whole words
+    auto issue = [&]() SMC_INLINE {
+        if (!next_step()) return false;
+        const int left = step_left();
         char* dst = s_tile + ahead_buf;
-        const uint32_t wa = LA == kAlongK ? bytes_a : whole_words(((left - 1) * p.lda + p.m) * ESIZE);
-        const uint32_t wb = LB == kAlongK ? bytes_b : whole_words(((left - 1) * p.ldb + p.n) * ESIZE);
-        if (ALIGNED || p.vec_a)
-            sa.template load<false>(next_a, wa, left, dst, wave);
-        else
-            sa.load_elements(next_a, wa, left, tid, dst, ahead.m0, p.m, 0);
-        if (ALIGNED || p.vec_b)
-            sb.template load<false>(next_b, wb, left, dst + T::BM * 128, wave);
-        else
-            sb.load_elements(next_b, wb, left, tid, dst + T::BM * 128, ahead.n0, p.n, p.half);
+        sa.template load<false>(next_a, LA == kAlongK ? bytes_a : whole_words(((left - 1) * p.lda + p.m) * ESIZE),
+                                left, dst, wave);
+        sb.template load<false>(next_b, LB == kAlongK ? bytes_b : whole_words(((left - 1) * p.ldb + p.n) * ESIZE),
+                                left, dst + T::BM * 128, wave);
         issued();
         return true;
+    };
+    // Operands that are not whole words: a step's words are held in registers
+    // while the step before it is multiplied, then put into LDS.
+    u32x4 held_a[decltype(sa)::kLoads], held_b[decltype(sb)::kLoads];
+    auto fetch = [&]() SMC_INLINE {
+        if (!next_step()) return false;
+        const int left = step_left();
+        // (bytes to the operand's end itself, not in whole words)
+        sa.fetch(next_a, LA == kAlongK ? (uint32_t)(end_a - next_a) : (uint32_t)(((left - 1) * p.lda + p.m) * ESIZE),
+                 left, tid, ahead.m0, p.m, 0, held_a);
+        sb.fetch(next_b, LB == kAlongK ? (uint32_t)(end_b - next_b) : (uint32_t)(((left - 1) * p.ldb + p.n) * ESIZE),
+                 left, tid, ahead.n0, p.n, p.half, held_b);
+        return true;
+    };
+    auto commit = [&]() SMC_INLINE {
+        sa.commit(s_tile + ahead_buf, tid, held_a);
+        sb.commit(s_tile + ahead_buf + T::BM * 128, tid, held_b);
+        issued();
     };
 
     ahead.start(p, t_first, kStep);
@@ -676,10 +700,15 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             if (i == in_flight) mark[i] = ops;
         ++in_flight;
     };
+    if constexpr (ALIGNED) {
 #pragma unroll 1
-    for (int i = 0; i < S; ++i) {
-        over = !issue();
-        if (!over) issued_one();
+        for (int i = 0; i < S; ++i) {
+            over = !issue();
+            if (!over) issued_one();
+        }
+    } else {
+        over = !fetch();
+        if (!over) commit();
     }
 
     int buf = 0;                        // byte offset of the step's buffer
@@ -801,9 +830,7 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
         auto arrive = [&]() SMC_INLINE {
             constexpr int kSteady = (S - 2) * T::kLoads;
             const int newer = ops - mark[0];
-            if (!ALIGNED)
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            else if (newer == kSteady)
+            if (newer == kSteady)
                 wait_vm<kSteady>();
             else if (newer >= 16)
                 wait_vm<16>();
@@ -824,15 +851,15 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
         // S steps are in flight at a tile's start: its first step issues none.
         // What the epilogue reads is loaded beside it, two steps before a wait
         // includes it.
-        int step = 0;
-        if (here.steps > 0) {
-            arrive();
-            load_epilogue();
-            if (kHasExtra && p.extra && p.vec_o) ops += MT * kPairs;
-            compute();
-            ++step;
-        }
         if constexpr (ALIGNED) {
+            int step = 0;
+            if (here.steps > 0) {
+                arrive();
+                load_epilogue();
+                if (kHasExtra && p.extra && p.vec_o) ops += MT * kPairs;
+                compute();
+                ++step;
+            }
             // the step issued is a whole one of this tile
             const int main_steps = here.k_len / kStep - (S - 1);
 #pragma unroll 1
@@ -842,30 +869,41 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
                 issued_one();
                 compute();
             }
-        }
 #pragma unroll 1
-        for (; step < here.steps; ++step) {
-            arrive();
+            for (; step < here.steps; ++step) {
+                arrive();
+                if (!over) {
+                    over = !issue();
+                    if (!over) issued_one();
+                }
+                compute();
+            }
+            if (kHasExtra && p.extra) {
+                // the compiler's own wait for them belongs here, before the next
+                // tile's loads, which it does not count
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < kPairs; ++h) asm volatile("" : "+v"(extra[i][h]));
+            }
+            // The last step's buffer is free once every wave has read it.
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
             if (!over) {
                 over = !issue();
                 if (!over) issued_one();
             }
-            compute();
-        }
-        if (kHasExtra && p.extra) {
-            // the compiler's own wait for them belongs here, before the next
-            // tile's loads, which it does not count
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < kPairs; ++h) asm volatile("" : "+v"(extra[i][h]));
-        }
-        // The last step's buffer is free once every wave has read it.
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (!over) {
-            over = !issue();
-            if (!over) issued_one();
+        } else {
+#pragma unroll 1
+            for (int step = 0; step < here.steps; ++step) {
+                __syncthreads();                        // the step's words are in LDS
+                const bool more = !over && fetch();
+                over = !more;
+                if (step == 0) load_epilogue();
+                compute();
+                if (more) commit();
+            }
+            __syncthreads();                            // (the column table of a one-step tile)
         }
 
         // ---- epilogue: acc[i][j] holds row 16 i + r, columns 16 j + 4 q .. + 3 ----
@@ -973,11 +1011,11 @@ hipError_t launch_product(ProductArgs p, hipStream_t s) {
     return hipErrorInvalidValue;                    // (launch_tiled picks a tile that takes them)
 }
 
-typedef Tile<128, 128, 2, 2, 2, 2> TileMid;     // 64 x 64 a wave
-typedef Tile<128, 128, 4, 2, 2, 2> TileWide;    // 32 x 64 a wave, twice the waves
-typedef Tile<64, 128, 2, 2, 2, 3> TileRows;     // three blocks a CU
-typedef Tile<32, 64, 2, 1, 3, 4, true> TileSmall;
-typedef Tile<128, 128, 2, 2, 2, 2, true> TileWeight;    // x^T dz
+typedef Tile<128, 128, 2, 2, 2, 2> TileMid;             // 64 x 64 a wave
+typedef Tile<128, 128, 2, 2, 2, 2, true> TileWeight;    // the same for x^T dz
+typedef Tile<128, 128, 4, 2, 2, 2, true> TileWide;      // 32 x 64 a wave, twice the waves
+typedef Tile<64, 128, 2, 2, 2, 3, true> TileRows;       // three blocks a CU
+typedef Tile<32, 64, 2, 1, 6, 2, true> TileSmall;       // deep: few blocks, long contractions
 
 }  // namespace
 }  // namespace smc

@@ -61,28 +61,44 @@ hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
 
 namespace {
 
-// dw[m, n] (and db[n], the row after) = the splits' float32 sums, added in
-// order and rounded once; W consecutive elements a thread, each split's read
-// independent of the others. Bound by reading them.
-template <int DT, int W>
+// dw[m, n] (and db[n], the row after) = the splits' float32 sums, added in a
+// fixed order and rounded once; W consecutive elements a thread. G threads share
+// an element's splits (each a strided sum) where there are many of them and few
+// elements. Bound by reading the sums.
+template <int DT, int W, int G>
 __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ part, int splits,
                                                    int64_t m, int n, int64_t rows, uint16_t* dw,
                                                    int64_t ldw, uint16_t* db) {
+    constexpr int kPer = 256 / G;                   // words a block
+    __shared__ float s_v[G > 1 ? G : 1][kPer * W + 1];
     const int64_t total = rows * n;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
-    if (i >= total) return;
+    const int x = threadIdx.x % kPer, g = threadIdx.x / kPer;
+    const int64_t i = ((int64_t)blockIdx.x * kPer + x) * W;
     float v[W] = {};
+    if (i < total) {
 #pragma unroll 4
-    for (int sp = 0; sp < splits; ++sp) {
-        const float* src = part + (int64_t)sp * total + i;
-        if constexpr (W == 4) {
-            const f32x4 u = *reinterpret_cast<const f32x4*>(src);
+        for (int sp = g; sp < splits; sp += G) {
+            const float* src = part + (int64_t)sp * total + i;
+            if constexpr (W == 4) {
+                const f32x4 u = *reinterpret_cast<const f32x4*>(src);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += u[e];
-        } else {
-            v[0] += *src;
+                for (int e = 0; e < 4; ++e) v[e] += u[e];
+            } else {
+                v[0] += *src;
+            }
         }
     }
+    if constexpr (G > 1) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) s_v[g][x * W + e] = v[e];
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int o = 1; o < G; ++o)
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] += s_v[o][x * W + e];
+    }
+    if (i >= total) return;
     const int64_t row = i / n;
     const int col = (int)(i - row * n);
     uint16_t* o = row < m ? dw + row * ldw + col : db + col;
@@ -90,16 +106,17 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ par
     for (int e = 0; e < W; ++e) o[e] = (uint16_t)from_f32<DT>(v[e]);
 }
 
-template <int DT>
+template <int DT, int W>
 void sum_parts(const float* part, int splits, int64_t m, int n, int64_t rows, void* dw, int64_t ldw,
                void* db, hipStream_t s) {
     uint16_t* w = static_cast<uint16_t*>(dw);
     uint16_t* b = static_cast<uint16_t*>(db);
-    if (n % 4 == 0)                             // a row's elements in whole 16-byte words of sums
-        launch(k_sum_parts<DT, 4>, dim3((unsigned)((rows * n + 1023) / 1024)), dim3(256), 0, s, part, splits, m,
-               n, rows, w, ldw, b);
+    const int64_t words = (rows * n + W - 1) / W;
+    if (splits >= 32)               // 247 splits of 129 x 16 sums: 25 us by one thread an element
+        launch(k_sum_parts<DT, W, 16>, dim3((unsigned)((words + 15) / 16)), dim3(256), 0, s, part, splits, m, n,
+               rows, w, ldw, b);
     else
-        launch(k_sum_parts<DT, 1>, dim3((unsigned)((rows * n + 255) / 256)), dim3(256), 0, s, part, splits, m, n,
+        launch(k_sum_parts<DT, W, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, part, splits, m, n,
                rows, w, ldw, b);
 }
 
@@ -108,10 +125,10 @@ void sum_parts(const float* part, int splits, int64_t m, int n, int64_t rows, vo
 hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
                             void* db, int dt, hipStream_t s) {
     const int64_t rows = m + (db ? 1 : 0);
-    if (dt == kF16)
-        sum_parts<kF16>(part, splits, m, n, rows, dw, ldw, db, s);
-    else
-        sum_parts<kBF16>(part, splits, m, n, rows, dw, ldw, db, s);
+    // a row's elements in whole 16-byte words of sums, or one at a time
+    auto go = n % 4 == 0 ? (dt == kF16 ? sum_parts<kF16, 4> : sum_parts<kBF16, 4>)
+                         : (dt == kF16 ? sum_parts<kF16, 1> : sum_parts<kBF16, 1>);
+    go(part, splits, m, n, rows, dw, ldw, db, s);
     return hipGetLastError();
 }
 

@@ -22,13 +22,13 @@ namespace {
 template <int DT, bool E4M3, int LA, int LB, int EPI>
 hipError_t launch_tiled(const ProductArgs& p, hipStream_t s) {
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
-    // Half the CUs without a 128 x 128 tile: small tiles (33 x 512 -> 1365: ... us).
-    const int64_t mid = ((p.m + 127) / 128) * ((p.n + 127) / 128);
-    if (!(p.vec_a && p.vec_b) || mid < device_cus() / 2)
-        return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
-    if constexpr (kGated) return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
-    else {
-        if (p.n <= 128) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
+    // fewer 128 x 128 tiles than half the CUs: small tiles, more blocks
+    const int64_t mid = ((p.m + 127) / 128) * (int64_t)((p.n + 127) / 128);
+    if (mid < device_cus() / 2) return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
+    if constexpr (kGated) {
+        return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
+    } else {
+        if (p.n <= 128 || !(p.vec_a && p.vec_b)) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
         return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
     }
 }
