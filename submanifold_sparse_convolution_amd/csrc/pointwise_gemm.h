@@ -445,41 +445,52 @@ __device__ __forceinline__ u32x4 load_extra(const ProductArgs& p, int row, int n
     return x;
 }
 
-// The values, in place of the sums.
-template <int DT, int EPI, int ACT, bool EXTRA>
+// extra's values in the accumulators' order.
+template <int DT, int EPI>
+__device__ __forceinline__ void unpack_extra(const u32x4 (&extra)[Shape<EPI>::kPairs], float (&x)[4][4]) {
+#pragma unroll
+    for (int h = 0; h < Shape<EPI>::kPairs; ++h) {
+        // (opaque: else all rows' values are unpacked at once, into too many registers)
+        u32x4 v = extra[h];
+        asm volatile("" : "+v"(v));
+        uint32_t l0 = v.x, l1 = v.y, h0 = v.z, h1 = v.w;
+        swap_rows(l0, h0);
+        swap_rows(l1, h1);
+        const uint32_t w[4] = {l0, l1, h0, h1};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[2 * h + (e >> 2)][e & 3] = to_f32<DT>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu);
+    }
+}
+
+// The values, in place of the sums (kEpiStore: without the residual).
+template <int DT, int EPI, int ACT>
 __device__ __forceinline__ void row_values(f32x4 (&acc)[4], const u32x4 (&extra)[Shape<EPI>::kPairs]) {
     using Sh = Shape<EPI>;
-    u32x4 x[Sh::kPairs];
-    if constexpr (EXTRA) {
-#pragma unroll
-        for (int h = 0; h < Sh::kPairs; ++h) {
-            // (opaque: else all rows' values are unpacked at once, into too many registers)
-            x[h] = extra[h];
-            asm volatile("" : "+v"(x[h]));
-            uint32_t l0 = x[h].x, l1 = x[h].y, h0 = x[h].z, h1 = x[h].w;
-            swap_rows(l0, h0);
-            swap_rows(l1, h1);
-            x[h] = (u32x4){l0, l1, h0, h1};         // the accumulators' order
-        }
-    }
+    float x[4][4];
+    if constexpr (EPI == kEpiSlope || EPI == kEpiGatedSlope) unpack_extra<DT, EPI>(extra, x);
 #pragma unroll
     for (int j = 0; j < (Sh::kGated ? 2 : 4); ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float z = acc[j][e], u = acc[(j + 2) & 3][e];
-            float ex = 0.f;
-            if constexpr (EXTRA) {
-                const uint32_t w = x[j >> 1][(j & 1) * 2 + (e >> 1)];
-                ex = to_f32<DT>(e & 1 ? w >> 16 : w & 0xffffu);
-            }
-            if (EPI == kEpiStore) acc[j][e] = EXTRA ? act_value<ACT>(z) + ex : act_value<ACT>(z);
-            if (EPI == kEpiSlope) acc[j][e] = ex * act_slope<ACT>(z);
+            if (EPI == kEpiStore) acc[j][e] = act_value<ACT>(z);
+            if (EPI == kEpiSlope) acc[j][e] = x[j][e] * act_slope<ACT>(z);
             if (EPI == kEpiGated) acc[j][e] = act_value<ACT>(z) * u;
             if (EPI == kEpiGatedSlope) {
-                acc[j][e] = ex * u * act_slope<ACT>(z);
-                acc[(j + 2) & 3][e] = ex * act_value<ACT>(z);
+                acc[j][e] = x[j][e] * u * act_slope<ACT>(z);
+                acc[(j + 2) & 3][e] = x[j][e] * act_value<ACT>(z);
             }
         }
+}
+
+template <int DT, int EPI>
+__device__ __forceinline__ void row_residual(f32x4 (&acc)[4], const u32x4 (&extra)[Shape<EPI>::kPairs]) {
+    float x[4][4];
+    unpack_extra<DT, EPI>(extra, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += x[j][e];
 }
 
 // Rounds and stores them. FULL: the row and its columns exist and words are
@@ -948,16 +959,15 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             }
             with_act(p.act, [&](auto act_c) SMC_INLINE {
                 constexpr int ACT = decltype(act_c)::value;
-                if (EPI == kEpiStore && !p.extra) {
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        row_values<DT, EPI, ACT, false>(acc[i], extra[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        row_values<DT, EPI, ACT, kHasExtra>(acc[i], extra[i]);
-                }
+                for (int i = 0; i < MT; ++i) row_values<DT, EPI, ACT>(acc[i], extra[i]);
             });
+            if constexpr (EPI == kEpiStore) {
+                if (p.extra) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) row_residual<DT, EPI>(acc[i], extra[i]);
+                }
+            }
             // in a full tile as many stores as the waits above rely on
             const bool full = p.vec_o && here.m0 + T::BM <= p.m &&
                               here.n0 + (kGated ? T::BN / 2 : T::BN) <= width;
