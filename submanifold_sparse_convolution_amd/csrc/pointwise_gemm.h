@@ -217,7 +217,12 @@ __device__ __forceinline__ void load_to_lds(u32x4 descriptor, uint32_t lds, uint
 // Word permutations of the kAcrossK images: over the k rows that one
 // transposing read touches (see frag_across, frag_across_e4m3).
 __device__ __forceinline__ int swizzle16(int k) { return (k & 3) | ((k >> 1) & 4); }
-__device__ __forceinline__ int swizzle8(int k) { return k & 7; }
+// e4m3 reads take 16 bytes of the k rows k .. k + 7 and k + 16 .. k + 23 at a time:
+// the row's bits that do not choose the bank group by themselves.
+template <int ROWS>
+__device__ __forceinline__ int swizzle8(int k) {
+    return ROWS >= 128 ? ((k >> 1) & 3) | ((k >> 2) & 4) : ((k >> 2) & 1) | ((k >> 3) & 2);
+}
 
 // One operand's step of 128 bytes x ROWS into LDS. GATED: row v of the tile is
 // column v of the interleaved halves: of every 64, 32 of the gate half, then
@@ -267,7 +272,7 @@ struct Stager {
         if (ESIZE == 2)
             v = (((pos >> 1) ^ (swizzle16(k) & (ROWS / 16 - 1))) << 4) | ((pos & 1) << 3);
         else
-            v = (pos ^ (swizzle8(k) & (ROWS / 16 - 1))) << 4;
+            v = (pos ^ (swizzle8<ROWS>(k) & (ROWS / 16 - 1))) << 4;
     }
 
     // base: the step's first element (kAlongK: of the tile's first row; else of
@@ -357,7 +362,7 @@ __device__ __forceinline__ u32x4 frag_across_e4m3(const char* tile, int piece, i
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int k = half * 64 + q * 16 + t * 8 + (s >> 1);
-        const char* p = tile + k * ROWS + ((piece ^ (swizzle8(k) & (ROWS / 16 - 1))) << 4) + ((s & 1) << 3);
+        const char* p = tile + k * ROWS + ((piece ^ (swizzle8<ROWS>(k) & (ROWS / 16 - 1))) << 4) + ((s & 1) << 3);
         v[t] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((SMC_LDS i32x2*)(p)));
     }
     return (u32x4){v[0].x, v[0].y, v[1].x, v[1].y};

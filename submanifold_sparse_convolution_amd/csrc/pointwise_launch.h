@@ -28,8 +28,7 @@ hipError_t launch_tiled(const ProductArgs& p, hipStream_t s) {
     if constexpr (kGated) {
         return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
     } else {
-        if (!(p.vec_a && p.vec_b)) return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
-        if (p.n <= 128) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
+        if (p.n <= 128 || !(p.vec_a && p.vec_b)) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
         return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
     }
 }
