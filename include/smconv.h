@@ -574,8 +574,9 @@ size_t smc_rms_norm_backward_workspace(int64_t n, int c);
  * Backward: dy is the gradient of y; dx [n, c_in], dw [c_in, c_out or 2 c_out]
  * and db (or NULL) those of x, w and bias. The residual's gradient is dy. 16-bit
  * types only. workspace: smc_linear_backward_workspace(args) or
- * smc_gated_backward_workspace(args) bytes (they read n, c_in, c_out,
- * activation, db), 16-byte aligned.
+ * smc_gated_backward_workspace(args) bytes, 16-byte aligned; the query takes the
+ * call's arguments, workspace apart (it depends on sizes, row distances and
+ * alignments: tensors whose rows are not whole 16-byte words are copied to it).
  */
 typedef struct smc_product_s {
     int64_t n;                /* rows */

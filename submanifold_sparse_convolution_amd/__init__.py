@@ -571,9 +571,9 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, e4m3: bool = False, st
     wp = _vector(weight, "weight", dt, dev, c)
     if residual is not None:
         rp, ldr = _rows(residual, "residual", dt, dev, (n, c))
-        s = torch.empty((n, c), dtype=dt, device=dev)
-    y = torch.empty((n, c), dtype=torch.float8_e4m3fn if e4m3 else dt, device=dev)
-    scale = torch.empty(n, dtype=torch.float32, device=dev) if e4m3 else None
+        s = x.new_empty((n, c))
+    y = x.new_empty((n, c), dtype=torch.float8_e4m3fn) if e4m3 else x.new_empty((n, c))
+    scale = x.new_empty(n, dtype=torch.float32) if e4m3 else None
     _check(lib().smc_rms_norm(NormArgs(
         n, c, code, eps, xp, ldx, rp, ldr, wp, y.data_ptr(), c,
         scale.data_ptr() if e4m3 and n else None, s.data_ptr() if s is not None else None, c),
@@ -599,10 +599,10 @@ def rms_norm_backward(dy, s, weight, eps: float = 1e-6, ds=None, stream=None):
     wp = _vector(weight, "weight", dt, dev, c)
     dsp, ldds = _rows(ds, "ds", dt, dev, (n, c)) if ds is not None else (None, 0)
     L = lib()
-    dx = torch.empty((n, c), dtype=dt, device=dev)
-    dweight = torch.empty(c, dtype=dt, device=dev)
+    dx = s.new_empty((n, c))
+    dweight = s.new_empty(c)
     nbytes = L.smc_rms_norm_backward_workspace(n, c)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = s.new_empty(nbytes, dtype=torch.uint8)
     _check(L.smc_rms_norm_backward(NormBackwardArgs(
         n, c, code, eps, dyp, lddy, sp, lds, wp, dsp, ldds, dx.data_ptr(), c,
         dweight.data_ptr(), ws.data_ptr(), nbytes), _raw_stream(dev)))
@@ -644,13 +644,12 @@ def _product_args(halves, x, w, bias, activation, x_scale, w_scale, dtype, backw
                        along, wsp, bp), dt, (n, wide // halves)
 
 
-def _product_out(a, out, dt, device, shape):
+def _product_out(a, x, out, dt, shape):
     if out is None:
-        import torch
-        out = torch.empty(shape, dtype=dt, device=device)
+        out = x.new_empty(shape, dtype=dt)
         a.y, a.ldy = out.data_ptr(), shape[1]
     else:
-        a.y, a.ldy = _rows(out, "out", dt, device, shape)
+        a.y, a.ldy = _rows(out, "out", dt, x.device, shape)
     return out
 
 
@@ -671,7 +670,7 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     a, dt, shape = _product_args(1, x, w, bias, activation, x_scale, w_scale, dtype)
     if residual is not None:
         a.residual, a.ld_residual = _rows(residual, "residual", dt, x.device, shape)
-    out = _product_out(a, out, dt, x.device, shape)
+    out = _product_out(a, x, out, dt, shape)
     _check(lib().smc_linear(a, _raw_stream(x.device)))
     return out
 
@@ -686,7 +685,7 @@ def gated(x, w, bias=None, activation="silu", x_scale=None, w_scale=None, dtype=
         with ctx:
             return gated(x, w, bias, activation, x_scale, w_scale, dtype, out)
     a, dt, shape = _product_args(2, x, w, bias, activation, x_scale, w_scale, dtype)
-    out = _product_out(a, out, dt, x.device, shape)
+    out = _product_out(a, x, out, dt, shape)
     _check(lib().smc_gated(a, _raw_stream(x.device)))
     return out
 
@@ -700,16 +699,16 @@ def _product_backward(halves, dy, x, w, bias, activation, stream):
     a, dt, (n, c_out) = _product_args(halves, x, w, bias, activation, None, None, None, True)
     dev, c_in, wide = x.device, x.shape[1], c_out * halves
     a.dy, a.ld_dy = _rows(dy, "dy", dt, dev, (n, c_out))
-    dx = torch.empty((n, c_in), dtype=dt, device=dev)
-    dw = torch.empty((c_in, wide), dtype=dt, device=dev)
-    db = torch.empty(wide, dtype=dt, device=dev) if bias is not None else None
+    dx = x.new_empty((n, c_in))
+    dw = x.new_empty((c_in, wide))
+    db = x.new_empty(wide) if bias is not None else None
     a.dx, a.ld_dx, a.dw, a.ld_dw = dx.data_ptr(), c_in, dw.data_ptr(), wide
     a.db = db.data_ptr() if db is not None else None
     L = lib()
     need, call = ((L.smc_linear_backward_workspace, L.smc_linear_backward) if halves == 1 else
                   (L.smc_gated_backward_workspace, L.smc_gated_backward))
     nbytes = need(a)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
     a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
     _check(call(a, _raw_stream(dev)))
     return dx, dw, db

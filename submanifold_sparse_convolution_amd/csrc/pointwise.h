@@ -38,6 +38,7 @@ struct ProductArgs {
     const float* b_scale = nullptr;
     const void* extra = nullptr;      // residual, dy or dh: [m, n] ([m, half] gated)
     int64_t ld_extra = 0;
+    int extra_width = 0;        // columns of extra (0: as many as out)
     void* out = nullptr;        // [m, n] ([m, half] for kEpiGated)
     int64_t ldo = 0;
     float* part = nullptr;      // kEpiPartial: [splits][m + colsum][n]
@@ -46,7 +47,7 @@ struct ProductArgs {
     int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
     int act = 0;
     int vec_a = 0, vec_b = 0;   // 16-byte loads are possible
-    int vec_o = 0;              // 16-byte stores (and loads of extra) are possible
+    int vec_o = 0, vec_x = 0;   // 16-byte stores of out, loads of extra are possible
     // the tile walk
     int tiles_m = 0, tiles_n = 0;
     int group_log = 0;          // row tiles walked together (log2)
@@ -68,8 +69,22 @@ hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s);
 // `splits` ranges of the rows, added and rounded by launch_sum_parts.
 int weight_gradient_splits(int64_t rows, int c_in, int n);
 hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s);
-hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
-                            void* db, int dt, hipStream_t s);
+// The sums have n = halves half_p columns; column c < c_out of half h goes to
+// column h c_out + c of dw (and db).
+struct SumArgs {
+    const float* part = nullptr;
+    int splits = 0;
+    int64_t m = 0;              // rows of dw
+    int n = 0, half_p = 0, c_out = 0;
+    void* dw = nullptr;
+    int64_t ldw = 0;
+    void* db = nullptr;         // or null
+};
+hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s);
+// dst [rows_p, ldd] = src [rows, halves c] with each half at a multiple of half_p
+// columns, zeros elsewhere; rows of dst are whole 16-byte words.
+hipError_t launch_pad_rows(const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
+                           int64_t ldd, int64_t rows_p, int half_p, hipStream_t s);
 
 // ---- norm (norm_kernels.hip) ----
 struct NormArgs {

@@ -134,31 +134,55 @@ int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
     p.ldo = a->ldy;
     p.extra = a->residual;
     p.ld_extra = a->ld_residual;
-    p.vec_o = a->c_out >= 8 && words16(a->y, a->ldy) && (!a->residual || words16(a->residual, a->ld_residual));
+    p.vec_o = words16(a->y, a->ldy);
+    p.vec_x = a->c_out >= 8 && words16(a->residual, a->ld_residual);
     return hip_status(launch_forward(p, epi, a->dtype, a->x_dtype == SMC_DTYPE_E4M3, a->w_transposed != 0,
                                      (hipStream_t)stream),
                       halves == 2 ? "smc_gated" : "smc_linear");
 }
 
-// Scratch of a backward pass: dz [n, ld_dz] (none where dz = dy), then the
-// weight gradient's float32 sums.
+// Scratch of a backward pass. Its products read x, w, dz or dy as 16-byte words;
+// where their rows are not made of such, and there are more than a few rows to
+// pay for the copies, padded copies take their place: xp [n, c_in_p], wp
+// [c_in_p, halves half_p] and the bias alike, zeros between; dz has wp's columns.
+// (4,818 rows, gated 144 -> 734: 77 us without the copies, see launch_tiled for
+// the unaligned form.) Then the weight gradient's float32 sums.
 struct Scratch {
-    int64_t ld_dz = 0;
-    size_t dz_bytes = 0;
+    bool slope = false;         // dz is made (else it is dy, or its copy)
+    bool copy_x = false, copy_w = false, copy_dy = false;
+    int half_p = 0, c_in_p = 0; // columns of a half of dz, w; of x
+    int wide_p = 0;
+    size_t xp = 0, wp = 0, bp = 0, dz = 0, part = 0, bytes = 0;     // offsets
     int splits = 1;
-    size_t part_bytes = 0;
-    size_t total() const { return dz_bytes + part_bytes; }
 };
+constexpr int64_t kCopyRows = 16;
 
 Scratch scratch_of(const smc_product_t* a, int halves) {
     Scratch s;
-    const int64_t wide = (int64_t)a->c_out * halves;
-    if (halves == 2 || a->activation != SMC_ACT_NONE) {
-        s.ld_dz = (wide + 7) / 8 * 8;
-        s.dz_bytes = round_up((size_t)a->n * s.ld_dz * 2);
+    s.slope = halves == 2 || a->activation != SMC_ACT_NONE;
+    s.half_p = a->c_out;
+    s.c_in_p = a->c_in;
+    const bool w_words = words16(a->w, a->ldw) && a->c_out % 8 == 0;
+    const bool x_words = words16(a->x, a->ldx) && (!s.slope || a->c_in % 8 == 0);
+    if (a->n > kCopyRows) {
+        s.copy_x = !x_words;
+        if (s.copy_x) s.c_in_p = (a->c_in + 7) / 8 * 8;
+        s.copy_w = !w_words || s.c_in_p != a->c_in;
+        s.half_p = (a->c_out + 7) / 8 * 8;
+        s.copy_dy = !s.slope && !(words16(a->dy, a->ld_dy) && a->c_out % 8 == 0);
     }
-    s.splits = weight_gradient_splits(a->n, a->c_in, (int)wide);
-    s.part_bytes = round_up((size_t)s.splits * (a->c_in + (a->db ? 1 : 0)) * wide * 4);
+    s.wide_p = s.half_p * halves;
+    auto take = [&](size_t bytes) {
+        const size_t at = s.bytes;
+        s.bytes += round_up(bytes);
+        return at;
+    };
+    if (s.copy_x) s.xp = take((size_t)a->n * s.c_in_p * 2);
+    if (s.copy_w) s.wp = take((size_t)s.c_in_p * s.wide_p * 2);
+    if (s.copy_w && a->bias) s.bp = take((size_t)s.wide_p * 2);
+    if (s.slope || s.copy_dy) s.dz = take((size_t)a->n * ((s.wide_p + 7) / 8 * 8) * 2);
+    s.splits = weight_gradient_splits(a->n, a->c_in, s.wide_p);
+    s.part = take((size_t)s.splits * (a->c_in + (a->db ? 1 : 0)) * s.wide_p * 4);
     return s;
 }
 
@@ -166,68 +190,108 @@ size_t workspace_of(const smc_product_t* a, int halves) {
     if (!a || a->n < 0 || a->n > kMaxRows || a->c_in < 1 || a->c_in > kMaxDim || a->c_out < 1 ||
         a->c_out > kMaxDim / halves)
         return 0;
-    return scratch_of(a, halves).total();
+    return scratch_of(a, halves).bytes;
 }
 
 int backward(const smc_product_t* a, int halves, void* stream) {
     const char* name = halves == 2 ? "smc_gated_backward" : "smc_linear_backward";
     CHECK(check_product(a, halves, true));
-    const int64_t wide = (int64_t)a->c_out * halves;
     const Scratch sc = scratch_of(a, halves);
-    if (a->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < sc.total()))
+    if (a->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < sc.bytes))
         return bad(SMC_ERR_ARG, "workspace: %zu bytes at %p, %zu needed, 16-byte aligned",
-                   a->workspace_bytes, a->workspace, sc.total());
+                   a->workspace_bytes, a->workspace, sc.bytes);
     const hipStream_t s = (hipStream_t)stream;
-    if (a->n == 0)
-        return hip_status(launch_sum_parts(nullptr, 0, a->c_in, (int)wide, a->dw, a->ld_dw, a->db,
-                                           a->dtype, s), name);
-    const void* dz = a->dy;
-    int64_t ld_dz = a->ld_dy;
-    if (sc.dz_bytes) {
-        ProductArgs p = forward_args(a, halves);
+    char* const ws = static_cast<char*>(a->workspace);
+    SumArgs sum;
+    sum.m = a->c_in;
+    sum.n = sc.wide_p;
+    sum.half_p = sc.half_p;
+    sum.c_out = a->c_out;
+    sum.dw = a->dw;
+    sum.ldw = a->ld_dw;
+    sum.db = a->db;
+    if (a->n == 0) return hip_status(launch_sum_parts(sum, a->dtype, s), name);
+
+    const void *x = a->x, *w = a->w, *bias = a->bias, *dz = a->dy;
+    int64_t ldx = a->ldx, ldw = a->ldw, ld_dz = a->ld_dy;
+    if (sc.copy_x) {
+        CHECK(hip_status(launch_pad_rows(x, ldx, a->n, 1, a->c_in, ws + sc.xp, sc.c_in_p, a->n, sc.c_in_p, s), name));
+        x = ws + sc.xp;
+        ldx = sc.c_in_p;
+    }
+    if (sc.copy_w) {
+        CHECK(hip_status(launch_pad_rows(w, ldw, a->c_in, halves, a->c_out, ws + sc.wp, sc.wide_p, sc.c_in_p,
+                                         sc.half_p, s), name));
+        w = ws + sc.wp;
+        ldw = sc.wide_p;
+        if (bias && sc.slope) {
+            CHECK(hip_status(launch_pad_rows(bias, (int64_t)a->c_out * halves, 1, halves, a->c_out, ws + sc.bp,
+                                             sc.wide_p, 1, sc.half_p, s), name));
+            bias = ws + sc.bp;
+        }
+    }
+    if (sc.slope) {
+        ProductArgs p;
+        p.a = x;
+        p.lda = ldx;
+        p.b = w;
+        p.ldb = ldw;
+        p.m = (int)a->n;
+        p.k = sc.c_in_p;
+        p.n = sc.wide_p;
+        p.half = sc.half_p;
+        p.bias = bias;
+        p.act = a->activation;
         p.extra = a->dy;
         p.ld_extra = a->ld_dy;
-        p.out = a->workspace;
-        p.ldo = sc.ld_dz;
-        // gated: dz's second half starts at column c_out
-        p.vec_o = a->c_out >= 8 && words16(a->dy, a->ld_dy) && (halves == 1 || a->c_out % 8 == 0);
-        CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false,
-                                        s), name));
-        dz = a->workspace;
-        ld_dz = sc.ld_dz;
+        p.extra_width = a->c_out;
+        p.out = ws + sc.dz;
+        p.ldo = (sc.wide_p + 7) / 8 * 8;
+        p.vec_a = words16(x, ldx) && sc.c_in_p % 8 == 0;
+        p.vec_b = words16(w, ldw) && (halves == 1 || sc.half_p % 8 == 0);
+        p.vec_o = halves == 1 || sc.half_p % 8 == 0;        // gated: dz's second half starts at a word
+        p.vec_x = a->c_out >= 8 && words16(a->dy, a->ld_dy);
+        CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false, s), name));
+        dz = p.out;
+        ld_dz = p.ldo;
+    } else if (sc.copy_dy) {
+        CHECK(hip_status(launch_pad_rows(dz, ld_dz, a->n, 1, a->c_out, ws + sc.dz, sc.half_p, a->n, sc.half_p, s), name));
+        dz = ws + sc.dz;
+        ld_dz = sc.half_p;
     }
     {
         ProductArgs p;                          // dx = dz W^T
         p.a = dz;
         p.lda = ld_dz;
-        p.b = a->w;
-        p.ldb = a->ldw;
+        p.b = w;
+        p.ldb = ldw;
         p.m = (int)a->n;
-        p.k = (int)wide;
+        p.k = sc.wide_p;
         p.n = a->c_in;
         p.out = a->dx;
         p.ldo = a->ld_dx;
-        p.vec_a = words16(dz, ld_dz) && wide % 8 == 0;
-        p.vec_b = words16(a->w, a->ldw) && wide % 8 == 0;
+        p.vec_a = words16(dz, ld_dz) && sc.wide_p % 8 == 0;
+        p.vec_b = words16(w, ldw) && sc.wide_p % 8 == 0;
         p.vec_o = words16(a->dx, a->ld_dx);
         CHECK(hip_status(launch_input_gradient(p, a->dtype, s), name));
     }
     ProductArgs p;                              // dW = x^T dz
-    p.a = a->x;
-    p.lda = a->ldx;
+    p.a = x;
+    p.lda = ldx;
     p.b = dz;
     p.ldb = ld_dz;
     p.m = a->c_in;
     p.k = (int)a->n;
-    p.n = (int)wide;
-    p.part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + sc.dz_bytes);
+    p.n = sc.wide_p;
+    p.part = reinterpret_cast<float*>(ws + sc.part);
     p.splits = sc.splits;
     p.colsum = a->db != nullptr;
-    p.vec_a = words16(a->x, a->ldx);
+    p.vec_a = words16(x, ldx);
     p.vec_b = words16(dz, ld_dz);
     CHECK(hip_status(launch_weight_gradient(p, a->dtype, s), name));
-    return hip_status(launch_sum_parts(p.part, sc.splits, a->c_in, (int)wide, a->dw, a->ld_dw, a->db,
-                                       a->dtype, s), name);
+    sum.part = p.part;
+    sum.splits = sc.splits;
+    return hip_status(launch_sum_parts(sum, a->dtype, s), name);
 }
 
 }  // namespace

@@ -440,13 +440,14 @@ __device__ __forceinline__ void fill_columns(ColumnTable<BN, E4M3>& t, const Pro
     if (E4M3) t.scale[v] = p.b_scale[b];
 }
 
+// (Past extra's last row or column another is read, where nothing is stored.)
 template <int EPI>
 __device__ __forceinline__ u32x4 load_extra(const ProductArgs& p, int row, int nw, int h, int q, int width) {
-    const int col = Shape<EPI>::word(nw, h, q);
+    const int col = Shape<EPI>::word(nw, h, q), own = p.extra_width ? p.extra_width : width;
     const uint16_t* e0 = static_cast<const uint16_t*>(p.extra) + (int64_t)(row < p.m ? row : p.m - 1) * p.ld_extra;
-    if (!p.vec_o) return load_tail(e0 + col, width - col);
-    u32x4 x = *reinterpret_cast<const u32x4*>(e0 + (col + 8 <= width ? col : 0));
-    if (col < width && col + 8 > width) x = load_tail(e0 + col, width - col);
+    if (!p.vec_x) return col + 8 <= own ? load_unaligned(e0 + col) : load_tail(e0 + col, own - col);
+    u32x4 x = *reinterpret_cast<const u32x4*>(e0 + (col + 8 <= own ? col : 0));
+    if (col < own && col + 8 > own) x = load_tail(e0 + col, own - col);
     return x;
 }
 
@@ -872,7 +873,7 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
             if (here.steps > 0) {
                 arrive();
                 load_epilogue();
-                if (kHasExtra && p.extra && p.vec_o) ops += MT * kPairs;
+                if (kHasExtra && p.extra && p.vec_x) ops += MT * kPairs;
                 compute();
                 ++step;
             }

@@ -61,24 +61,22 @@ hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
 
 namespace {
 
-// dw[m, n] (and db[n], the row after) = the splits' float32 sums, added in a
-// fixed order and rounded once; W consecutive elements a thread. G threads share
-// an element's splits (each a strided sum) where there are many of them and few
+// dw (and db, the row after) = the splits' float32 sums, added in a fixed order
+// and rounded once; W consecutive elements a thread. G threads share an
+// element's splits (each a strided sum) where there are many of them and few
 // elements. Bound by reading the sums.
 template <int DT, int W, int G>
-__global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ part, int splits,
-                                                   int64_t m, int n, int64_t rows, uint16_t* dw,
-                                                   int64_t ldw, uint16_t* db) {
+__global__ __launch_bounds__(256) void k_sum_parts(SumArgs a) {
     constexpr int kPer = 256 / G;                   // words a block
     __shared__ float s_v[G > 1 ? G : 1][kPer * W + 1];
-    const int64_t total = rows * n;
+    const int64_t total = (a.m + (a.db ? 1 : 0)) * a.n;
     const int x = threadIdx.x % kPer, g = threadIdx.x / kPer;
     const int64_t i = ((int64_t)blockIdx.x * kPer + x) * W;
     float v[W] = {};
     if (i < total) {
 #pragma unroll 4
-        for (int sp = g; sp < splits; sp += G) {
-            const float* src = part + (int64_t)sp * total + i;
+        for (int sp = g; sp < a.splits; sp += G) {
+            const float* src = a.part + (int64_t)sp * total + i;
             if constexpr (W == 4) {
                 const f32x4 u = *reinterpret_cast<const f32x4*>(src);
 #pragma unroll
@@ -99,36 +97,55 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ par
             for (int e = 0; e < W; ++e) v[e] += s_v[o][x * W + e];
     }
     if (i >= total) return;
-    const int64_t row = i / n;
-    const int col = (int)(i - row * n);
-    uint16_t* o = row < m ? dw + row * ldw + col : db + col;
+    const int64_t row = i / a.n;
+    const int col = (int)(i - row * a.n), h = col / a.half_p, c = col - h * a.half_p;   // (a word lies in one half)
+    uint16_t* o = (row < a.m ? static_cast<uint16_t*>(a.dw) + row * a.ldw : static_cast<uint16_t*>(a.db)) + h * a.c_out + c;
 #pragma unroll
-    for (int e = 0; e < W; ++e) o[e] = (uint16_t)from_f32<DT>(v[e]);
+    for (int e = 0; e < W; ++e)
+        if (c + e < a.c_out) o[e] = (uint16_t)from_f32<DT>(v[e]);
 }
 
 template <int DT, int W>
-void sum_parts(const float* part, int splits, int64_t m, int n, int64_t rows, void* dw, int64_t ldw,
-               void* db, hipStream_t s) {
-    uint16_t* w = static_cast<uint16_t*>(dw);
-    uint16_t* b = static_cast<uint16_t*>(db);
-    const int64_t words = (rows * n + W - 1) / W;
-    if (splits >= 32)               // 247 splits of 129 x 16 sums: 25 us by one thread an element
-        launch(k_sum_parts<DT, W, 16>, dim3((unsigned)((words + 15) / 16)), dim3(256), 0, s, part, splits, m, n,
-               rows, w, ldw, b);
+void sum_parts(const SumArgs& a, hipStream_t s) {
+    const int64_t words = ((a.m + (a.db ? 1 : 0)) * a.n + W - 1) / W;
+    if (a.splits >= 32)             // 247 splits of 129 x 16 sums: 25 us by one thread an element
+        launch(k_sum_parts<DT, W, 16>, dim3((unsigned)((words + 15) / 16)), dim3(256), 0, s, a);
     else
-        launch(k_sum_parts<DT, W, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, part, splits, m, n,
-               rows, w, ldw, b);
+        launch(k_sum_parts<DT, W, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, a);
+}
+
+// 8 columns of dst a thread. Bound by memory.
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ src, int64_t lds, int64_t rows,
+                                                  int halves, int c, uint16_t* __restrict__ dst, int64_t ldd,
+                                                  int64_t rows_p, int half_p) {
+    const int words = (int)(ldd / 8);
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / words;
+    if (row >= rows_p) return;
+    const int col = (int)(i - row * words) * 8, h = col / half_p, k = col - h * half_p;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (row < rows && h < halves) {
+        const uint16_t* e0 = src + row * lds + h * c + k;
+        v = k + 8 <= c ? load_unaligned(e0) : load_tail(e0, c - k);
+    }
+    *reinterpret_cast<u32x4*>(dst + row * ldd + col) = v;
 }
 
 }  // namespace
 
-hipError_t launch_sum_parts(const float* part, int splits, int64_t m, int n, void* dw, int64_t ldw,
-                            void* db, int dt, hipStream_t s) {
-    const int64_t rows = m + (db ? 1 : 0);
-    // a row's elements in whole 16-byte words of sums, or one at a time
-    auto go = n % 4 == 0 ? (dt == kF16 ? sum_parts<kF16, 4> : sum_parts<kBF16, 4>)
-                         : (dt == kF16 ? sum_parts<kF16, 1> : sum_parts<kBF16, 1>);
-    go(part, splits, m, n, rows, dw, ldw, db, s);
+hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s) {
+    // whole 16-byte words of sums, each in one row and half, or one at a time
+    if (a.half_p % 4 == 0)
+        (dt == kF16 ? sum_parts<kF16, 4> : sum_parts<kBF16, 4>)(a, s);
+    else
+        (dt == kF16 ? sum_parts<kF16, 1> : sum_parts<kBF16, 1>)(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_pad_rows(const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
+                           int64_t ldd, int64_t rows_p, int half_p, hipStream_t s) {
+    launch(k_pad_rows, dim3((unsigned)((rows_p * (ldd / 8) + 255) / 256)), dim3(256), 0, s,
+           static_cast<const uint16_t*>(src), lds, rows, halves, c, static_cast<uint16_t*>(dst), ldd, rows_p, half_p);
     return hipGetLastError();
 }
 

@@ -22,13 +22,14 @@ namespace {
 template <int DT, bool E4M3, int LA, int LB, int EPI>
 hipError_t launch_tiled(const ProductArgs& p, hipStream_t s) {
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
-    // fewer 128 x 128 tiles than half the CUs: small tiles, more blocks
-    const int64_t mid = ((p.m + 127) / 128) * (int64_t)((p.n + 127) / 128);
-    if (mid < device_cus() / 2) return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
+    const bool words = p.vec_a && p.vec_b;
+    const int rows = words ? 128 : 64;          // of the tile that would be taken
+    const int64_t tiles = ((p.m + rows - 1) / rows) * (int64_t)((p.n + 127) / 128);
+    if (tiles < device_cus() / 2) return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
     if constexpr (kGated) {
         return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
     } else {
-        if (p.n <= 128 || !(p.vec_a && p.vec_b)) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
+        if (p.n <= 128 || !words) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
         return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
     }
 }

@@ -37,6 +37,10 @@ inline void launch(void (*kern)(P...), dim3 grid, dim3 block, size_t lds, hipStr
     static_assert(sizeof...(P) == sizeof...(A), "argument count");
     hipEvent_t b = nullptr;
     if (g_ktimer.take && !g_ktimer.take(g_ktimer.ctx, &b)) b = nullptr;
+    if (!b) {
+        hipLaunchKernelGGL(kern, grid, block, (uint32_t)lds, s, static_cast<P>(args)...);
+        return;
+    }
     hipExtLaunchKernelGGL(kern, grid, block, (uint32_t)lds, s, nullptr, b, 0u,
                           static_cast<P>(args)...);
 }
