@@ -44,8 +44,8 @@ EXPORTED_SYMBOLS = [
     "smc_probe_mfma_bf16", "smc_probe_copy", "smc_conv_forward_noalloc",
     "smc_test_force_lookback_timeout", "smc_map_rows", "smc_rms_norm", "smc_rms_norm_backward",
     "smc_rms_norm_backward_workspace", "smc_linear", "smc_gated", "smc_linear_backward",
-    "smc_gated_backward", "smc_linear_backward_workspace", "smc_gated_backward_workspace",
-    "smc_weight_quantize",
+    "smc_gated_backward", "smc_linear_workspace", "smc_gated_workspace",
+    "smc_linear_backward_workspace", "smc_gated_backward_workspace", "smc_weight_quantize",
 ]
 STAGES = ["map", "neighbours", "mask_sort", "compact", "gemm", "centre"]
 
@@ -168,7 +168,8 @@ def lib():
                        ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
         getattr(L, name).restype = i32
-    for name in ("smc_linear_backward_workspace", "smc_gated_backward_workspace"):
+    for name in ("smc_linear_workspace", "smc_gated_workspace", "smc_linear_backward_workspace",
+                 "smc_gated_backward_workspace"):
         getattr(L, name).argtypes = [ctypes.POINTER(ProductArgs)]
         getattr(L, name).restype = ctypes.c_size_t
     L.smc_rms_norm_backward_workspace.argtypes = [i64, i32]
@@ -653,6 +654,20 @@ def _product_out(a, x, out, dt, shape):
     return out
 
 
+def _product_forward(halves, a, x):
+    import torch
+    L = lib()
+    need, call = ((L.smc_linear_workspace, L.smc_linear) if halves == 1 else
+                  (L.smc_gated_workspace, L.smc_gated))
+    # rows that are not whole 16-byte words: room for padded copies of them
+    if (a.ldx | a.ldw | a.c_in | a.c_out) & 7 or ((a.x or 0) | a.w) & 15:
+        nbytes = need(a)
+        if nbytes:
+            ws = x.new_empty(nbytes, dtype=torch.uint8)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _check(call(a, _raw_stream(x.device)))
+
+
 def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scale=None, dtype=None,
            out=None, stream=None):
     """y = activation(x @ w + bias) + residual in one kernel.
@@ -671,7 +686,7 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     if residual is not None:
         a.residual, a.ld_residual = _rows(residual, "residual", dt, x.device, shape)
     out = _product_out(a, x, out, dt, shape)
-    _check(lib().smc_linear(a, _raw_stream(x.device)))
+    _product_forward(1, a, x)
     return out
 
 
@@ -686,7 +701,7 @@ def gated(x, w, bias=None, activation="silu", x_scale=None, w_scale=None, dtype=
             return gated(x, w, bias, activation, x_scale, w_scale, dtype, out)
     a, dt, shape = _product_args(2, x, w, bias, activation, x_scale, w_scale, dtype)
     out = _product_out(a, x, out, dt, shape)
-    _check(lib().smc_gated(a, _raw_stream(x.device)))
+    _product_forward(2, a, x)
     return out
 
 

@@ -32,7 +32,8 @@ struct ProductArgs {
     int64_t lda = 0, ldb = 0;   // elements from one memory row to the next
     int m = 0, k = 0;
     int n = 0;                  // columns of b (gated: both halves)
-    int half = 0;               // gated: columns of one half
+    int half = 0;               // gated: columns of one half of b
+    int half_out = 0;           // gated: columns of out and of a half of the bias (0: half)
     const void* bias = nullptr; // [n]
     const float* a_scale = nullptr;   // e4m3: one a row of a, of b
     const float* b_scale = nullptr;
@@ -47,21 +48,19 @@ struct ProductArgs {
     int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
     int act = 0;
     int vec_a = 0, vec_b = 0;   // 16-byte loads are possible
-    int vec_o = 0, vec_x = 0;   // 16-byte stores of out, loads of extra are possible
+    int vec_x = 0;              // a row of extra has a whole 16-byte word
     // the tile walk
     int tiles_m = 0, tiles_n = 0;
     int group_log = 0;          // row tiles walked together (log2)
     int xcds = 8;
 };
 
-// Tile shapes of the product kernel.
-enum TileShape : int { kTileLarge = 0, kTileMid = 1, kTileSmall = 2 };
-
 // Compute units of the current device (looked up once per device).
 int device_cus();
 
 // out = product (see ProductArgs); dt: type of out, bias and extra, and of a
 // and b unless e4m3 (whose b lies along k or across it). Fills in the tile walk.
+constexpr int kFewRows = 16;    // forward 16-bit products of up to as many rows have a kernel of their own
 hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w_along, hipStream_t s);
 // dx = dz W^T: both operands along k.
 hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s);

@@ -77,7 +77,8 @@ int check_product(const smc_product_t* a, int halves, bool backward) {
     if (a->ldw < w_cols || a->ldw > kMaxDim)
         return bad(SMC_ERR_ARG, "row distance of w is %lld, outside [%lld, 2^21]", (long long)a->ldw,
                    (long long)w_cols);
-    if (w_rows * a->ldw * (e4m3 ? 1 : 2) >= ((int64_t)1 << 31))
+    const int64_t padded = e4m3 ? 0 : (a->c_in + 7) / 8 * 8 * ((int64_t)(a->c_out + 7) / 8 * 8) * halves;
+    if ((w_rows * a->ldw > padded ? w_rows * a->ldw : padded) * (e4m3 ? 1 : 2) >= ((int64_t)1 << 31))
         return bad(SMC_ERR_UNSUPPORTED, "w spans 2^31 bytes or more");
     if (e4m3) {
         if (!a->w_scale || (!a->x_scale && a->n > 0)) return bad(SMC_ERR_ARG, "e4m3 operands need scales");
@@ -126,6 +127,45 @@ ProductArgs forward_args(const smc_product_t* a, int halves) {
     return p;
 }
 
+// Padded copies of x and w that a forward product takes where their rows are
+// not whole 16-byte words: x [n, k] and w [k, halves half], zeros between. They
+// cost a pass over x and w and two launches, and spare the product the staging
+// of both operands through registers. In place and with copies, us on the GPU:
+//   w unaligned:  1,000 x 128 -> 141 11.4, 6.7   91,000 x 128 -> 141 59.4, 27.6
+//                 91,000 x 141 -> 141 81.4, 44.4   gated 300 x 702 -> 1365 51.2, 16.4
+//                 91,000 x 128 -> 341 gated 61.8, 45.6
+//   x alone:      20,000 x 250 -> 128 13.3, 17.6; -> 256 15.8, 21.6; -> 512 29.1, 27.4;
+//                 -> 1024 53.9, 34.0   4,000 x 1241 -> 464 38.1, 25.9
+//   one step:     220 x 46 -> 128 5.9, 7.6   13,654 x 29 -> 65 8.2, 8.9
+// so they are made for contractions of more than one step (64) where w is
+// unaligned, or x is and is staged often (more than 256 columns) or long (512).
+struct Padded {
+    bool copy_x = false, copy_w = false;
+    int k = 0, half = 0;
+    size_t w = 0, bytes = 0;    // offset of w's; all of them (0: none needed)
+};
+
+Padded padded_of(const smc_product_t* a, const ProductArgs& p) {
+    Padded pd;
+    const int halves = p.n / a->c_out;
+    if (a->x_dtype == SMC_DTYPE_E4M3 || a->n <= kFewRows || (p.vec_a && p.vec_b)) return pd;
+    if (a->c_in <= 64 || (p.vec_b && p.n <= 256 && a->c_in <= 512)) return pd;
+    pd.copy_x = !p.vec_a;
+    pd.k = (a->c_in + 7) / 8 * 8;
+    pd.copy_w = !p.vec_b || pd.k != a->c_in;
+    pd.half = pd.copy_w ? (a->c_out + 7) / 8 * 8 : a->c_out;
+    if (pd.copy_x) pd.w = round_up((size_t)a->n * pd.k * 2);
+    pd.bytes = pd.w + (pd.copy_w ? round_up((size_t)pd.k * pd.half * halves * 2) : 0);
+    return pd;
+}
+
+size_t forward_workspace_of(const smc_product_t* a, int halves) {
+    if (!a || a->n < 0 || a->n > kMaxRows || a->c_in < 1 || a->c_in > kMaxDim || a->c_out < 1 ||
+        a->c_out > kMaxDim / halves)
+        return 0;
+    return padded_of(a, forward_args(a, halves)).bytes;
+}
+
 int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
     CHECK(check_product(a, halves, false));
     if (a->n == 0) return SMC_OK;
@@ -134,8 +174,30 @@ int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
     p.ldo = a->ldy;
     p.extra = a->residual;
     p.ld_extra = a->ld_residual;
-    p.vec_o = words16(a->y, a->ldy);
-    p.vec_x = a->c_out >= 8 && words16(a->residual, a->ld_residual);
+    const Padded pd = padded_of(a, p);
+    if (pd.bytes && a->workspace && aligned16(a->workspace) && a->workspace_bytes >= pd.bytes) {
+        const hipStream_t s = (hipStream_t)stream;
+        char* const ws = static_cast<char*>(a->workspace);
+        if (pd.copy_x) {
+            CHECK(hip_status(launch_pad_rows(p.a, p.lda, a->n, 1, a->c_in, ws, pd.k, a->n, pd.k, s), "copy of x"));
+            p.a = ws;
+            p.lda = pd.k;
+        }
+        if (pd.copy_w) {
+            CHECK(hip_status(launch_pad_rows(p.b, p.ldb, a->c_in, halves, a->c_out, ws + pd.w, pd.half * halves, pd.k,
+                                             pd.half, s), "copy of w"));
+            p.b = ws + pd.w;
+            p.ldb = pd.half * halves;
+        }
+        p.k = pd.k;
+        if (halves == 2) {
+            p.half_out = a->c_out;
+            p.half = pd.half;
+            p.n = 2 * pd.half;
+        }
+        p.vec_a = p.vec_b = 1;
+    }
+    p.vec_x = a->c_out >= 8;
     return hip_status(launch_forward(p, epi, a->dtype, a->x_dtype == SMC_DTYPE_E4M3, a->w_transposed != 0,
                                      (hipStream_t)stream),
                       halves == 2 ? "smc_gated" : "smc_linear");
@@ -155,7 +217,6 @@ struct Scratch {
     size_t xp = 0, wp = 0, bp = 0, dz = 0, part = 0, bytes = 0;     // offsets
     int splits = 1;
 };
-constexpr int64_t kCopyRows = 16;
 
 Scratch scratch_of(const smc_product_t* a, int halves) {
     Scratch s;
@@ -164,7 +225,7 @@ Scratch scratch_of(const smc_product_t* a, int halves) {
     s.c_in_p = a->c_in;
     const bool w_words = words16(a->w, a->ldw) && a->c_out % 8 == 0;
     const bool x_words = words16(a->x, a->ldx) && (!s.slope || a->c_in % 8 == 0);
-    if (a->n > kCopyRows) {
+    if (a->n > 0) {
         s.copy_x = !x_words;
         if (s.copy_x) s.c_in_p = (a->c_in + 7) / 8 * 8;
         s.copy_w = !w_words || s.c_in_p != a->c_in;
@@ -249,8 +310,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.ldo = (sc.wide_p + 7) / 8 * 8;
         p.vec_a = words16(x, ldx) && sc.c_in_p % 8 == 0;
         p.vec_b = words16(w, ldw) && (halves == 1 || sc.half_p % 8 == 0);
-        p.vec_o = halves == 1 || sc.half_p % 8 == 0;        // gated: dz's second half starts at a word
-        p.vec_x = a->c_out >= 8 && words16(a->dy, a->ld_dy);
+        p.vec_x = a->c_out >= 8;
         CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false, s), name));
         dz = p.out;
         ld_dz = p.ldo;
@@ -272,7 +332,6 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.ldo = a->ld_dx;
         p.vec_a = words16(dz, ld_dz) && sc.wide_p % 8 == 0;
         p.vec_b = words16(w, ldw) && sc.wide_p % 8 == 0;
-        p.vec_o = words16(a->dx, a->ld_dx);
         CHECK(hip_status(launch_input_gradient(p, a->dtype, s), name));
     }
     ProductArgs p;                              // dW = x^T dz
@@ -373,6 +432,8 @@ int smc_linear(const smc_product_t* a, void* stream) { return forward(a, 1, kEpi
 int smc_gated(const smc_product_t* a, void* stream) { return forward(a, 2, kEpiGated, stream); }
 int smc_linear_backward(const smc_product_t* a, void* stream) { return backward(a, 1, stream); }
 int smc_gated_backward(const smc_product_t* a, void* stream) { return backward(a, 2, stream); }
+size_t smc_linear_workspace(const smc_product_t* a) { return forward_workspace_of(a, 1); }
+size_t smc_gated_workspace(const smc_product_t* a) { return forward_workspace_of(a, 2); }
 size_t smc_linear_backward_workspace(const smc_product_t* a) { return workspace_of(a, 1); }
 size_t smc_gated_backward_workspace(const smc_product_t* a) { return workspace_of(a, 2); }
 

@@ -27,7 +27,9 @@ hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w
     p.splits = 1;
     if (e4m3)
         return epi == kEpiGated ? launch_gated_e4m3(p, dt, w_along, s) : launch_store_e4m3(p, dt, w_along, s);
-    if (p.m <= kFewRows && (epi == kEpiStore || epi == kEpiGated)) return launch_few_rows(p, epi, dt, s);
+    const bool gated_words = epi == kEpiGated && p.vec_a && p.vec_b;
+    if (p.m <= (gated_words ? 4 : kFewRows) && (epi == kEpiStore || epi == kEpiGated))
+        return launch_few_rows(p, epi, dt, s);
     switch (epi) {
         case kEpiGated: return launch_gated_16(p, dt, s);
         case kEpiSlope: return launch_slope_16(p, dt, s);
@@ -55,8 +57,8 @@ int weight_gradient_splits(int64_t rows, int c_in, int n) {
 hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
     const int64_t per = ((int64_t)p.k + p.splits - 1) / p.splits;
     p.k_split = (int)((per + 63) / 64 * 64);
-    return dt == kF16 ? launch_product<kF16, false, kAcrossK, kAcrossK, kEpiPartial, TileWeight>(p, s)
-                      : launch_product<kBF16, false, kAcrossK, kAcrossK, kEpiPartial, TileWeight>(p, s);
+    return dt == kF16 ? launch_product<kF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s)
+                      : launch_product<kBF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s);
 }
 
 namespace {

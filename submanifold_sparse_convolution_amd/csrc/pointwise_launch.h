@@ -13,23 +13,46 @@ hipError_t launch_slope_16(const ProductArgs& p, int dt, hipStream_t s);
 hipError_t launch_gated_slope_16(const ProductArgs& p, int dt, hipStream_t s);
 hipError_t launch_store_e4m3(const ProductArgs& p, int dt, bool along, hipStream_t s);
 hipError_t launch_gated_e4m3(const ProductArgs& p, int dt, bool along, hipStream_t s);
-// Up to kFewRows rows (kEpiStore, kEpiGated; 16-bit operands).
-constexpr int kFewRows = 8;
+// Up to kFewRows rows, aligned gated layers 4 (kEpiStore, kEpiGated; 16-bit operands).
 hipError_t launch_few_rows(const ProductArgs& p, Epilogue epi, int dt, hipStream_t s);
 
 namespace {
 
+// Tile by the number of tiles (bf16, us on the GPU, silu unless noted).
+// Small (32 x 64, six steps ahead) while two of them a CU are enough: one round
+// of blocks, each with little work, and the latency of its loads well covered.
+//   c_in -> 512, rows        Small   Rows   Mid
+//   128   1,024                4.5    4.9   6.0
+//   512   1,024 / 2,048    6.5/7.9 7.2/7.3 9.1/9.3
+//   2048  2,048 / 3,000  15.9/26.0 19.1/19.6 22.4/22.7
+//   gated 512 -> 1024, 512 / 768 rows: Small 7.7 / 10.8, Wide 8.3 / 8.4
+//   unaligned 141 -> 141, 4,000 rows: Small 16.4, Rows 18.1; 20,000 x 141 -> 525: 89.6, 59.3
+// Rows (64 x 128, three blocks a CU) while Mid would leave CUs idle, and for
+// narrow outputs, where a tile is mostly epilogue and three blocks overlap it:
+//   512 -> 512, 3,000 / 6,000 / 12,000 / 16,000 rows: Rows 8.3 / 9.5 / 13.4 / 16.9,
+//   Mid 9.8 / 10.4 / 13.2 / 15.0; with 2048 -> 512, 6,000 / 12,000: 21.5 / 34.0, 23.9 / 28.8
+//   91,000 x 128 -> 64 / 128 with a residual: Rows 13.2 / 14.7, Mid 15.0 / 15.0
+//   (without one 11.6 / 12.2, 12.0 / 11.5)
+// Unaligned operands, which go through registers, leave Mid too few of them.
+// Gated: Wide, 32 x 64 a wave, twice the waves to overlap the epilogues of both
+// halves; long 16-bit contractions in Mid, whose waves read less from LDS for a
+// product. 91,000 x 128 -> 344: Wide 35.4, Mid 36.9; e4m3 15,000 x 512 -> 2048:
+// 50.6, 53.5; bf16 4,096 x 512 -> 1024 and 15,000 x 512 -> 2048: 13.9 and 74.3,
+// 12.5 and 69.0. (Slopes only in Wide.)
 template <int DT, bool E4M3, int LA, int LB, int EPI>
 hipError_t launch_tiled(const ProductArgs& p, hipStream_t s) {
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedSlope;
-    const bool words = p.vec_a && p.vec_b;
-    const int rows = words ? 128 : 64;          // of the tile that would be taken
-    const int64_t tiles = ((p.m + rows - 1) / rows) * (int64_t)((p.n + 127) / 128);
-    if (tiles < device_cus() / 2) return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
+    const int64_t cus = device_cus();
+    const int64_t small = ((p.m + 31) / 32) * (int64_t)((p.n + 63) / 64);
+    const int64_t mid = ((p.m + 127) / 128) * (int64_t)((p.n + 127) / 128);
+    if (small <= 2 * cus) return launch_product<DT, E4M3, LA, LB, EPI, TileSmall>(p, s);
     if constexpr (kGated) {
+        if constexpr (EPI == kEpiGated && !E4M3)
+            if (p.k >= 256 && p.vec_a && p.vec_b) return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
         return launch_product<DT, E4M3, LA, LB, EPI, TileWide>(p, s);
     } else {
-        if (p.n <= 128 || !words) return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
+        if (p.n <= 128 || mid <= cus || !p.vec_a || !p.vec_b)
+            return launch_product<DT, E4M3, LA, LB, EPI, TileRows>(p, s);
         return launch_product<DT, E4M3, LA, LB, EPI, TileMid>(p, s);
     }
 }

@@ -1,4 +1,4 @@
-// Forward products of a few rows (up to 8) on 16-bit operands: the serving form
+// Forward products of a few rows (up to 16) on 16-bit operands: the serving form
 // of the linear and gated layers, bound by reading the weights once and by the
 // launch.
 //
@@ -9,6 +9,12 @@
 // partial sums are added across the lanes, then across the waves through LDS,
 // in a fixed order. Few columns a block give many blocks, and 1024 lanes a
 // short chain of loads in each.
+// More rows than a block takes (8, gated 4: registers) are a second dimension of
+// blocks, which read the weights from the cache again. Up to 16 rows: against
+// the product kernel, us on the GPU, 2048 -> 512 with 8 and 16 rows 9.0 and 9.1
+// (13.4 and 13.5), gated 512 -> 1365 8.9 and 14.4 (35.0 and 34.9, unaligned rows),
+// gated 512 -> 1368 7.4 and 12.6 (6.4 and 6.4, so aligned gated layers of more
+// than 4 rows go there).
 #include "pointwise_gemm.h"
 #include "pointwise_launch.h"
 
@@ -30,7 +36,8 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int width = kGated ? p.half : p.n;
     const int c0 = blockIdx.x * CB, col = c0 + lane / kLanes * 8;
-    const uint16_t* x = static_cast<const uint16_t*>(p.a);
+    const int r0 = blockIdx.y * R, rows = p.m - r0;     // this block's rows (R of them at most)
+    const uint16_t* x = static_cast<const uint16_t*>(p.a) + (int64_t)r0 * p.lda;
     const uint16_t* w = static_cast<const uint16_t*>(p.b);
     const int cols = width - col;                       // of this lane's 8 that exist (or more)
 
@@ -54,7 +61,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) v[i][h] = word(w + (int64_t)kc * p.ldb + col + (h ? p.half : 0));
 #pragma unroll
-                for (int r = 0; r < R; ++r) xv[i][r] = to_f32<DT>(x[(int64_t)(r < p.m ? r : 0) * p.lda + kc]);
+                for (int r = 0; r < R; ++r) xv[i][r] = to_f32<DT>(x[(int64_t)(r < rows ? r : 0) * p.lda + kc]);
             }
 #pragma unroll
             for (int i = 0; i < kRounds; ++i) {
@@ -90,7 +97,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
     static_assert(R * CB <= kFewThreads, "a thread an output");
     {
         const int r = tid / CB, c = tid - r * CB;
-        if (r >= p.m || r >= R || c0 + c >= width) return;
+        if (r >= rows || r >= R || c0 + c >= width) return;
         float z[kHalves];
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
@@ -103,24 +110,25 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
         with_act(p.act, [&](auto act_c) SMC_INLINE { y = act_value<decltype(act_c)::value>(z[0]); });
         if (kGated) y *= z[kHalves - 1];
         if (!kGated && p.extra)
-            y += to_f32<DT>(static_cast<const uint16_t*>(p.extra)[(int64_t)r * p.ld_extra + c0 + c]);
-        static_cast<uint16_t*>(p.out)[(int64_t)r * p.ldo + c0 + c] = (uint16_t)from_f32<DT>(y);
+            y += to_f32<DT>(static_cast<const uint16_t*>(p.extra)[(int64_t)(r0 + r) * p.ld_extra + c0 + c]);
+        static_cast<uint16_t*>(p.out)[(int64_t)(r0 + r) * p.ldo + c0 + c] = (uint16_t)from_f32<DT>(y);
     }
 }
 
 template <int DT, int EPI, int R>
 hipError_t few_t(const ProductArgs& p, hipStream_t s) {
     const int width = EPI == kEpiGated ? p.half : p.n;
+    const unsigned groups = (unsigned)((p.m + R - 1) / R);
     // The widest blocks (whole 128-byte lines of a weight row) that still give
     // 128 of them, else 16 columns. One row, 2048 -> 512 and gated 512 -> 1365:
     // 8.4 and 7.3 us with 8 columns a block, 5.0 and 7.6 with 16, 7.1 and 10.3
     // with 32, 10.7 and 11.7 with 64.
     if (width >= 128 * 64)
-        launch(k_few_rows<DT, EPI, R, 64>, dim3((unsigned)((width + 63) / 64)), dim3(kFewThreads), 0, s, p);
+        launch(k_few_rows<DT, EPI, R, 64>, dim3((unsigned)((width + 63) / 64), groups), dim3(kFewThreads), 0, s, p);
     else if (width >= 128 * 32)
-        launch(k_few_rows<DT, EPI, R, 32>, dim3((unsigned)((width + 31) / 32)), dim3(kFewThreads), 0, s, p);
+        launch(k_few_rows<DT, EPI, R, 32>, dim3((unsigned)((width + 31) / 32), groups), dim3(kFewThreads), 0, s, p);
     else
-        launch(k_few_rows<DT, EPI, R, 16>, dim3((unsigned)((width + 15) / 16)), dim3(kFewThreads), 0, s, p);
+        launch(k_few_rows<DT, EPI, R, 16>, dim3((unsigned)((width + 15) / 16), groups), dim3(kFewThreads), 0, s, p);
     return hipGetLastError();
 }
 
@@ -128,8 +136,8 @@ template <int DT, int EPI>
 hipError_t few(const ProductArgs& p, hipStream_t s) {
     if (p.m <= 1) return few_t<DT, EPI, 1>(p, s);
     if (p.m <= 2) return few_t<DT, EPI, 2>(p, s);
-    if (p.m <= 4) return few_t<DT, EPI, 4>(p, s);
-    return few_t<DT, EPI, 8>(p, s);
+    if constexpr (EPI == kEpiGated) return few_t<DT, EPI, 4>(p, s);
+    else return p.m <= 4 ? few_t<DT, EPI, 4>(p, s) : few_t<DT, EPI, 8>(p, s);
 }
 
 }  // namespace

@@ -125,6 +125,8 @@ int main(void) {
         REFUSED(back[i], a, x_dtype, SMC_DTYPE_E4M3, SMC_ERR_UNSUPPORTED);
         EXPECT(need[i](NULL), 0);
         EXPECT(need[i](&a) >= (size_t)16 * 8 * 4, 1);
+        size_t (*room[2])(const smc_product_t*) = {smc_linear_workspace, smc_gated_workspace};
+        EXPECT(room[i](NULL), 0);
     }
 
     EXPECT(smc_weight_quantize(NULL, 8, 16, 8, SMC_DTYPE_BF16, p, 16, f32, NULL), SMC_ERR_ARG);

@@ -100,6 +100,42 @@ def test_gated_backward(n, c_in, c_out, dt):
                 ro.check(v, wv, bd, f"{label} {name} bias={bias}")
 
 
+@pytest.mark.parametrize("n", [9, 12, 15, 16])
+@pytest.mark.parametrize("c_in,c_out", [(64, 64), (65, 63), (2048, 40), (130, 1100)])
+def test_few_rows(n, c_in, c_out):
+    """More rows than one block of the few-row kernel takes."""
+    g, x, w, b = layer(n + c_in, n, c_in, c_out, 1, BF16, True)
+    r = normal(g, (n, c_out), 2.0)
+    y = smc.linear(dev(x), dev(w), bias=dev(b), residual=dev(r), activation="silu")
+    ro.check(y, *ro.linear(d(x), d(w), d(b), d(r), "silu", BF16), "linear")
+    g, x, w, b = layer(n + c_in, n, c_in, c_out, 2, BF16, True)
+    y = smc.gated(dev(x), dev(w), bias=dev(b), activation="gelu")
+    ro.check(y, *ro.gated(d(x), d(w), d(b), "gelu", BF16), "gated")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("n,c_in,c_out", [(17, 65, 63), (40, 64, 50), (300, 33, 56), (2500, 141, 141), (4200, 72, 525)])
+def test_unaligned_rows_without_workspace(n, c_in, c_out, dt):
+    """The C entries read rows that are not whole 16-byte words in place where
+    they are given no room for copies; both forms agree with the formulas."""
+    L = smc.lib()
+    for halves, entry, need in ((1, L.smc_linear, L.smc_linear_workspace), (2, L.smc_gated, L.smc_gated_workspace)):
+        g, x, w, b = layer(n + c_in, n, c_in, c_out, halves, dt, True)
+        xd, wd, bd = dev(x), dev(w), dev(b)
+        want = (ro.linear(d(x), d(w), d(b), None, "silu", dt) if halves == 1 else
+                ro.gated(d(x), d(w), d(b), "silu", dt))
+        a, _, shape = smc._product_args(halves, xd, wd, bd, "silu", None, None, None)
+        y = smc._product_out(a, xd, None, dt, shape)
+        nbytes = need(a)
+        assert nbytes > 0 or c_in <= 64         # no copies for a single step
+        for ws in (None, torch.full((max(nbytes, 16),), 255, dtype=torch.uint8, device="cuda")):
+            y.fill_(float("nan"))
+            if ws is not None:
+                a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+            assert entry(a, smc._raw_stream(xd.device)) == 0
+            ro.check(y, *want, f"halves={halves} workspace={ws is not None}")
+
+
 # Sizes of every tile shape, tails of rows, columns and contraction. Integers:
 # every product and sum is exact in float32, so the one rounding left is the
 # output's (and dz's), and results are equal bit for bit.
