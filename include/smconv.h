@@ -569,11 +569,12 @@ size_t smc_rms_norm_backward_workspace(int64_t n, int c);
  * scale an output column, and x w is the product of the scaled values; with
  * w_transposed, w is stored as [c_out (gated: 2 c_out), c_in]
  * (smc_weight_quantize writes that). w's last element lies within 2^31 bytes
- * of its first, with c_in and c_out rounded up to 8 (else SMC_ERR_UNSUPPORTED).
+ * of its first, with c_in and c_out rounded up to 16 bytes (else
+ * SMC_ERR_UNSUPPORTED).
  * workspace may be NULL in a forward call. Given at least smc_linear_workspace(args)
- * (smc_gated_workspace) bytes, 16-byte aligned, 16-bit tensors whose rows are not
- * whole 16-byte words are copied to it first, which is faster; the query
- * takes the call's arguments and is 0 where no copy would be made.
+ * (smc_gated_workspace) bytes, 16-byte aligned, tensors whose rows are not whole
+ * 16-byte words are copied to it first, which is faster; the query takes the
+ * call's arguments and is 0 where no copy would be made.
  *
  * Backward: dy is the gradient of y; dx [n, c_in], dw [c_in, c_out or 2 c_out]
  * and db (or NULL) those of x, w and bias. The residual's gradient is dy. 16-bit

@@ -660,7 +660,7 @@ def _product_forward(halves, a, x):
     need, call = ((L.smc_linear_workspace, L.smc_linear) if halves == 1 else
                   (L.smc_gated_workspace, L.smc_gated))
     # rows that are not whole 16-byte words: room for padded copies of them
-    if (a.ldx | a.ldw | a.c_in | a.c_out) & 7 or ((a.x or 0) | a.w) & 15:
+    if (a.ldx | a.ldw | a.c_in | a.c_out) & (15 if a.x_dtype == 2 else 7) or ((a.x or 0) | a.w) & 15:
         nbytes = need(a)
         if nbytes:
             ws = x.new_empty(nbytes, dtype=torch.uint8)

@@ -81,8 +81,9 @@ struct SumArgs {
 };
 hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s);
 // dst [rows_p, ldd] = src [rows, halves c] with each half at a multiple of half_p
-// columns, zeros elsewhere; rows of dst are whole 16-byte words.
-hipError_t launch_pad_rows(const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
+// columns, zeros elsewhere; rows of dst are whole 16-byte words. esize: bytes an
+// element (1 or 2).
+hipError_t launch_pad_rows(int esize, const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
                            int64_t ldd, int64_t rows_p, int half_p, hipStream_t s);
 
 // ---- norm (norm_kernels.hip) ----

@@ -77,7 +77,8 @@ int check_product(const smc_product_t* a, int halves, bool backward) {
     if (a->ldw < w_cols || a->ldw > kMaxDim)
         return bad(SMC_ERR_ARG, "row distance of w is %lld, outside [%lld, 2^21]", (long long)a->ldw,
                    (long long)w_cols);
-    const int64_t padded = e4m3 ? 0 : (a->c_in + 7) / 8 * 8 * ((int64_t)(a->c_out + 7) / 8 * 8) * halves;
+    const int per = e4m3 ? 16 : 8;
+    const int64_t padded = ((int64_t)a->c_in + per - 1) / per * per * ((a->c_out + per - 1) / per * per) * halves;
     if ((w_rows * a->ldw > padded ? w_rows * a->ldw : padded) * (e4m3 ? 1 : 2) >= ((int64_t)1 << 31))
         return bad(SMC_ERR_UNSUPPORTED, "w spans 2^31 bytes or more");
     if (e4m3) {
@@ -136,8 +137,10 @@ ProductArgs forward_args(const smc_product_t* a, int halves) {
 //                 91,000 x 128 -> 341 gated 61.8, 45.6
 //   x alone:      20,000 x 250 -> 128 13.3, 17.6; -> 256 15.8, 21.6; -> 512 29.1, 27.4;
 //                 -> 1024 53.9, 34.0   4,000 x 1241 -> 464 38.1, 25.9
+//   e4m3, w in [k, n] order: 20 x 1488 -> 106 78.2, 10.3   41,305 x 240 -> 995 93.9, 51.8
+//   e4m3, x alone: 20,000 x 250 -> 128 / 512 20.9 / 42.9, 14.9 / 23.1
 //   one step:     220 x 46 -> 128 5.9, 7.6   13,654 x 29 -> 65 8.2, 8.9
-// so they are made for contractions of more than one step (64) where w is
+// so they are made for contractions of more than one step (128 bytes) where w is
 // unaligned, or x is and is staged often (more than 256 columns) or long (512).
 struct Padded {
     bool copy_x = false, copy_w = false;
@@ -147,15 +150,16 @@ struct Padded {
 
 Padded padded_of(const smc_product_t* a, const ProductArgs& p) {
     Padded pd;
-    const int halves = p.n / a->c_out;
-    if (a->x_dtype == SMC_DTYPE_E4M3 || a->n <= kFewRows || (p.vec_a && p.vec_b)) return pd;
-    if (a->c_in <= 64 || (p.vec_b && p.n <= 256 && a->c_in <= 512)) return pd;
+    const int halves = p.n / a->c_out, es = a->x_dtype == SMC_DTYPE_E4M3 ? 1 : 2, per = 16 / es;
+    if ((es == 2 && a->n <= kFewRows) || (p.vec_a && p.vec_b)) return pd;
+    if (a->c_in <= 128 / es || (p.vec_b && p.n <= 256 && a->c_in <= 512)) return pd;
     pd.copy_x = !p.vec_a;
-    pd.k = (a->c_in + 7) / 8 * 8;
+    pd.k = (a->c_in + per - 1) / per * per;
     pd.copy_w = !p.vec_b || pd.k != a->c_in;
-    pd.half = pd.copy_w ? (a->c_out + 7) / 8 * 8 : a->c_out;
-    if (pd.copy_x) pd.w = round_up((size_t)a->n * pd.k * 2);
-    pd.bytes = pd.w + (pd.copy_w ? round_up((size_t)pd.k * pd.half * halves * 2) : 0);
+    // (w^T has its halves in rows)
+    pd.half = pd.copy_w && !a->w_transposed ? (a->c_out + per - 1) / per * per : a->c_out;
+    if (pd.copy_x) pd.w = round_up((size_t)a->n * pd.k * es);
+    pd.bytes = pd.w + (pd.copy_w ? round_up((size_t)pd.k * pd.half * halves * es) : 0);
     return pd;
 }
 
@@ -178,22 +182,26 @@ int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
     if (pd.bytes && a->workspace && aligned16(a->workspace) && a->workspace_bytes >= pd.bytes) {
         const hipStream_t s = (hipStream_t)stream;
         char* const ws = static_cast<char*>(a->workspace);
+        const int es = a->x_dtype == SMC_DTYPE_E4M3 ? 1 : 2, wide = pd.half * halves;
         if (pd.copy_x) {
-            CHECK(hip_status(launch_pad_rows(p.a, p.lda, a->n, 1, a->c_in, ws, pd.k, a->n, pd.k, s), "copy of x"));
+            CHECK(hip_status(launch_pad_rows(es, p.a, p.lda, a->n, 1, a->c_in, ws, pd.k, a->n, pd.k, s), "copy of x"));
             p.a = ws;
             p.lda = pd.k;
         }
         if (pd.copy_w) {
-            CHECK(hip_status(launch_pad_rows(p.b, p.ldb, a->c_in, halves, a->c_out, ws + pd.w, pd.half * halves, pd.k,
-                                             pd.half, s), "copy of w"));
+            const hipError_t e =
+                a->w_transposed
+                    ? launch_pad_rows(es, p.b, p.ldb, p.n, 1, a->c_in, ws + pd.w, pd.k, p.n, pd.k, s)
+                    : launch_pad_rows(es, p.b, p.ldb, a->c_in, halves, a->c_out, ws + pd.w, wide, pd.k, pd.half, s);
+            CHECK(hip_status(e, "copy of w"));
             p.b = ws + pd.w;
-            p.ldb = pd.half * halves;
+            p.ldb = a->w_transposed ? pd.k : wide;
         }
         p.k = pd.k;
         if (halves == 2) {
             p.half_out = a->c_out;
             p.half = pd.half;
-            p.n = 2 * pd.half;
+            p.n = wide;
         }
         p.vec_a = p.vec_b = 1;
     }
@@ -276,17 +284,17 @@ int backward(const smc_product_t* a, int halves, void* stream) {
     const void *x = a->x, *w = a->w, *bias = a->bias, *dz = a->dy;
     int64_t ldx = a->ldx, ldw = a->ldw, ld_dz = a->ld_dy;
     if (sc.copy_x) {
-        CHECK(hip_status(launch_pad_rows(x, ldx, a->n, 1, a->c_in, ws + sc.xp, sc.c_in_p, a->n, sc.c_in_p, s), name));
+        CHECK(hip_status(launch_pad_rows(2, x, ldx, a->n, 1, a->c_in, ws + sc.xp, sc.c_in_p, a->n, sc.c_in_p, s), name));
         x = ws + sc.xp;
         ldx = sc.c_in_p;
     }
     if (sc.copy_w) {
-        CHECK(hip_status(launch_pad_rows(w, ldw, a->c_in, halves, a->c_out, ws + sc.wp, sc.wide_p, sc.c_in_p,
+        CHECK(hip_status(launch_pad_rows(2, w, ldw, a->c_in, halves, a->c_out, ws + sc.wp, sc.wide_p, sc.c_in_p,
                                          sc.half_p, s), name));
         w = ws + sc.wp;
         ldw = sc.wide_p;
         if (bias && sc.slope) {
-            CHECK(hip_status(launch_pad_rows(bias, (int64_t)a->c_out * halves, 1, halves, a->c_out, ws + sc.bp,
+            CHECK(hip_status(launch_pad_rows(2, bias, (int64_t)a->c_out * halves, 1, halves, a->c_out, ws + sc.bp,
                                              sc.wide_p, 1, sc.half_p, s), name));
             bias = ws + sc.bp;
         }
@@ -315,7 +323,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         dz = p.out;
         ld_dz = p.ldo;
     } else if (sc.copy_dy) {
-        CHECK(hip_status(launch_pad_rows(dz, ld_dz, a->n, 1, a->c_out, ws + sc.dz, sc.half_p, a->n, sc.half_p, s), name));
+        CHECK(hip_status(launch_pad_rows(2, dz, ld_dz, a->n, 1, a->c_out, ws + sc.dz, sc.half_p, a->n, sc.half_p, s), name));
         dz = ws + sc.dz;
         ld_dz = sc.half_p;
     }

@@ -116,19 +116,26 @@ void sum_parts(const SumArgs& a, hipStream_t s) {
         launch(k_sum_parts<DT, W, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, a);
 }
 
-// 8 columns of dst a thread. Bound by memory.
-__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ src, int64_t lds, int64_t rows,
-                                                  int halves, int c, uint16_t* __restrict__ dst, int64_t ldd,
-                                                  int64_t rows_p, int half_p) {
-    const int words = (int)(ldd / 8);
+// 16 bytes of dst a thread. Bound by memory. (Divided in 32 bits where they do.)
+template <typename E>
+__global__ __launch_bounds__(256) void k_pad_rows(const E* __restrict__ src, int64_t lds, int64_t rows, int halves,
+                                                  int c, E* __restrict__ dst, int64_t ldd, int64_t rows_p, int half_p) {
+    constexpr int kPer = 16 / sizeof(E);
+    const int words = (int)(ldd / kPer);
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i / words;
+    const int64_t row = rows_p * words < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)words) : i / words;
     if (row >= rows_p) return;
-    const int col = (int)(i - row * words) * 8, h = col / half_p, k = col - h * half_p;
+    const int col = (int)(i - row * words) * kPer, h = col / half_p, k = col - h * half_p;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (row < rows && h < halves) {
-        const uint16_t* e0 = src + row * lds + h * c + k;
-        v = k + 8 <= c ? load_unaligned(e0) : load_tail(e0, c - k);
+        const E* e0 = src + row * lds + (int64_t)h * c + k;
+        if (k + kPer <= c) {
+            v = load_unaligned(e0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (k + e < c) v[e * (int)sizeof(E) / 4] |= (uint32_t)e0[e] << (e * (int)sizeof(E) % 4 * 8);
+        }
     }
     *reinterpret_cast<u32x4*>(dst + row * ldd + col) = v;
 }
@@ -144,10 +151,15 @@ hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_pad_rows(const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
+hipError_t launch_pad_rows(int esize, const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
                            int64_t ldd, int64_t rows_p, int half_p, hipStream_t s) {
-    launch(k_pad_rows, dim3((unsigned)((rows_p * (ldd / 8) + 255) / 256)), dim3(256), 0, s,
-           static_cast<const uint16_t*>(src), lds, rows, halves, c, static_cast<uint16_t*>(dst), ldd, rows_p, half_p);
+    const dim3 grid((unsigned)((rows_p * (ldd * esize / 16) + 255) / 256));
+    if (esize == 1)
+        launch(k_pad_rows<uint8_t>, grid, dim3(256), 0, s, static_cast<const uint8_t*>(src), lds, rows, halves, c,
+               static_cast<uint8_t*>(dst), ldd, rows_p, half_p);
+    else
+        launch(k_pad_rows<uint16_t>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src), lds, rows, halves, c,
+               static_cast<uint16_t*>(dst), ldd, rows_p, half_p);
     return hipGetLastError();
 }
 

@@ -214,6 +214,42 @@ def test_e4m3_layers(n, c_in, c_out, transposed):
         ro.check(y, want, ro.rounded(want, err, dt), f"halves={halves} {name}")
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("n,c_in,c_out", [(1, 145, 33), (20, 1488, 106), (40, 130, 50), (300, 530, 300), (2500, 241, 141)])
+def test_unaligned_e4m3_without_workspace(n, c_in, c_out, transposed):
+    """e4m3 rows that are not whole 16-byte words, in place and through copies,
+    w in both memory orders."""
+    L = smc.lib()
+    for halves, entry, need in ((1, L.smc_linear, L.smc_linear_workspace), (2, L.smc_gated, L.smc_gated_workspace)):
+        g = gen(n + c_in + halves)
+        q, xs = smc.rms_norm(dev(normal(g, (n, c_in))), torch.ones(c_in, dtype=BF16, device="cuda"), e4m3=True)
+        wq, ws = smc.quantize_weight(dev(normal(g, (c_in, halves * c_out), c_in ** -0.5)))
+        if not transposed:
+            wq = wq.t().contiguous().t()
+        b = normal(g, (halves * c_out,), 0.3)
+        xd = q.cpu().double() * xs.cpu().double()[:, None]
+        wd = (wq.cpu().double() * ws.cpu().double()[:, None]).t()
+        z, ez = ro.pre(xd, wd, d(b), extra_terms=5, loss=ro.E4M3_LOSS)
+        if halves == 1:
+            want, err = z, ez
+        else:
+            a = ro.act(z[:, :c_out], "relu")
+            want = a * z[:, c_out:]
+            err = ez[:, :c_out] * z[:, c_out:].abs() + a * ez[:, c_out:] + ez[:, :c_out] * ez[:, c_out:] + ro.U * want.abs()
+        bound = ro.rounded(want, err, BF16)
+        args, dt, shape = smc._product_args(halves, q, wq, dev(b), None if halves == 1 else "relu", xs, ws, BF16)
+        bias = dev(b)
+        args.bias = bias.data_ptr()
+        y = smc._product_out(args, q, None, dt, shape)
+        nbytes = need(args)
+        for room in (None, torch.full((max(nbytes, 16),), 255, dtype=torch.uint8, device="cuda")):
+            y.fill_(float("nan"))
+            if room is not None:
+                args.workspace, args.workspace_bytes = room.data_ptr(), nbytes
+            assert entry(args, smc._raw_stream(q.device)) == 0
+            ro.check(y, want, bound, f"halves={halves} workspace={room is not None} ({nbytes} bytes)")
+
+
 def test_e4m3_exact():
     """Small integers are e4m3 values; powers of two as scales: bit for bit."""
     g = gen(5)
