@@ -8,7 +8,11 @@
 //   dx = rstd (a - x_hat mean(a x_hat)) + ds,   dw = sum over rows of dy x_hat
 //
 // Bound by memory: every row is read once and kept in registers between its
-// sums and its outputs.
+// sums and its outputs, by as many lanes as its 16-byte words (16 of them for 128
+// channels, so a wave takes four rows and the sums stay inside it); rows too
+// long for that are read again. With the residual, bf16: 91,000 x 128 15.3 us (93
+// MB, 6.1 TB/s, part of it cached), e4m3 15,000 x 512 12.2 us (4.4 TB/s), backward
+// 95,000 x 128 18.3 us (5.3 TB/s) and 3.9 us for the sums of dw.
 #include <algorithm>
 
 #include "pointwise_gemm.h"
