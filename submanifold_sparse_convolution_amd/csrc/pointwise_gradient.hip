@@ -45,12 +45,14 @@ hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s) {
                       : launch_tiled<kBF16, false, kAlongK, kAlongK, kEpiStore>(p, s);
 }
 
-// Ranges of the rows: enough to give every CU two 128 x 128 tiles, none
-// shorter than 256 rows (4 steps), so that a tile's sums (64 KiB to memory and
-// back) stay small beside the rows it reads.
+// Ranges of the rows: as many as give every CU at most two 128 x 128 tiles, what
+// is resident at once (rounded up, a few blocks took a second tile: dW of 84,276 x
+// 144 -> 832 61.7 us, 40.5 so; 5,172 x 336 -> 1824 20.7, 16.7), none shorter than 256
+// rows (4 steps), so that a tile's sums (64 KiB to memory and back) stay small
+// beside the rows it reads.
 int weight_gradient_splits(int64_t rows, int c_in, int n) {
     const int64_t tiles = (int64_t)((c_in + 127) / 128) * ((n + 127) / 128);
-    const int64_t want = (2 * device_cus() + tiles - 1) / tiles;
+    const int64_t want = 2 * device_cus() / tiles;
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, (rows + 255) / 256));
 }
 
@@ -64,11 +66,15 @@ hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
 namespace {
 
 // dw (and db, the row after) = the splits' float32 sums, added in a fixed order
-// and rounded once; W consecutive elements a thread. G threads share an
-// element's splits (each a strided sum) where there are many of them and few
-// elements. Bound by reading the sums.
-template <int DT, int W, int G>
+// and rounded once; kSumWord consecutive elements a thread (halves start at
+// multiples of 8 columns). G threads share an element's splits (each a strided
+// sum) where there are many of them and few elements. Bound by reading the sums:
+// 8 splits of 2048 x 512, 16.8 MB, 7.0 us.
+constexpr int kSumWord = 4;
+
+template <int DT, int G>
 __global__ __launch_bounds__(256) void k_sum_parts(SumArgs a) {
+    constexpr int W = kSumWord;
     constexpr int kPer = 256 / G;                   // words a block
     __shared__ float s_v[G > 1 ? G : 1][kPer * W + 1];
     const int64_t total = (a.m + (a.db ? 1 : 0)) * a.n;
@@ -79,13 +85,9 @@ __global__ __launch_bounds__(256) void k_sum_parts(SumArgs a) {
 #pragma unroll 4
         for (int sp = g; sp < a.splits; sp += G) {
             const float* src = a.part + (int64_t)sp * total + i;
-            if constexpr (W == 4) {
-                const f32x4 u = *reinterpret_cast<const f32x4*>(src);
+            const f32x4 u = *reinterpret_cast<const f32x4*>(src);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += u[e];
-            } else {
-                v[0] += *src;
-            }
+            for (int e = 0; e < W; ++e) v[e] += u[e];
         }
     }
     if constexpr (G > 1) {
@@ -101,19 +103,20 @@ __global__ __launch_bounds__(256) void k_sum_parts(SumArgs a) {
     if (i >= total) return;
     const int64_t row = i / a.n;
     const int col = (int)(i - row * a.n), h = col / a.half_p, c = col - h * a.half_p;   // (a word lies in one half)
-    uint16_t* o = (row < a.m ? static_cast<uint16_t*>(a.dw) + row * a.ldw : static_cast<uint16_t*>(a.db)) + h * a.c_out + c;
+    uint16_t* o = row < a.m ? static_cast<uint16_t*>(a.dw) + row * a.ldw : static_cast<uint16_t*>(a.db);
+    o += h * a.c_out + c;
 #pragma unroll
     for (int e = 0; e < W; ++e)
         if (c + e < a.c_out) o[e] = (uint16_t)from_f32<DT>(v[e]);
 }
 
-template <int DT, int W>
+template <int DT>
 void sum_parts(const SumArgs& a, hipStream_t s) {
-    const int64_t words = ((a.m + (a.db ? 1 : 0)) * a.n + W - 1) / W;
+    const int64_t words = ((a.m + (a.db ? 1 : 0)) * a.n + kSumWord - 1) / kSumWord;
     if (a.splits >= 32)             // 247 splits of 129 x 16 sums: 25 us by one thread an element
-        launch(k_sum_parts<DT, W, 16>, dim3((unsigned)((words + 15) / 16)), dim3(256), 0, s, a);
+        launch(k_sum_parts<DT, 16>, dim3((unsigned)((words + 15) / 16)), dim3(256), 0, s, a);
     else
-        launch(k_sum_parts<DT, W, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, a);
+        launch(k_sum_parts<DT, 1>, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, a);
 }
 
 // 16 bytes of dst a thread. Bound by memory. (Divided in 32 bits where they do.)
@@ -143,11 +146,7 @@ __global__ __launch_bounds__(256) void k_pad_rows(const E* __restrict__ src, int
 }  // namespace
 
 hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s) {
-    // whole 16-byte words of sums, each in one row and half, or one at a time
-    if (a.half_p % 4 == 0)
-        (dt == kF16 ? sum_parts<kF16, 4> : sum_parts<kBF16, 4>)(a, s);
-    else
-        (dt == kF16 ? sum_parts<kF16, 1> : sum_parts<kBF16, 1>)(a, s);
+    (dt == kF16 ? sum_parts<kF16> : sum_parts<kBF16>)(a, s);
     return hipGetLastError();
 }
 

@@ -33,6 +33,8 @@ namespace {
 //   Mid 9.8 / 10.4 / 13.2 / 15.0; with 2048 -> 512, 6,000 / 12,000: 21.5 / 34.0, 23.9 / 28.8
 //   91,000 x 128 -> 64 / 128 with a residual: Rows 13.2 / 14.7, Mid 15.0 / 15.0
 //   (without one 11.6 / 12.2, 12.0 / 11.5)
+// (With three steps in flight and two blocks a CU: 2048 -> 512, 3,000 rows 18.0, but
+// 512 -> 512, 6,000 and 8,000 rows 10.2 and 10.8 against 9.5 and 9.7.)
 // Unaligned operands, which go through registers, leave Mid too few of them.
 // Gated: Wide, 32 x 64 a wave, twice the waves to overlap the epilogues of both
 // halves; long 16-bit contractions in Mid, whose waves read less from LDS for a
