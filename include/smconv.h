@@ -482,8 +482,9 @@ int smc_version(void);
  * scratch memory take it from the caller, and calls on several streams with
  * their own scratch do not touch each other. n = 0 is valid (gradients of
  * weights are then zeros). Outputs may not overlap inputs, except y = residual
- * (smc_linear) and s = x or residual, y = x (smc_rms_norm) with equal
- * addresses and row distances.
+ * (smc_linear) and s = x or residual, 16-bit y = x (smc_rms_norm), with equal
+ * addresses and row distances. e4m3 y that shares memory with x, residual or s is
+ * refused (SMC_ERR_ARG).
  *
  * Sums, norms and pre-activations are float32; every output is rounded once
  * (to nearest, ties to even) from float32. The backward passes keep nothing of

@@ -43,6 +43,20 @@ int check_rows(const char* name, const void* p, int64_t rows, int64_t cols, int6
     return SMC_OK;
 }
 
+// Do the [rows, cols] tensors at p and q (es bytes an element, ld elements from
+// row to row) share memory? Columns of one buffer, whose ranges overlap with equal
+// row distances in bytes, are told apart; other overlapping ranges count as shared.
+bool share_memory(const void* p, int64_t ldp, int esp, const void* q, int64_t ldq, int esq, int64_t rows,
+                  int64_t cols) {
+    if (!p || !q || rows <= 0) return false;
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    const uint64_t pitch = (uint64_t)ldp * esp, wp = (uint64_t)cols * esp, wq = (uint64_t)cols * esq;
+    if (a + (uint64_t)(rows - 1) * pitch + wp <= b || b + (uint64_t)(rows - 1) * ldq * esq + wq <= a) return false;
+    if (pitch != (uint64_t)ldq * esq) return true;
+    const uint64_t apart = a > b ? (pitch - (a - b) % pitch) % pitch : (b - a) % pitch;    // q's columns after p's
+    return apart < wp || apart + wq > pitch;
+}
+
 int check_common(int64_t n, int64_t c, const char* cname, int dtype) {
     if (n < 0 || n > kMaxRows) return bad(SMC_ERR_ARG, "n = %lld", (long long)n);
     if (c < 1 || c > kMaxDim) return bad(SMC_ERR_ARG, "%s = %lld outside [1, 2^21]", cname, (long long)c);
@@ -376,6 +390,12 @@ int smc_rms_norm(const smc_norm_t* a, void* stream) {
     if (a->ldy < a->c || a->ldy > kMaxDim)
         return bad(SMC_ERR_ARG, "row distance of y is %lld, outside [%d, 2^21]", (long long)a->ldy, a->c);
     if (!a->y_scale && ((uintptr_t)a->y & 1)) return bad(SMC_ERR_ARG, "y is not aligned to its elements");
+    // e4m3 rows over 16-bit ones: a row of y would lie in other rows' bytes, which
+    // another wave may not have read
+    if (a->y_scale && (share_memory(a->y, a->ldy, 1, a->x, a->ldx, 2, a->n, a->c) ||
+                       share_memory(a->y, a->ldy, 1, a->residual, a->ld_residual, 2, a->n, a->c) ||
+                       share_memory(a->y, a->ldy, 1, a->s, a->lds, 2, a->n, a->c)))
+        return bad(SMC_ERR_ARG, "e4m3 y shares memory with x, residual or s");
     NormArgs p;
     p.n = a->n;
     p.c = a->c;

@@ -1,0 +1,69 @@
+"""Host rules of the row operators that need no GPU: overlapping buffers and the
+sizes of scratch memory. The addresses below are never read: a call that passes
+the argument checks ends at the missing device."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import submanifold_sparse_convolution_amd as smc
+
+SMC_ERR_ARG = 1
+BASE = 1 << 20
+
+
+def norm(**kw):
+    a = smc.NormArgs(8, 64, 0, 1e-6, BASE, 64, None, 0, BASE << 4, BASE << 5, 64, BASE << 6, None, 0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+# y e4m3 (one byte an element) against x, residual and s (two bytes): 8 rows of 64
+SHARED = [
+    dict(y=BASE),                                               # row r of y over row r / 2 of x
+    dict(y=BASE, ldy=128),                                      # equal distances in bytes
+    dict(y=BASE + 64, ldy=128),                                 # the second half of each row of x
+    dict(y=BASE + 8 * 128 - 1),                                 # the last byte of x
+    dict(y=BASE - 8 * 64 + 1),                                  # y's last byte
+    dict(residual=BASE << 5, ld_residual=64),
+    dict(s=BASE << 5, lds=64),
+]
+APART = [
+    dict(y=BASE + 8 * 128),                                     # right after x
+    dict(y=BASE - 8 * 64),                                      # right before it
+    dict(y=BASE + 128, ldy=256, ldx=128),                       # columns of one buffer
+    dict(y=BASE - 64, ldy=256, ldx=128),
+    dict(residual=BASE, ld_residual=64, s=BASE, lds=64),        # in place, y elsewhere
+]
+
+
+@pytest.fixture(scope="module")
+def answers():
+    """Status and message of every call, from a process that sees no device (and
+    makes no call if it does)."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = %r\n"
+            "import ctypes, torch, test_rowops_host_cpu as t\n"
+            "import submanifold_sparse_convolution_amd as smc\n"
+            "assert torch.cuda.device_count() == 0\n"
+            "for kw in t.SHARED + t.APART:\n"
+            "    rc = smc.lib().smc_rms_norm(ctypes.byref(t.norm(**kw)), None)\n"
+            "    print(rc, smc.lib().smc_last_error().decode())\n" % [here, os.path.dirname(here)])
+    env = dict(os.environ, HIP_VISIBLE_DEVICES="-1")
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=300)
+    assert out.returncode == 0, out.stdout + out.stderr
+    return [(int(line.partition(" ")[0]), line.partition(" ")[2]) for line in out.stdout.strip().splitlines()]
+
+
+@pytest.mark.parametrize("i", range(len(SHARED)))
+def test_e4m3_rows_that_share_memory_are_refused(answers, i):
+    rc, msg = answers[i]
+    assert rc == SMC_ERR_ARG and "shares memory" in msg, (SHARED[i], rc, msg)
+
+
+@pytest.mark.parametrize("i", range(len(APART)))
+def test_e4m3_rows_beside_the_inputs_pass_the_checks(answers, i):
+    rc, msg = answers[len(SHARED) + i]
+    assert rc != SMC_ERR_ARG, (APART[i], rc, msg)
