@@ -490,8 +490,11 @@ int smc_version(void);
  * (to nearest, ties to even) from float32. The backward passes keep nothing of
  * the forward pass but its inputs: pre-activations are computed again, and
  * the gradient dz that reaches them is rounded to `dtype` in the scratch
- * memory, as it is the operand of two MFMA products. Sums have a fixed order:
- * equal inputs give equal bits.
+ * memory, as it is the operand of two MFMA products. Where f16 cannot hold it
+ * (its largest value is above 65504, or below 2^-8) it is kept there times a
+ * power of two, found on the device: finite gradients that fit f16 come out
+ * finite, at the cost of the first of the three products a second time. Sums have
+ * a fixed order: equal inputs give equal bits.
  * ------------------------------------------------------------------------- */
 enum {
     SMC_DTYPE_BF16 = 0,

@@ -46,6 +46,11 @@ struct ProductArgs {
     int k_split = 0;            // contraction length of a split (all of k: one split)
     int splits = 1;
     int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
+    // f16 slopes, whose rows are written times a power of two (see range_scale):
+    float* dz_max = nullptr;          // one a block, the largest finite |dz|: written by the first
+                                      // launch, read by the second, which
+    float* dz_unscale = nullptr;      // writes the inverse scale here (null: the first launch)
+    const float* unscale = nullptr;   // f16 input gradient: its sums are multiplied by this
     int act = 0;
     int vec_a = 0, vec_b = 0;   // 16-byte loads are possible
     int vec_x = 0;              // a row of extra has a whole 16-byte word
@@ -60,6 +65,7 @@ int device_cus();
 
 // out = product (see ProductArgs); dt: type of out, bias and extra, and of a
 // and b unless e4m3 (whose b lies along k or across it). Fills in the tile walk.
+constexpr int kMaxBlocksPerCu = 3;      // blocks of a product kernel, at most, for each CU
 constexpr int kFewRows = 16;    // forward 16-bit products of up to as many rows have a kernel of their own
 hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w_along, hipStream_t s);
 // dx = dz W^T: both operands along k.
@@ -78,6 +84,7 @@ struct SumArgs {
     void* dw = nullptr;
     int64_t ldw = 0;
     void* db = nullptr;         // or null
+    const float* unscale = nullptr;     // factor of the sums (or null)
 };
 hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s);
 // dst [rows_p, ldd] = src [rows, halves c] with each half at a multiple of half_p

@@ -228,7 +228,7 @@ int forward(const smc_product_t* a, int halves, Epilogue epi, void* stream) {
 // Scratch of a backward pass. Its products read x, w, dz or dy as 16-byte words;
 // where their rows are not made of such, padded copies take their place: xp
 // [n, c_in_p], wp [c_in_p, halves half_p] and the bias alike, zeros between; dz has
-// wp's columns. (Through registers instead, us on the GPU: gated 144 -> 734 with 8 /
+// wp's columns; f16: the slopes' maxima and their scale. (Through registers instead, us on the GPU: gated 144 -> 734 with 8 /
 // 256 / 4,818 rows 45.7 / 49.3 / 92.6, with the copies 24.6 / 27.0 / 43.0.) Then the
 // weight gradient's float32 sums.
 struct Scratch {
@@ -236,7 +236,7 @@ struct Scratch {
     bool copy_x = false, copy_w = false, copy_dy = false;
     int half_p = 0, c_in_p = 0; // columns of a half of dz, w; of x
     int wide_p = 0;
-    size_t xp = 0, wp = 0, bp = 0, dz = 0, part = 0, bytes = 0;     // offsets
+    size_t xp = 0, wp = 0, bp = 0, dz = 0, range = 0, part = 0, bytes = 0;      // offsets
     int splits = 1;
 };
 
@@ -263,6 +263,7 @@ Scratch scratch_of(const smc_product_t* a, int halves) {
     if (s.copy_w) s.wp = take((size_t)s.c_in_p * s.wide_p * 2);
     if (s.copy_w && a->bias) s.bp = take((size_t)s.wide_p * 2);
     if (s.slope || s.copy_dy) s.dz = take((size_t)a->n * ((s.wide_p + 7) / 8 * 8) * 2);
+    if (s.slope && a->dtype == SMC_DTYPE_F16) s.range = take((size_t)(1 + kMaxBlocksPerCu * device_cus()) * 4);
     s.splits = weight_gradient_splits(a->n, a->c_in, s.wide_p);
     s.part = take((size_t)s.splits * (a->c_in + (a->db ? 1 : 0)) * s.wide_p * 4);
     return s;
@@ -295,6 +296,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
     if (a->n == 0) return hip_status(launch_sum_parts(sum, a->dtype, s), name);
 
     const void *x = a->x, *w = a->w, *bias = a->bias, *dz = a->dy;
+    const float* unscale = nullptr;
     int64_t ldx = a->ldx, ldw = a->ldw, ld_dz = a->ld_dy;
     if (sc.copy_x) {
         CHECK(hip_status(launch_pad_rows(2, x, ldx, a->n, 1, a->c_in, ws + sc.xp, sc.c_in_p, a->n, sc.c_in_p, s), name));
@@ -332,7 +334,16 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.vec_a = words16(x, ldx) && sc.c_in_p % 8 == 0;
         p.vec_b = words16(w, ldw) && (halves == 1 || sc.half_p % 8 == 0);
         p.vec_x = a->c_out >= 8;
-        CHECK(hip_status(launch_forward(p, halves == 2 ? kEpiGatedSlope : kEpiSlope, a->dtype, false, false, s), name));
+        const Epilogue epi = halves == 2 ? kEpiGatedSlope : kEpiSlope;
+        const bool f16 = a->dtype == SMC_DTYPE_F16;
+        float* const range = reinterpret_cast<float*>(ws + sc.range);
+        if (f16) p.dz_max = range + 1;
+        CHECK(hip_status(launch_forward(p, epi, a->dtype, false, false, s), name));
+        if (f16) {
+            p.dz_unscale = range;
+            CHECK(hip_status(launch_forward(p, epi, a->dtype, false, false, s), name));
+            unscale = range;
+        }
         dz = p.out;
         ld_dz = p.ldo;
     } else if (sc.copy_dy) {
@@ -349,6 +360,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
         p.m = (int)a->n;
         p.k = sc.wide_p;
         p.n = a->c_in;
+        p.unscale = unscale;
         p.out = a->dx;
         p.ldo = a->ld_dx;
         p.vec_a = words16(dz, ld_dz) && sc.wide_p % 8 == 0;
@@ -371,6 +383,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
     CHECK(hip_status(launch_weight_gradient(p, a->dtype, s), name));
     sum.part = p.part;
     sum.splits = sc.splits;
+    sum.unscale = unscale;
     return hip_status(launch_sum_parts(sum, a->dtype, s), name);
 }
 

@@ -101,13 +101,14 @@ __global__ __launch_bounds__(256) void k_sum_parts(SumArgs a) {
             for (int e = 0; e < W; ++e) v[e] += s_v[o][x * W + e];
     }
     if (i >= total) return;
+    const float by = a.unscale ? *a.unscale : 1.f;
     const int64_t row = i / a.n;
     const int col = (int)(i - row * a.n), h = col / a.half_p, c = col - h * a.half_p;   // (a word lies in one half)
     uint16_t* o = row < a.m ? static_cast<uint16_t*>(a.dw) + row * a.ldw : static_cast<uint16_t*>(a.db);
     o += h * a.c_out + c;
 #pragma unroll
     for (int e = 0; e < W; ++e)
-        if (c + e < a.c_out) o[e] = (uint16_t)from_f32<DT>(v[e]);
+        if (c + e < a.c_out) o[e] = (uint16_t)from_f32<DT>(v[e] * by);
 }
 
 template <int DT>

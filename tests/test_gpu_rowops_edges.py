@@ -85,3 +85,129 @@ def test_e4m3_norm_beside_its_input():
     q, want = smc.rms_norm(before, w, e4m3=True)
     assert torch.equal(y.view(torch.uint8), q.view(torch.uint8)) and torch.equal(scale, want)
     assert torch.equal(x, before) and torch.all(buf[:, 3 * c:] == 0)
+
+
+# ---- f16 gradients whose dz is outside f16 ------------------------------------------
+
+
+def d(t):
+    return None if t is None else t.double()
+
+
+def f16_gradients(halves, dy, x, w, b, name):
+    """dz and (dx, dw, db) in 64 bits with the bounds of _rowops, where the stored dz
+    is within half an ulp of f16 and 2^-17 of its largest value: the smallest step
+    of f16 is 2^-24, and a largest value below 2^-8 is scaled up first."""
+    back = ro.linear_backward if halves == 1 else ro.gated_backward
+    z, _ = ro.pre(d(x), d(w), d(b))
+    if halves == 1:
+        dz = d(dy) * ro.slope(z, name)
+    else:
+        f = dy.shape[1]
+        dz = torch.cat((d(dy) * z[:, f:] * ro.slope(z[:, :f], name), d(dy) * ro.act(z[:, :f], name)), 1)
+    floor = ro.FLOOR[F16]
+    try:                                    # the rounding floor of dz: 2^-17 of the largest
+        ro.FLOOR[F16] = float(dz.abs().max()) * 2.0 ** -17
+        wide = back(d(dy), d(x), d(w), d(b), name, F16)
+    finally:
+        own = ro.FLOOR[F16]
+        ro.FLOOR[F16] = floor
+    return dz, [(v, bd - own + floor) for v, bd in wide]
+
+
+# (rows, c_in, c_out): one tile, several, odd sizes, all tile shapes of the slopes
+RANGE_SHAPES = [(1, 16, 24), (40, 72, 33), (300, 128, 96), (2500, 64, 200), (9000, 64, 264), (3000, 512, 520)]
+
+
+@pytest.mark.parametrize("n,c_in,c_out", RANGE_SHAPES)
+@pytest.mark.parametrize("name", ["silu", "gelu", None])
+def test_f16_gradients_with_large_dz(n, c_in, c_out, name):
+    """dh times the up half is up to 10^6 or so, small weights bring dx, dW and
+    db back into f16."""
+    g = gen(n + c_in)
+    x = normal(g, (n, c_in), 0.02, F16)
+    w = normal(g, (c_in, 2 * c_out), 2.0 ** -9 / n ** 0.5, F16)
+    b = torch.cat((torch.full((c_out,), 2.0), torch.full((c_out,), 500.0))).to(F16)
+    dh = (normal(g, (n, c_out), 0.02, F16).float() + 1).to(F16)
+    dh[0, 0], dh[n // 2, c_out // 2] = 400.0, -300.0
+    sign = torch.where(torch.rand(n, c_out, generator=g) < 0.5, -1.0, 1.0)
+    dh = (dh.float() * sign / n ** 0.5).to(F16)
+    dh[n - 1, c_out - 1] = 300.0            # times 500: 150,000 or so, beyond f16
+    dz, want = f16_gradients(2, dh, x, w, b, name)
+    assert dz.abs().max() > 65504 * 1.5
+    assert all(v.abs().max() < 65504 for v, _ in want[:2])
+    got = smc.gated_backward(dh.cuda(), x.cuda(), w.cuda(), bias=b.cuda(), activation=name)
+    for v, (wv, bd), label in zip(got[:2], want[:2], ("dx", "dw")):
+        assert torch.isfinite(v).all(), label
+        ro.check(v, wv, bd, label)
+    keep = want[2][0].abs() < 65000         # a column sum may itself be beyond f16
+    ro.check(got[2][keep.cuda()], want[2][0][keep], want[2][1][keep], "db")
+    assert keep.sum() >= c_out
+
+
+@pytest.mark.parametrize("n,c_in,c_out", RANGE_SHAPES)
+@pytest.mark.parametrize("halves", [1, 2])
+def test_f16_gradients_with_small_dz(n, c_in, c_out, halves):
+    """A loss that nobody scaled: every dz is below f16's normal range, the
+    gradients of the weights (x of 2,000) and of x (weights of 30) are not."""
+    g = gen(n + c_in + halves)
+    x = normal(g, (n, c_in), 2000.0, F16)
+    w = normal(g, (c_in, halves * c_out), 30.0, F16)
+    w = (w.float() * (torch.rand(w.shape, generator=g) < 1e-3)).to(F16)       # few: |z| stays small
+    w[0] = 30.0
+    x[:, 0] = normal(g, (n,), 2.0 ** -5, F16)
+    dy = normal(g, (n, c_out), 2.0 ** -21, F16)
+    dz, want = f16_gradients(halves, dy, x, w, None, "silu")
+    back = smc.linear_backward if halves == 1 else smc.gated_backward
+    got = back(dy.cuda(), x.cuda(), w.cuda(), activation="silu")
+    for v, (wv, bd), label in zip(got, want, ("dx", "dw")):
+        ro.check(v, wv, bd, label)
+
+
+def test_f16_gradients_with_an_infinity():
+    """One row of dy at infinity: its dx is not finite, every other row's is what
+    it is without that row, also where dz is beyond f16."""
+    g = gen(3)
+    n, c_in, c_out = 300, 64, 72
+    x, w = normal(g, (n, c_in), 0.1, F16), normal(g, (c_in, 2 * c_out), 2.0 ** -10, F16)
+    b = torch.full((2 * c_out,), 300.0).to(F16)
+    for size in (1.0, 500.0):
+        dh = normal(g, (n, c_out), size, F16)
+        clean = smc.gated_backward(dh.cuda(), x.cuda(), w.cuda(), bias=b.cuda())[0]
+        assert torch.isfinite(clean).all()
+        bad = dh.clone()
+        bad[17, 5] = float("inf")
+        dx = smc.gated_backward(bad.cuda(), x.cuda(), w.cuda(), bias=b.cuda())[0]
+        keep = [i for i in range(n) if i != 17]
+        assert not torch.isfinite(dx[17]).all()
+        # (the largest finite value may be another one: a different power of two,
+        # which the smallest values' rounding sees)
+        top = clean.abs().max().item()
+        assert (dx[keep].float() - clean[keep].float()).abs().max() <= 2.0 ** -10 * top
+
+
+def test_f16_gradients_scale_in_a_graph():
+    """The scale is found on the device: replays with small, ordinary and large
+    gradients give the eager bits."""
+    g = gen(4)
+    n, c_in, c_out = 700, 64, 72
+    x, w = normal(g, (n, c_in), 0.1, F16).cuda(), normal(g, (c_in, 2 * c_out), 2.0 ** -8, F16).cuda()
+    b = torch.full((2 * c_out,), 300.0).to(F16).cuda()
+    dh = torch.zeros(n, c_out, dtype=F16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        smc.gated_backward(dh, x, w, bias=b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = smc.gated_backward(dh, x, w, bias=b)
+    for k, size in enumerate((1.0, 400.0, 2.0 ** -20, 0.1, 300.0)):
+        fresh = normal(gen(50 + k), (n, c_out), size, F16).cuda()
+        want = smc.gated_backward(fresh, x, w, bias=b)
+        torch.cuda.synchronize()
+        dh.copy_(fresh)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(out, want)), size
+        assert torch.isfinite(out[0]).all()
