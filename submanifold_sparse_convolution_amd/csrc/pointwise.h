@@ -43,7 +43,7 @@ struct ProductArgs {
     void* out = nullptr;        // [m, n] ([m, half] for kEpiGated)
     int64_t ldo = 0;
     float* part = nullptr;      // kEpiPartial: [splits][m + colsum][n]
-    int k_split = 0;            // contraction length of a split (all of k: one split)
+    int k_split = 0;            // contraction length of a split (all of k: one split; none is empty)
     int splits = 1;
     int colsum = 0;             // kEpiPartial: row m of a split's sums is the sum of b over k
     // f16 slopes, whose rows are written times a power of two (see range_scale):
@@ -71,8 +71,8 @@ hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w
 // dx = dz W^T: both operands along k.
 hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s);
 // dW = x^T dz (both operands across k) and, with colsum, db: float32 sums of
-// `splits` ranges of the rows, added and rounded by launch_sum_parts.
-int weight_gradient_splits(int64_t rows, int c_in, int n);
+// `splits` ranges of k_split rows, added and rounded by launch_sum_parts.
+int weight_gradient_range(int64_t rows, int c_in, int n);      // rows of a range (0 for no rows)
 hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s);
 // The sums have n = halves half_p columns; column c < c_out of half h goes to
 // column h c_out + c of dw (and db).

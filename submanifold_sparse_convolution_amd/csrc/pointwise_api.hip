@@ -237,7 +237,7 @@ struct Scratch {
     int half_p = 0, c_in_p = 0; // columns of a half of dz, w; of x
     int wide_p = 0;
     size_t xp = 0, wp = 0, bp = 0, dz = 0, range = 0, part = 0, bytes = 0;      // offsets
-    int splits = 1;
+    int range_rows = 0, splits = 1;     // ranges of the rows that dW is summed over
 };
 
 Scratch scratch_of(const smc_product_t* a, int halves) {
@@ -264,7 +264,8 @@ Scratch scratch_of(const smc_product_t* a, int halves) {
     if (s.copy_w && a->bias) s.bp = take((size_t)s.wide_p * 2);
     if (s.slope || s.copy_dy) s.dz = take((size_t)a->n * ((s.wide_p + 7) / 8 * 8) * 2);
     if (s.slope && a->dtype == SMC_DTYPE_F16) s.range = take((size_t)(1 + kMaxBlocksPerCu * device_cus()) * 4);
-    s.splits = weight_gradient_splits(a->n, a->c_in, s.wide_p);
+    s.range_rows = weight_gradient_range(a->n, a->c_in, s.wide_p);
+    if (a->n > 0) s.splits = (int)((a->n + s.range_rows - 1) / s.range_rows);
     s.part = take((size_t)s.splits * (a->c_in + (a->db ? 1 : 0)) * s.wide_p * 4);
     return s;
 }
@@ -376,6 +377,7 @@ int backward(const smc_product_t* a, int halves, void* stream) {
     p.k = (int)a->n;
     p.n = sc.wide_p;
     p.part = reinterpret_cast<float*>(ws + sc.part);
+    p.k_split = sc.range_rows;
     p.splits = sc.splits;
     p.colsum = a->db != nullptr;
     p.vec_a = words16(x, ldx);

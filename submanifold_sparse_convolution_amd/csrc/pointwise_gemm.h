@@ -626,7 +626,7 @@ struct Place {
         m0 = tm * T::BM;
         k0 = split * p.k_split;
         k_len = p.k - k0 < p.k_split ? p.k - k0 : p.k_split;
-        steps = k_len > 0 ? (k_len + step_k - 1) / step_k : 0;
+        steps = (k_len + step_k - 1) / step_k;      // at least one
     }
 };
 
@@ -732,12 +732,11 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
     };
     // moves on to a step that exists; false when the walk is over
     auto next_step = [&]() SMC_INLINE {
-        while (ahead_step >= ahead.steps) {             // (a split may be empty)
-            if (ahead.t + t_step >= t_end) return false;
-            const int tm = ahead.tm, tn = ahead.tn;
-            ahead.advance(p, t_step, kStep);
-            enter(false, ahead.tm != tm, ahead.tn != tn);
-        }
+        if (ahead_step < ahead.steps) return true;
+        if (ahead.t + t_step >= t_end) return false;
+        const int tm = ahead.tm, tn = ahead.tn;
+        ahead.advance(p, t_step, kStep);
+        enter(false, ahead.tm != tm, ahead.tn != tn);
         return true;
     };
     auto step_left = [&]() SMC_INLINE {                 // contraction elements of it
@@ -943,14 +942,11 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
         // What the epilogue reads is loaded beside it, two steps before a wait
         // includes it.
         if constexpr (ALIGNED) {
-            int step = 0;
-            if (here.steps > 0) {
-                arrive();
-                load_epilogue();
-                if (kHasExtra && p.extra && p.vec_x) ops += MT * kPairs;
-                compute();
-                ++step;
-            }
+            arrive();
+            load_epilogue();
+            if (kHasExtra && p.extra && p.vec_x) ops += MT * kPairs;
+            compute();
+            int step = 1;
             // the step issued is a whole one of this tile
             const int main_steps = here.k_len / kStep - (S - 1);
 #pragma unroll 1
@@ -1120,6 +1116,8 @@ hipError_t launch_product(ProductArgs p, hipStream_t s) {
     const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     if (total <= 0) return hipSuccess;
     if (total > 0x7fffffff) return hipErrorInvalidValue;
+    // the walk counts on a step in every tile
+    if (p.k_split <= 0 || (int64_t)(p.splits - 1) * p.k_split >= p.k) return hipErrorInvalidValue;
     // row tiles a group: 1 MiB of a at most, a quarter of an XCD's L2 (columns
     // fastest over single row tiles, b was read from memory again for nearly
     // every row tile: 15,000 x 512 -> 4096 backward 380 MB of fetches)

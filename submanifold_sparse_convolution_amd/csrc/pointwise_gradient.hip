@@ -50,15 +50,16 @@ hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s) {
 // 144 -> 832 61.7 us, 40.5 so; 5,172 x 336 -> 1824 20.7, 16.7), none shorter than 256
 // rows (4 steps), so that a tile's sums (64 KiB to memory and back) stay small
 // beside the rows it reads.
-int weight_gradient_splits(int64_t rows, int c_in, int n) {
+// A range is whole steps (64 rows), and every range has rows: rounding their length
+// up may take fewer of them.
+int weight_gradient_range(int64_t rows, int c_in, int n) {
     const int64_t tiles = (int64_t)((c_in + 127) / 128) * ((n + 127) / 128);
     const int64_t want = 2 * device_cus() / tiles;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, (rows + 255) / 256));
+    const int64_t ranges = std::max<int64_t>(1, std::min<int64_t>(want, (rows + 255) / 256));
+    return (int)(((rows + ranges - 1) / ranges + 63) / 64 * 64);
 }
 
 hipError_t launch_weight_gradient(ProductArgs p, int dt, hipStream_t s) {
-    const int64_t per = ((int64_t)p.k + p.splits - 1) / p.splits;
-    p.k_split = (int)((per + 63) / 64 * 64);
     return dt == kF16 ? launch_product<kF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s)
                       : launch_product<kBF16, false, kAcrossK, kAcrossK, kEpiPartial, TileMid>(p, s);
 }

@@ -211,3 +211,30 @@ def test_f16_gradients_scale_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, want)), size
         assert torch.isfinite(out[0]).all()
+
+
+# ---- weight gradients over long row ranges --------------------------------------------
+# Integers: every product and sum is exact in float32, so dw and db are equal bit
+# for bit. The first four have as many ranges of the rows as the device takes (more
+# than 256 rows each, the last one short); the last has more tiles than blocks.
+
+
+@pytest.mark.parametrize("n,c_in,c_out,halves", [(91000, 128, 344, 2), (95000, 144, 256, 1), (131584, 128, 128, 1),
+                                                 (15000, 512, 520, 2), (300, 3000, 3100, 1)])
+def test_weight_gradient_ranges(n, c_in, c_out, halves):
+    g = gen(n + c_in)
+    x = torch.randint(-1, 2, (n, c_in), generator=g).to(BF16)
+    dy = torch.randint(-1, 2, (n, c_out), generator=g).to(BF16)
+    if halves == 1:
+        w = torch.randint(-1, 2, (c_in, c_out), generator=g).to(BF16)
+        b = torch.zeros(c_out, dtype=BF16)
+        dz = dy.float()
+        got = smc.linear_backward(dy.cuda(), x.cuda(), w.cuda(), bias=b.cuda())
+    else:                                   # gate 2, up 1 for every row: dz = (dh, 2 dh)
+        w = torch.zeros(c_in, 2 * c_out, dtype=BF16)
+        b = torch.cat((torch.full((c_out,), 2.0), torch.full((c_out,), 1.0))).to(BF16)
+        dz = torch.cat((dy.float(), 2 * dy.float()), 1)
+        got = smc.gated_backward(dy.cuda(), x.cuda(), w.cuda(), bias=b.cuda(), activation="relu")
+    assert torch.equal(got[0].cpu(), (dz @ w.float().t()).to(BF16))
+    assert torch.equal(got[1].cpu(), (x.float().t() @ dz).to(BF16))
+    assert torch.equal(got[2].cpu(), dz.sum(0).to(BF16))

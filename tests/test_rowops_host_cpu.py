@@ -67,3 +67,17 @@ def test_e4m3_rows_that_share_memory_are_refused(answers, i):
 def test_e4m3_rows_beside_the_inputs_pass_the_checks(answers, i):
     rc, msg = answers[len(SHARED) + i]
     assert rc != SMC_ERR_ARG, (APART[i], rc, msg)
+
+
+@pytest.mark.parametrize("n,c_in,c_out", [(1, 8, 8), (257, 8, 8), (15000, 2048, 512), (15000, 512, 4096),
+                                          (91000, 128, 688), (95000, 144, 256), (131584, 128, 128),
+                                          (1000000, 64, 64), (300, 3000, 3104)])
+def test_every_range_of_a_weight_gradient_has_rows(n, c_in, c_out):
+    """Aligned operands and no activation: the scratch memory holds the ranges' sums
+    alone. A range is a multiple of 64 rows; the last one begins before row n."""
+    a = smc.ProductArgs(n, c_in, c_out, 0, 0, 0, BASE, c_in, None, BASE, c_out)
+    a.dy, a.ld_dy, a.dx, a.ld_dx, a.dw, a.ld_dw = BASE, c_out, BASE, c_in, BASE, c_out
+    ranges, rest = divmod(smc.lib().smc_linear_backward_workspace(a), c_in * c_out * 4)
+    assert ranges >= 1 and rest == 0
+    length = -(-(-(-n // ranges)) // 64) * 64
+    assert (ranges - 1) * length < n, f"{ranges} ranges of {length} rows for {n}"
