@@ -515,7 +515,10 @@ enum {
  * The norm is taken of the float32 sum, before s is rounded. With y_scale the
  * rows go out as e4m3: y_scale[i] = max(max_c |y[i, c]| / 448, 2^-126) and
  * y[i, c] = e4m3(y[i, c] / y_scale[i]), what smc_linear and smc_gated read. A
- * row with a NaN gets a NaN scale; a row of zeros stays zeros.
+ * row with a NaN gets a NaN scale; a row of zeros stays zeros, also with eps = 0
+ * (its gradient is then ds alone). The sum of squares is float32: rows whose
+ * squares pass its range (bf16 values beyond 2^63) come out as zeros, and with
+ * eps = 0 rows whose squares all fall below it count as zeros.
  */
 typedef struct smc_norm_s {
     int64_t n;                /* rows */

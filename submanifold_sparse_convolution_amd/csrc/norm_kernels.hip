@@ -78,6 +78,9 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     return s < kTinyScale ? kTinyScale : s;        // NaN stays
 }
 
+// 1 / sqrt(v); a row of zeros without an epsilon stays zeros.
+__device__ __forceinline__ float inverse_root(float v) { return v == 0.f ? 0.f : 1.f / sqrtf(v); }
+
 // L lanes a row, NV words of W elements a lane, the row in registers.
 template <int DT, bool A, int L, int NV>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
             if (ok && c < a.c) store_16<DT, A>(a.s, row * a.lds + c, a.c - c, v[j]);
         }
     }
-    const float rstd = 1.f / sqrtf(lane_sum<L>(ss) / (float)a.c + a.eps);
+    const float rstd = inverse_root(lane_sum<L>(ss) / (float)a.c + a.eps);
     uint32_t amax = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < W; ++e) ss += v[e] * v[e];
     }
-    const float rstd = 1.f / sqrtf(block_sum(ss, s_sum) / (float)a.c + a.eps);
+    const float rstd = inverse_root(block_sum(ss, s_sum) / (float)a.c + a.eps);
     uint32_t amax = 0;
     for (int pass = a.y_scale ? 0 : 1; pass < 2; ++pass) {
         float scale = 1.f;
@@ -251,7 +254,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward(NormArgs a) {
             }
         ss = lane_sum<L>(ss);
         dot = lane_sum<L>(dot);
-        const float rstd = 1.f / sqrtf(ss / (float)a.c + a.eps);
+        const float rstd = inverse_root(ss / (float)a.c + a.eps);
         const float mean = dot * rstd / (float)a.c;        // mean(a x_hat)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_backward_wide(NormArgs a)
                 dot += dy[e] * w[e] * x[e];
             }
         }
-        const float rstd = 1.f / sqrtf(block_sum(ss, s_sum) / (float)a.c + a.eps);
+        const float rstd = inverse_root(block_sum(ss, s_sum) / (float)a.c + a.eps);
         const float mean = block_sum(dot, s_sum) * rstd / (float)a.c;
         for (int c = threadIdx.x * W; c < a.c; c += kNormThreads * W) {
             float x[W], dy[W], w[W], o[W], ds[W];

@@ -238,3 +238,35 @@ def test_weight_gradient_ranges(n, c_in, c_out, halves):
     assert torch.equal(got[0].cpu(), (dz @ w.float().t()).to(BF16))
     assert torch.equal(got[1].cpu(), (x.float().t() @ dz).to(BF16))
     assert torch.equal(got[2].cpu(), dz.sum(0).to(BF16))
+
+
+# ---- rows of zeros without an epsilon ---------------------------------------------------
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("n,c", [(5, 7), (40, 128), (9, 512), (6, 1000), (4, 4104), (3, 4099)])
+def test_norm_of_zero_rows_without_epsilon(n, c, dt):
+    """eps = 0: a row of zeros stays zeros, in e4m3 with the smallest scale; its
+    gradient is ds alone and it adds nothing to dweight. The other rows are as
+    the formulas say."""
+    g = gen(n * c)
+    x, w, dy, ds = (normal(g, s, v, dt) for s, v in (((n, c), 1.0), ((c,), 1.0), ((n, c), 0.2), ((n, c), 0.5)))
+    zero = torch.zeros(n, dtype=torch.bool)
+    zero[::2] = True
+    x[zero] = 0
+    y, s = smc.rms_norm(x.cuda(), w.cuda(), residual=torch.zeros_like(x).cuda(), eps=0.0)
+    assert torch.all(y[zero.cuda()] == 0) and torch.equal(s.cpu(), x)
+    want, rel, _ = ro.norm(d(x[~zero]), None, d(w), 0.0)
+    ro.check(y[(~zero).cuda()], want, ro.rounded(want, rel * want.abs(), dt), "y")
+    q, scale = smc.rms_norm(x.cuda(), w.cuda(), eps=0.0, e4m3=True)
+    q, scale = q.cpu().float(), scale.cpu()
+    assert torch.all(q[zero] == 0) and torch.all(scale[zero] == 2.0 ** -126)
+    assert torch.all(q[~zero].abs().amax(1) == 448)
+    for extra in (None, ds):
+        dx, dw = smc.rms_norm_backward(dy.cuda(), x.cuda(), w.cuda(), eps=0.0, ds=None if extra is None else ds.cuda())
+        at = zero.cuda()
+        assert torch.equal(dx[at].cpu(), ds[zero]) if extra is not None else torch.all(dx[at] == 0)
+        (wx, bx), (ww, bw) = ro.norm_backward(d(dy[~zero]), d(x[~zero]), d(w), 0.0,
+                                              None if extra is None else d(ds[~zero]), dt)
+        ro.check(dx[~at], wx, bx, "dx")
+        ro.check(dw, ww, bw, "dweight")
