@@ -20,7 +20,7 @@
 namespace smc {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;       // what grid_of counts on
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;      // 2^-126
 
@@ -85,7 +85,7 @@ __device__ __forceinline__ float inverse_root(float v) { return v == 0.f ? 0.f :
 template <int DT, bool A, int L, int NV>
 __global__ __launch_bounds__(kNormThreads) void k_norm(NormArgs a) {
     const int lane = threadIdx.x % L;
-    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+    const int64_t row = block_number() * (kNormThreads / L) + threadIdx.x / L;
     const bool ok = row < a.n;
     float v[NV][W];
     float ss = 0.f;
@@ -155,7 +155,8 @@ template <int DT, bool A>
 __global__ __launch_bounds__(kNormThreads) void k_norm_wide(NormArgs a) {
     __shared__ float s_sum[4];
     __shared__ uint32_t s_max[4];
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_number();
+    if (row >= a.n) return;
     auto value = [&](int c, float (&v)[W]) {
         load_f32<DT, A>(a.x, row * a.ldx + c, a.c - c, v);
         if (a.residual) {
@@ -418,7 +419,7 @@ template <int DT, bool A, int L, int NV>
 struct Forward {
     static void go(const NormArgs& a, hipStream_t s) {
         constexpr int kRows = kNormThreads / L;
-        launch(k_norm<DT, A, L, NV>, dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kNormThreads), 0, s, a);
+        launch(k_norm<DT, A, L, NV>, grid_of((a.n + kRows - 1) / kRows), dim3(kNormThreads), 0, s, a);
     }
 };
 
@@ -434,9 +435,9 @@ template <int DT>
 hipError_t norm_t(const NormArgs& a, hipStream_t s) {
     if (!by_shape<Forward, DT>(a, s)) {
         if (a.vec)
-            launch(k_norm_wide<DT, true>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_wide<DT, true>, grid_of(a.n), dim3(kNormThreads), 0, s, a);
         else
-            launch(k_norm_wide<DT, false>, dim3((unsigned)a.n), dim3(kNormThreads), 0, s, a);
+            launch(k_norm_wide<DT, false>, grid_of(a.n), dim3(kNormThreads), 0, s, a);
     }
     return hipGetLastError();
 }

@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void k_pad_rows(const E* __restrict__ src, int
                                                   int c, E* __restrict__ dst, int64_t ldd, int64_t rows_p, int half_p) {
     constexpr int kPer = 16 / sizeof(E);
     const int words = (int)(ldd / kPer);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_number() * 256 + threadIdx.x;
     const int64_t row = rows_p * words < ((int64_t)1 << 31) ? (int64_t)((uint32_t)i / (uint32_t)words) : i / words;
     if (row >= rows_p) return;
     const int col = (int)(i - row * words) * kPer, h = col / half_p, k = col - h * half_p;
@@ -154,7 +154,7 @@ hipError_t launch_sum_parts(const SumArgs& a, int dt, hipStream_t s) {
 
 hipError_t launch_pad_rows(int esize, const void* src, int64_t lds, int64_t rows, int halves, int c, void* dst,
                            int64_t ldd, int64_t rows_p, int half_p, hipStream_t s) {
-    const dim3 grid((unsigned)((rows_p * (ldd * esize / 16) + 255) / 256));
+    const dim3 grid = grid_of((rows_p * (ldd * esize / 16) + 255) / 256);
     if (esize == 1)
         launch(k_pad_rows<uint8_t>, grid, dim3(256), 0, s, static_cast<const uint8_t*>(src), lds, rows, halves, c,
                static_cast<uint8_t*>(dst), ldd, rows_p, half_p);

@@ -270,3 +270,48 @@ def test_norm_of_zero_rows_without_epsilon(n, c, dt):
                                               None if extra is None else d(ds[~zero]), dt)
         ro.check(dx[~at], wx, bx, "dx")
         ro.check(dw, ww, bw, "dweight")
+
+
+# ---- more rows than one grid dimension counts threads --------------------------------
+
+
+def room_for(gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+@pytest.mark.parametrize("n,c,gib", [((1 << 26) + 131, 264, 40), ((1 << 24) + 3, 4104, 140)])
+def test_norm_of_many_rows(n, c, gib):
+    """Rows that take 2^32 threads and more, four rows a block and a block a row:
+    every one is normalised, in place."""
+    room_for(gib)
+    x = torch.empty(n, c, dtype=BF16, device="cuda").fill_(3.0)
+    w = torch.ones(c, dtype=BF16, device="cuda")
+    assert norm_call(x, w, None, x, eps=0.0) == 0, smc.lib().smc_last_error()
+    step = (1 << 30) // c
+    for at in range(0, n, step):
+        assert torch.all(x[at:at + step] == 1)
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_linear_of_many_unaligned_rows():
+    """Rows of 1023 channels are copied to 1024 by more than 2^32 threads."""
+    room_for(150)
+    n, c, m = (1 << 25) + 77, 1023, 8
+    x = torch.zeros(n, c, dtype=BF16, device="cuda")
+    w = torch.zeros(c, m, dtype=BF16, device="cuda")
+    w[c - 1] = torch.arange(1, m + 1)
+    x[:, c - 1] = 1
+    x[n - 1, c - 1] = 5
+    x[1 << 24, 0] = 7
+    w[0] = 1
+    y = smc.linear(x, w)
+    want = torch.arange(1, m + 1, device="cuda").to(BF16)
+    assert torch.equal(y[n - 1], 5 * want) and torch.equal(y[1 << 24], want + 7)
+    y[n - 1] = want
+    y[1 << 24] = want
+    assert torch.all(y == want)
+    del x, y
+    torch.cuda.empty_cache()
