@@ -315,3 +315,34 @@ def test_linear_of_many_unaligned_rows():
     assert torch.all(y == want)
     del x, y
     torch.cuda.empty_cache()
+
+
+# ---- 8-bit weights ----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("c_in,c_out,extra", [(1, 1, 0), (7, 5, 0), (32, 32, 0), (33, 31, 3), (64, 200, 0),
+                                              (513, 129, 8), (130, 1365, 1), (2048, 72, 0)])
+def test_quantize_weight(c_in, c_out, extra, dt):
+    """scale[j] = max(max |w[:, j]| / 448, 2^-126) and q[j, k] = e4m3(w[k, j] / scale[j])
+    with float32 divisions and round to nearest even: the same bits as on the
+    CPU. Columns of zeros, of the smallest values, with an infinity and with a NaN."""
+    g = gen(c_in + c_out)
+    wide = normal(g, (c_in, c_out + extra), 1.0, dt) * torch.logspace(-3, 2, c_out + extra).to(dt)
+    w = wide[:, extra:]
+    if c_out >= 31:
+        w[:, 1] = 0
+        w[:, 3] = 2.0 ** (-24 if dt == F16 else -130)
+        w[0, 5], w[c_in - 1, 8] = float("inf"), float("nan")
+    q, scale = smc.quantize_weight(wide.cuda()[:, extra:])
+    assert q.shape == (c_out, c_in) and q.dtype == ro.E4M3 and scale.dtype == torch.float32
+    f = w.float()
+    want = (f.abs().amax(0) / 448).clamp(min=2.0 ** -126)
+    if c_out >= 31:
+        want[8] = float("nan")
+    assert torch.equal(scale.cpu().nan_to_num(-1.0), want.nan_to_num(-1.0))
+    ref, got = (f / want).t().to(ro.E4M3).float(), q.cpu().float()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got.nan_to_num(999.0), ref.nan_to_num(999.0))
+    keep = torch.isfinite(want) & (f.abs().amax(0) >= 448 * 2.0 ** -126)
+    assert torch.all(got[keep].abs().amax(1) == 448)
