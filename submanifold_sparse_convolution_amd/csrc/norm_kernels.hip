@@ -459,11 +459,15 @@ hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 // Blocks of the backward pass: each writes c sums, so no more than fill the
-// device, and no more than there are rows. 95,000 x 128 with 2, 3, 4, 6 and 8
+// device, and no more than there are rows (as many a block as its 256 threads hold
+// by by_shape; one where they are too wide for that). 95,000 x 128 with 2, 3, 4, 6 and 8
 // blocks a CU: rows and sums 24.3, 22.8, 22.5, 23.5 and 24.4 us.
 int norm_backward_blocks(int64_t n, int c) {
-    (void)c;
-    return (int)std::min<int64_t>(n, (int64_t)4 * device_cus());
+    const int words = (c + W - 1) / W;
+    int lanes = 1;
+    while (lanes < words && lanes < 64) lanes *= 2;
+    const int64_t rows = words > 64 * 8 ? 1 : kNormThreads / lanes;
+    return (int)std::min<int64_t>((n + rows - 1) / rows, (int64_t)4 * device_cus());
 }
 
 hipError_t launch_norm(const NormArgs& a, int dt, hipStream_t s) {

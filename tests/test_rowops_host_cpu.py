@@ -81,3 +81,12 @@ def test_every_range_of_a_weight_gradient_has_rows(n, c_in, c_out):
     assert ranges >= 1 and rest == 0
     length = -(-(-(-n // ranges)) // 64) * 64
     assert (ranges - 1) * length < n, f"{ranges} ranges of {length} rows for {n}"
+
+
+@pytest.mark.parametrize("n,c,rows_a_block", [(1, 128, 16), (1000, 128, 16), (1000, 7, 256), (1000, 257, 4),
+                                              (37, 4096, 4), (1000, 4097, 1), (95000, 128, 16)])
+def test_every_block_of_a_norm_gradient_has_rows(n, c, rows_a_block):
+    """The scratch memory is one row of sums a block (rounded up to 256 bytes):
+    no more blocks than the rows need, 256 threads each, or than 4 a CU."""
+    blocks = min(-(-n // rows_a_block), 4 * 256)
+    assert smc.lib().smc_rms_norm_backward_workspace(n, c) == -(-blocks * c * 4 // 256) * 256
