@@ -64,11 +64,12 @@ struct ProductArgs {
 // 32 bits (beyond them the launch succeeds with the blocks that are left), so many
 // blocks lie in two dimensions; block_number() tells them apart, the last few of
 // them past `blocks`.
+constexpr int kGridLog = 23;
 inline dim3 grid_of(int64_t blocks) {
-    constexpr int64_t kMost = 1 << 23;
-    return dim3((unsigned)(blocks < kMost ? blocks : kMost), (unsigned)((blocks + kMost - 1) / kMost));
+    const int64_t most = 1 << kGridLog;
+    return dim3((unsigned)(blocks < most ? blocks : most), (unsigned)((blocks + most - 1) >> kGridLog));
 }
-__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+__device__ __forceinline__ int64_t block_number() { return ((int64_t)blockIdx.y << kGridLog) + blockIdx.x; }
 
 // Compute units of the current device (looked up once per device).
 int device_cus();
