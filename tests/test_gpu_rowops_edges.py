@@ -346,3 +346,19 @@ def test_quantize_weight(c_in, c_out, extra, dt):
     assert torch.equal(got.nan_to_num(999.0), ref.nan_to_num(999.0))
     keep = torch.isfinite(want) & (f.abs().amax(0) >= 448 * 2.0 ** -126)
     assert torch.all(got[keep].abs().amax(1) == 448)
+
+
+# ---- tiles ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("n,c_in,c_out", [(50000, 64, 72), (40000, 64, 72), (70000, 128, 40), (70000, 264, 104),
+                                          (66000, 192, 264), (66000, 64, 520), (15000, 512, 384)])
+def test_linear_in_every_tile(n, c_in, c_out):
+    """Sizes on the sides of the rule that picks a tile; integers, bit for bit."""
+    g = gen(n + c_in)
+    x, w = (torch.randint(-1, 2, s, generator=g).to(BF16) for s in ((n, c_in), (c_in, c_out)))
+    b, r = torch.randint(-3, 4, (c_out,), generator=g).to(BF16), torch.randint(-4, 5, (n, c_out), generator=g).to(BF16)
+    z = (x.float() @ w.float() + b.float()).clamp(min=0)
+    assert torch.equal(smc.linear(x.cuda(), w.cuda(), bias=b.cuda(), activation="relu").cpu(), z.to(BF16))
+    y = smc.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda(), activation="relu")
+    assert torch.equal(y.cpu(), (z + r.float()).to(BF16))
