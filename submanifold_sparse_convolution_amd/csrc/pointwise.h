@@ -77,7 +77,8 @@ int device_cus();
 // out = product (see ProductArgs); dt: type of out, bias and extra, and of a
 // and b unless e4m3 (whose b lies along k or across it). Fills in the tile walk.
 constexpr int kMaxBlocksPerCu = 3;      // blocks of a product kernel, at most, for each CU
-constexpr int kFewRows = 16;    // forward 16-bit products of up to as many rows have a kernel of their own
+constexpr int kFewRows = 16;    // forward 16-bit products of up to as many rows may take a kernel of their own
+bool few_rows_pay(const ProductArgs& p, Epilogue epi);      // (kEpiStore or kEpiGated, 16-bit operands)
 hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w_along, hipStream_t s);
 // dx = dz W^T: both operands along k.
 hipError_t launch_input_gradient(ProductArgs p, int dt, hipStream_t s);

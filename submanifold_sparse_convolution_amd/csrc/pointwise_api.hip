@@ -165,7 +165,7 @@ struct Padded {
 Padded padded_of(const smc_product_t* a, const ProductArgs& p) {
     Padded pd;
     const int halves = p.n / a->c_out, es = a->x_dtype == SMC_DTYPE_E4M3 ? 1 : 2, per = 16 / es;
-    if ((es == 2 && a->n <= kFewRows) || (p.vec_a && p.vec_b)) return pd;
+    if ((es == 2 && few_rows_pay(p, halves == 2 ? kEpiGated : kEpiStore)) || (p.vec_a && p.vec_b)) return pd;
     if (a->c_in <= 128 / es || (p.vec_b && p.n <= 256 && a->c_in <= 512)) return pd;
     pd.copy_x = !p.vec_a;
     pd.k = (a->c_in + per - 1) / per * per;

@@ -27,8 +27,9 @@ hipError_t launch_forward(ProductArgs p, Epilogue epi, int dt, bool e4m3, bool w
     p.splits = 1;
     if (e4m3)
         return epi == kEpiGated ? launch_gated_e4m3(p, dt, w_along, s) : launch_store_e4m3(p, dt, w_along, s);
-    const bool gated_words = epi == kEpiGated && p.vec_a && p.vec_b;
-    if (p.m <= (gated_words ? 4 : kFewRows) && (epi == kEpiStore || epi == kEpiGated))
+    // (unaligned rows of which no copies were made cost the product kernel far more)
+    if ((epi == kEpiStore || epi == kEpiGated) &&
+        (p.vec_a && p.vec_b ? few_rows_pay(p, epi) : p.m <= kFewRows))
         return launch_few_rows(p, epi, dt, s);
     switch (epi) {
         case kEpiGated: return launch_gated_16(p, dt, s);

@@ -10,11 +10,26 @@
 // in a fixed order. Few columns a block give many blocks, and 1024 lanes a
 // short chain of loads in each.
 // More rows than a block takes (8, gated 4: registers) are a second dimension of
-// blocks, which read the weights from the cache again. Up to 16 rows: against
-// the product kernel, us on the GPU, 2048 -> 512 with 8 and 16 rows 9.0 and 9.1
-// (13.4 and 13.5), gated 512 -> 1365 8.9 and 14.4 (35.0 and 34.9, unaligned rows),
-// gated 512 -> 1368 7.4 and 12.6 (6.4 and 6.4, so aligned gated layers of more
-// than 4 rows go there).
+// blocks, which read the weights from the cache again. Against 32 x 64 tiles of
+// the product kernel (whose time does not depend on the rows), us on the GPU:
+//                 2 rows  4 rows  16 rows  tiles
+//     64 ->   64     -      4.3     6.4     3.8
+//    512 ->  512    3.5     4.7     6.9     6.3
+//    768 ->  512    3.8     5.0     7.6     7.5
+//   1024 ->  512    4.1     5.2     7.8     8.6
+//   2048 -> 2048    6.8     8.0    11.0    13.2
+//   gated:
+//     64 ->  176    4.3     6.3     6.4     3.6
+//    512 -> 1368    4.8     7.0    12.8     6.2
+//   1024 -> 1024    6.0     8.6     9.5     8.5
+//   2048 ->  512    7.7    10.4    10.8    13.1
+// so up to 4 rows come here and up to 16 of contractions above 768; gated, 2 and 4 of
+// contractions above 1024.
+// Unaligned rows, against copies and the product kernel: 1500 -> 512 with 16 rows 8.4,
+// 15.5; 2048 -> 2001 14.1, 19.9; 130 -> 1100 7.6, 9.2; gated 512 -> 1365 with 8 rows 8.8,
+// 10.0, but with 12 or 16, whose 258 and more blocks have to take turns, 14.2;
+// 700 -> 2001 with 8, 12 and 16 rows 11.8, 18.4, 21.3, 14.5: up to 16 rows while there are no
+// more blocks than CUs.
 #include "pointwise_gemm.h"
 #include "pointwise_launch.h"
 
@@ -115,32 +130,48 @@ __global__ __launch_bounds__(kFewThreads) void k_few_rows(ProductArgs p) {
     }
 }
 
+// The widest blocks (whole 128-byte lines of a weight row) that still give 128 of
+// them, else 16 columns. One row, 2048 -> 512 and gated 512 -> 1365: 8.4 and 7.3 us
+// with 8 columns a block, 5.0 and 7.6 with 16, 7.1 and 10.3 with 32, 10.7 and 11.7
+// with 64.
+int block_columns(int width) { return width >= 128 * 64 ? 64 : width >= 128 * 32 ? 32 : 16; }
+int block_rows(int m, bool gated) { return m <= 2 ? m : m <= 4 || gated ? 4 : 8; }
+
 template <int DT, int EPI, int R>
 hipError_t few_t(const ProductArgs& p, hipStream_t s) {
     const int width = EPI == kEpiGated ? p.half : p.n;
     const unsigned groups = (unsigned)((p.m + R - 1) / R);
-    // The widest blocks (whole 128-byte lines of a weight row) that still give
-    // 128 of them, else 16 columns. One row, 2048 -> 512 and gated 512 -> 1365:
-    // 8.4 and 7.3 us with 8 columns a block, 5.0 and 7.6 with 16, 7.1 and 10.3
-    // with 32, 10.7 and 11.7 with 64.
-    if (width >= 128 * 64)
-        launch(k_few_rows<DT, EPI, R, 64>, dim3((unsigned)((width + 63) / 64), groups), dim3(kFewThreads), 0, s, p);
-    else if (width >= 128 * 32)
-        launch(k_few_rows<DT, EPI, R, 32>, dim3((unsigned)((width + 31) / 32), groups), dim3(kFewThreads), 0, s, p);
-    else
-        launch(k_few_rows<DT, EPI, R, 16>, dim3((unsigned)((width + 15) / 16), groups), dim3(kFewThreads), 0, s, p);
+    const int cb = block_columns(width);
+    const dim3 grid((unsigned)((width + cb - 1) / cb), groups);
+    switch (cb) {
+        case 64: launch(k_few_rows<DT, EPI, R, 64>, grid, dim3(kFewThreads), 0, s, p); break;
+        case 32: launch(k_few_rows<DT, EPI, R, 32>, grid, dim3(kFewThreads), 0, s, p); break;
+        default: launch(k_few_rows<DT, EPI, R, 16>, grid, dim3(kFewThreads), 0, s, p);
+    }
     return hipGetLastError();
 }
 
 template <int DT, int EPI>
 hipError_t few(const ProductArgs& p, hipStream_t s) {
-    if (p.m <= 1) return few_t<DT, EPI, 1>(p, s);
-    if (p.m <= 2) return few_t<DT, EPI, 2>(p, s);
-    if constexpr (EPI == kEpiGated) return few_t<DT, EPI, 4>(p, s);
-    else return p.m <= 4 ? few_t<DT, EPI, 4>(p, s) : few_t<DT, EPI, 8>(p, s);
+    switch (block_rows(p.m, EPI == kEpiGated)) {
+        case 1: return few_t<DT, EPI, 1>(p, s);
+        case 2: return few_t<DT, EPI, 2>(p, s);
+        case 4: return few_t<DT, EPI, 4>(p, s);
+        default:
+            if constexpr (EPI == kEpiStore) return few_t<DT, EPI, 8>(p, s);
+            else return hipErrorInvalidValue;       // (block_rows has no more for gated layers)
+    }
 }
 
 }  // namespace
+
+bool few_rows_pay(const ProductArgs& p, Epilogue epi) {
+    const bool gated = epi == kEpiGated;
+    if (p.m > kFewRows) return false;
+    if (p.vec_a && p.vec_b && p.m > (gated ? (p.k > 1024 ? 4 : 2) : p.k > 768 ? kFewRows : 4)) return false;
+    const int width = gated ? p.half : p.n, cb = block_columns(width), r = block_rows(p.m, gated);
+    return p.m <= r || (int64_t)((width + cb - 1) / cb) * ((p.m + r - 1) / r) <= device_cus();
+}
 
 hipError_t launch_few_rows(const ProductArgs& p, Epilogue epi, int dt, hipStream_t s) {
     if (dt == kF16) return epi == kEpiGated ? few<kF16, kEpiGated>(p, s) : few<kF16, kEpiStore>(p, s);

@@ -362,3 +362,20 @@ def test_linear_in_every_tile(n, c_in, c_out):
     assert torch.equal(smc.linear(x.cuda(), w.cuda(), bias=b.cuda(), activation="relu").cpu(), z.to(BF16))
     y = smc.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda(), activation="relu")
     assert torch.equal(y.cpu(), (z + r.float()).to(BF16))
+
+
+@pytest.mark.parametrize("n", [2, 3, 4, 5, 7])
+@pytest.mark.parametrize("c_in,c_out", [(64, 64), (768, 40), (776, 40), (1024, 72), (1032, 64), (2048, 200), (1030, 66)])
+def test_few_rows_in_either_kernel(n, c_in, c_out):
+    """Sizes on the sides of the rule that picks the few-row kernel."""
+    for halves in (1, 2):
+        g = gen(n + c_in + halves)
+        x, w = normal(g, (n, c_in)), normal(g, (c_in, halves * c_out), c_in ** -0.5)
+        b = normal(g, (halves * c_out,), 0.3)
+        if halves == 1:
+            r = normal(g, (n, c_out), 2.0)
+            y = smc.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda(), activation="silu")
+            ro.check(y, *ro.linear(d(x), d(w), d(b), d(r), "silu", BF16), "linear")
+        else:
+            y = smc.gated(x.cuda(), w.cuda(), bias=b.cuda(), activation="silu")
+            ro.check(y, *ro.gated(d(x), d(w), d(b), "silu", BF16), "gated")
