@@ -626,7 +626,11 @@ struct Place {
         m0 = tm * T::BM;
         k0 = split * p.k_split;
         k_len = p.k - k0 < p.k_split ? p.k - k0 : p.k_split;
-        steps = (k_len + step_k - 1) / step_k;      // at least one
+        // At least one: launch_product refuses empty splits. The walk is written as if
+        // there were none now and then, which the compiler schedules better: 91,000 x
+        // 128 -> 128 with a residual 15.6 us, as straight code 16.0; e4m3 gated 91,000 x
+        // 128 -> 344 from [k, n] weights 59 and 64.
+        steps = k_len > 0 ? (k_len + step_k - 1) / step_k : 0;
     }
 };
 
@@ -732,11 +736,12 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
     };
     // moves on to a step that exists; false when the walk is over
     auto next_step = [&]() SMC_INLINE {
-        if (ahead_step < ahead.steps) return true;
-        if (ahead.t + t_step >= t_end) return false;
-        const int tm = ahead.tm, tn = ahead.tn;
-        ahead.advance(p, t_step, kStep);
-        enter(false, ahead.tm != tm, ahead.tn != tn);
+        while (ahead_step >= ahead.steps) {             // (once: see Place::derive)
+            if (ahead.t + t_step >= t_end) return false;
+            const int tm = ahead.tm, tn = ahead.tn;
+            ahead.advance(p, t_step, kStep);
+            enter(false, ahead.tm != tm, ahead.tn != tn);
+        }
         return true;
     };
     auto step_left = [&]() SMC_INLINE {                 // contraction elements of it
@@ -942,11 +947,14 @@ __global__ __launch_bounds__(T::kThreads, T::kBlocks* T::kThreads / 256) void k_
         // What the epilogue reads is loaded beside it, two steps before a wait
         // includes it.
         if constexpr (ALIGNED) {
-            arrive();
-            load_epilogue();
-            if (kHasExtra && p.extra && p.vec_x) ops += MT * kPairs;
-            compute();
-            int step = 1;
+            int step = 0;
+            if (here.steps > 0) {                       // (always: see Place::derive)
+                arrive();
+                load_epilogue();
+                if (kHasExtra && p.extra && p.vec_x) ops += MT * kPairs;
+                compute();
+                ++step;
+            }
             // the step issued is a whole one of this tile
             const int main_steps = here.k_len / kStep - (S - 1);
 #pragma unroll 1
