@@ -483,8 +483,9 @@ int smc_version(void);
  * their own scratch do not touch each other. n = 0 is valid (gradients of
  * weights are then zeros). Outputs may not overlap inputs, except y = residual
  * (smc_linear) and s = x or residual, 16-bit y = x (smc_rms_norm), with equal
- * addresses and row distances. e4m3 y that shares memory with x, residual or s is
- * refused (SMC_ERR_ARG).
+ * addresses and row distances. Refused (SMC_ERR_ARG) are e4m3 y that shares memory
+ * with x, residual or s, y of a layer that shares it with x, and dx with x or, without
+ * an activation, with dy; columns of one buffer do not share it.
  *
  * Sums, norms and pre-activations are float32; every output is rounded once
  * (to nearest, ties to even) from float32. The backward passes keep nothing of

@@ -677,7 +677,7 @@ def linear(x, w, bias=None, residual=None, activation=None, x_scale=None, w_scal
     "silu" or "gelu" (erf). Served in 8 bits: x float8_e4m3fn with x_scale [N]
     (rms_norm's e4m3 output), w float8_e4m3fn [C_out, C_in] with w_scale [C_out]
     (quantize_weight; its transpose's memory order is taken too), y of `dtype`
-    (default bf16). out may be the residual."""
+    (default bf16). out may be the residual, not x."""
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:

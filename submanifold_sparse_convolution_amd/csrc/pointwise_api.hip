@@ -43,14 +43,14 @@ int check_rows(const char* name, const void* p, int64_t rows, int64_t cols, int6
     return SMC_OK;
 }
 
-// Do the [rows, cols] tensors at p and q (es bytes an element, ld elements from
+// Do the tensors at p and q (rows of cols elements of es bytes, ld elements from
 // row to row) share memory? Columns of one buffer, whose ranges overlap with equal
 // row distances in bytes, are told apart; other overlapping ranges count as shared.
 bool share_memory(const void* p, int64_t ldp, int esp, const void* q, int64_t ldq, int esq, int64_t rows,
-                  int64_t cols) {
+                  int64_t colsp, int64_t colsq) {
     if (!p || !q || rows <= 0) return false;
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    const uint64_t pitch = (uint64_t)ldp * esp, wp = (uint64_t)cols * esp, wq = (uint64_t)cols * esq;
+    const uint64_t pitch = (uint64_t)ldp * esp, wp = (uint64_t)colsp * esp, wq = (uint64_t)colsq * esq;
     if (a + (uint64_t)(rows - 1) * pitch + wp <= b || b + (uint64_t)(rows - 1) * ldq * esq + wq <= a) return false;
     if (pitch != (uint64_t)ldq * esq) return true;
     const uint64_t apart = a > b ? (pitch - (a - b) % pitch) % pitch : (b - a) % pitch;    // q's columns after p's
@@ -109,13 +109,23 @@ int check_product(const smc_product_t* a, int halves, bool backward) {
         return bad(SMC_ERR_ARG, "residual is an argument of smc_linear only");
     if (!backward) {
         if (a->residual) CHECK(check_rows("residual", a->residual, a->n, a->c_out, a->ld_residual));
-        return check_rows("y", a->y, a->n, a->c_out, a->ldy);
+        CHECK(check_rows("y", a->y, a->n, a->c_out, a->ldy));
+        // (blocks of other column tiles read x again)
+        if (share_memory(a->y, a->ldy, 2, a->x, a->ldx, e4m3 ? 1 : 2, a->n, a->c_out, a->c_in))
+            return bad(SMC_ERR_ARG, "y shares memory with x");
+        return SMC_OK;
     }
     CHECK(check_rows("dy", a->dy, a->n, a->c_out, a->ld_dy));
     CHECK(check_rows("dx", a->dx, a->n, a->c_in, a->ld_dx));
     if (!a->dw) return bad(SMC_ERR_ARG, "dw is NULL");
     CHECK(check_rows("dw", a->dw, a->c_in, wide, a->ld_dw));
     if (((uintptr_t)a->db & 1) != 0) return bad(SMC_ERR_ARG, "db is not aligned to its elements");
+    // dW is taken from x after dx, and from dy too where no activation changes it
+    if (share_memory(a->dx, a->ld_dx, 2, a->x, a->ldx, 2, a->n, a->c_in, a->c_in))
+        return bad(SMC_ERR_ARG, "dx shares memory with x");
+    if (halves == 1 && a->activation == SMC_ACT_NONE &&
+        share_memory(a->dx, a->ld_dx, 2, a->dy, a->ld_dy, 2, a->n, a->c_in, a->c_out))
+        return bad(SMC_ERR_ARG, "dx shares memory with dy");
     return SMC_OK;
 }
 
@@ -407,9 +417,9 @@ int smc_rms_norm(const smc_norm_t* a, void* stream) {
     if (!a->y_scale && ((uintptr_t)a->y & 1)) return bad(SMC_ERR_ARG, "y is not aligned to its elements");
     // e4m3 rows over 16-bit ones: a row of y would lie in other rows' bytes, which
     // another wave may not have read
-    if (a->y_scale && (share_memory(a->y, a->ldy, 1, a->x, a->ldx, 2, a->n, a->c) ||
-                       share_memory(a->y, a->ldy, 1, a->residual, a->ld_residual, 2, a->n, a->c) ||
-                       share_memory(a->y, a->ldy, 1, a->s, a->lds, 2, a->n, a->c)))
+    if (a->y_scale && (share_memory(a->y, a->ldy, 1, a->x, a->ldx, 2, a->n, a->c, a->c) ||
+                       share_memory(a->y, a->ldy, 1, a->residual, a->ld_residual, 2, a->n, a->c, a->c) ||
+                       share_memory(a->y, a->ldy, 1, a->s, a->lds, 2, a->n, a->c, a->c)))
         return bad(SMC_ERR_ARG, "e4m3 y shares memory with x, residual or s");
     NormArgs p;
     p.n = a->n;

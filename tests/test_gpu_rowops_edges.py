@@ -379,3 +379,15 @@ def test_few_rows_in_either_kernel(n, c_in, c_out):
         else:
             y = smc.gated(x.cuda(), w.cuda(), bias=b.cuda(), activation="silu")
             ro.check(y, *ro.gated(d(x), d(w), d(b), "silu", BF16), "gated")
+
+
+def test_out_over_x_is_refused():
+    x = normal(gen(1), (70, 64)).cuda()
+    w = normal(gen(2), (64, 64), 0.1).cuda()
+    want = smc.linear(x, w)
+    for out in (x, x[:, :64]):
+        with pytest.raises(smc.SmconvError):
+            smc.linear(x, w, out=out)
+    buf = torch.cat((x, x), 1)                  # columns of one buffer
+    assert torch.equal(smc.linear(buf[:, :64], w, out=buf[:, 64:]), want)
+    assert torch.equal(buf[:, :64], x)

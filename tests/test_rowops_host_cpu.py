@@ -39,6 +39,29 @@ APART = [
 ]
 
 
+# outputs of the layers over inputs that other blocks, or later kernels, still read
+W, Y, DY, DX, FAR = (BASE << k for k in range(1, 6))
+
+
+def product(**kw):
+    a = smc.ProductArgs(8, 64, 64, 0, 0, 0, BASE, 64, None, W, 128)
+    a.y, a.ldy, a.dy, a.ld_dy, a.dx, a.ld_dx, a.dw, a.ld_dw = Y, 64, DY, 64, DX, 64, FAR, 128
+    a.workspace, a.workspace_bytes = FAR << 1, 1 << 30
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+LAYERS, BACK = ("smc_linear", "smc_gated"), ("smc_linear_backward", "smc_gated_backward")
+OVER = ([(name, dict(y=BASE)) for name in LAYERS] + [(name, dict(y=BASE + 128 * 8 - 2)) for name in LAYERS]
+        + [(name, dict(dx=BASE)) for name in BACK] + [("smc_linear_backward", dict(dx=DY))]
+        + [("smc_linear", dict(x_dtype=2, x_scale=FAR, w_scale=FAR, y=BASE))])
+BESIDE = ([(name, dict(y=BASE + 128, ldy=128, ldx=128)) for name in LAYERS]
+          + [("smc_linear", dict(residual=Y, ld_residual=64))]
+          + [("smc_linear_backward", dict(dx=DY + 128, ld_dx=128, ld_dy=128))])
+CALLS = [("smc_rms_norm", kw) for kw in SHARED + APART] + OVER + BESIDE
+
+
 @pytest.fixture(scope="module")
 def answers():
     """Status and message of every call, from a process that sees no device (and
@@ -48,13 +71,16 @@ def answers():
             "import ctypes, torch, test_rowops_host_cpu as t\n"
             "import submanifold_sparse_convolution_amd as smc\n"
             "assert torch.cuda.device_count() == 0\n"
-            "for kw in t.SHARED + t.APART:\n"
-            "    rc = smc.lib().smc_rms_norm(ctypes.byref(t.norm(**kw)), None)\n"
+            "for name, kw in t.CALLS:\n"
+            "    args = t.norm(**kw) if name == 'smc_rms_norm' else t.product(**kw)\n"
+            "    rc = getattr(smc.lib(), name)(ctypes.byref(args), None)\n"
             "    print(rc, smc.lib().smc_last_error().decode())\n" % [here, os.path.dirname(here)])
     env = dict(os.environ, HIP_VISIBLE_DEVICES="-1")
     out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=300)
     assert out.returncode == 0, out.stdout + out.stderr
-    return [(int(line.partition(" ")[0]), line.partition(" ")[2]) for line in out.stdout.strip().splitlines()]
+    lines = out.stdout.strip().splitlines()
+    assert len(lines) == len(CALLS)
+    return [(int(line.partition(" ")[0]), line.partition(" ")[2]) for line in lines]
 
 
 @pytest.mark.parametrize("i", range(len(SHARED)))
@@ -67,6 +93,18 @@ def test_e4m3_rows_that_share_memory_are_refused(answers, i):
 def test_e4m3_rows_beside_the_inputs_pass_the_checks(answers, i):
     rc, msg = answers[len(SHARED) + i]
     assert rc != SMC_ERR_ARG, (APART[i], rc, msg)
+
+
+@pytest.mark.parametrize("i", range(len(OVER)))
+def test_layers_over_their_inputs_are_refused(answers, i):
+    rc, msg = answers[len(SHARED) + len(APART) + i]
+    assert rc == SMC_ERR_ARG and "shares memory" in msg, (OVER[i], rc, msg)
+
+
+@pytest.mark.parametrize("i", range(len(BESIDE)))
+def test_layers_beside_their_inputs_pass_the_checks(answers, i):
+    rc, msg = answers[len(SHARED) + len(APART) + len(OVER) + i]
+    assert rc != SMC_ERR_ARG, (BESIDE[i], rc, msg)
 
 
 @pytest.mark.parametrize("n,c_in,c_out", [(1, 8, 8), (257, 8, 8), (15000, 2048, 512), (15000, 512, 4096),
