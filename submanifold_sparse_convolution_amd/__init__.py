@@ -479,6 +479,8 @@ def subm_conv3d(coords, x, w, spatial_shape=None, relu: bool = False, route: str
 
 
 # ---- row operators ------------------------------------------------------------
+# Like the convolution they are not connected to autograd: results are detached, also
+# where an input requires gradients; the _backward functions give the gradients.
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 

@@ -10,9 +10,9 @@
 // Bound by memory: every row is read once and kept in registers between its
 // sums and its outputs, by as many lanes as its 16-byte words (16 of them for 128
 // channels, so a wave takes four rows and the sums stay inside it); rows too
-// long for that are read again. With the residual, bf16: 91,000 x 128 15.3 us (93
-// MB, 6.1 TB/s, part of it cached), e4m3 15,000 x 512 12.2 us (4.4 TB/s), backward
-// 95,000 x 128 18.3 us (5.3 TB/s) and 3.9 us for the sums of dw.
+// long for that are read again. With the residual, bf16: 91,000 x 128 15.5 us (93
+// MB, 6.0 TB/s, part of it cached), e4m3 15,000 x 512 12.5 us (4.3 TB/s), backward
+// 95,000 x 128 18.5 us (5.3 TB/s) and 4.0 us for the sums of dw.
 #include <algorithm>
 
 #include "pointwise_gemm.h"
@@ -355,7 +355,9 @@ __global__ __launch_bounds__(1024) void k_norm_weight_sum(const float* __restric
 }
 
 // W [c_in, c_out] -> q [c_out, c_in] e4m3, one scale a column of W. 32 columns
-// a block; W is read twice (once per weight and program, not a hot path).
+// a block; W is read twice. Made for a call a weight and program, not for the path
+// of a step: bound by the latency of a block's chain of loads over c_in (512 x 4096 29
+// us, 2048 x 512 109 us).
 template <int DT>
 __global__ __launch_bounds__(256) void k_quantize_weight(const uint16_t* __restrict__ w, int64_t ldw,
                                                          int c_in, int c_out, uint8_t* q,

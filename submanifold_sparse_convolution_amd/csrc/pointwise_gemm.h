@@ -21,14 +21,20 @@
 // Loads that write LDS place lane l at 16 l, so the permutation is applied to
 // the address a lane loads from.
 //
-// What bounds it. A 128 x 128 tile asks for 32 KiB a step of 16-bit products that
-// take the CU's matrix units 1,024 clocks: 32 bytes a clock and CU, about what the
-// L2 delivers to LDS (19 TB/s in all). Larger tiles need fewer bytes, but their accumulators leave
-// one block a CU and nothing to overlap the epilogue, and were not faster.
+// What bounds it. A step of a 128 x 128 tile is 32 KiB to LDS and 128 MFMAs of 16 x 16
+// x 32, 16 clocks each: 512 clocks of the CU's four matrix units, 64 bytes a clock at
+// their full rate. Measured: dz W^T of 15,000 x 4096 -> 512 and x^T dz of the same keep
+// them 45 and 49 % busy at 28 and 31 bytes a clock and CU (14 TB/s to LDS in all):
+// no unit is at its end, a step's arrival, fragment reads and products do not
+// overlap fully in two blocks a CU. With few steps a tile, or activations after them,
+// the tile's start and epilogue stand beside too few products: 24 to 30 % busy at 15
+// to 19 bytes in the linear backward's products, the slopes and the e4m3 layer.
+// Larger tiles need fewer bytes, but their accumulators leave one block a CU and
+// nothing to overlap the epilogue, and were not faster.
 // bf16, GPU times: dz W^T of 15,000 x 4096 -> 512 70 us (0.90 PFLOP/s), x^T dz of the
-// same 69 us (0.91), the slopes of the gated 512 -> 2048 105 us (0.60, with 184 MB in
+// same 67 us (0.93), the slopes of the gated 512 -> 2048 107 us (0.59, with 184 MB in
 // the epilogue), 91,000 x 128 -> 128 with a residual 15.6 us (4.5 TB/s), gated
-// 128 -> 344 37.9 us (2.3 TB/s); e4m3 gated 15,000 x 512 -> 2048 50.5 us (1.25 PFLOP/s).
+// 128 -> 344 38.0 us (2.3 TB/s); e4m3 gated 15,000 x 512 -> 2048 51.2 us (1.23 PFLOP/s).
 //
 // Edges. The buffer descriptors end at the operand's last valid element, and a
 // lane whose word is past the end of a row gets an offset outside: such loads
