@@ -391,3 +391,27 @@ def test_out_over_x_is_refused():
     buf = torch.cat((x, x), 1)                  # columns of one buffer
     assert torch.equal(smc.linear(buf[:, :64], w, out=buf[:, 64:]), want)
     assert torch.equal(buf[:, :64], x)
+
+
+@pytest.mark.parametrize("halves,size", [(1, 2.0 ** -22), (2, 2.0 ** -22), (1, 60000.0), (2, 3000.0)])
+def test_f16_gradients_in_large_tiles(halves, size):
+    """dz below and above f16's range in 128-row tiles of every product. Weights
+    and x of powers of two, one nonzero weight a column and slopes of 1 (z far
+    above 0): dz, dx and dw are sums of a few exact terms."""
+    g = gen(halves)
+    n, c, m = 15000, 512, 512
+    x = torch.where(torch.rand(n, c, generator=g) < 0.5, -1.0, 1.0).to(F16) * 2.0 ** -10
+    w = torch.zeros(c, halves * m, dtype=F16)
+    w[torch.randint(0, c, (halves * m,), generator=g), torch.arange(halves * m)] = 2.0 ** -6
+    b = torch.full((halves * m,), 1.0 if halves == 1 else 64.0).to(F16)
+    dy = (torch.randint(-3, 4, (n, m), generator=g) * (size / 3)).to(F16)
+    z = d(x) @ d(w) + d(b)
+    dz = d(dy) if halves == 1 else torch.cat((d(dy) * z[:, m:], d(dy) * z[:, :m]), 1)
+    assert z.min() > 0 and (dz.abs().max() > 65504 or dz.abs().max() < 2.0 ** -8 or halves == 1)
+    back = smc.linear_backward if halves == 1 else smc.gated_backward
+    dx, dw, _ = back(dy.cuda(), x.cuda(), w.cuda(), bias=b.cuda(), activation="relu")
+    (wx, bx), (ww, bw), _ = ro.gradients(dz, dz.abs() * 2.0 ** -11 + dz.abs().max() * 2.0 ** -17, d(x), d(w), F16)
+    for v, want, bound, label in ((dx, wx, bx, "dx"), (dw, ww, bw, "dw")):
+        keep = want.abs() < 65000               # (a few sums are themselves beyond f16)
+        assert keep.double().mean() > 0.99
+        ro.check(v.cpu()[keep], want[keep], bound[keep], label)
