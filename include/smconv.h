@@ -639,6 +639,62 @@ size_t smc_gated_backward_workspace(const smc_product_t* args);
 int smc_weight_quantize(const void* w, int64_t ldw, int c_in, int c_out, int dtype, void* q,
                         int64_t ldq, float* scale, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators that mix rows. The conventions of the row operators hold: row distances,
+ * alignment, float32 sums and statistics in a fixed order, one rounding on the way
+ * out, nothing kept and nothing allocated.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Group norm with an activation, over the rows of each sample of a batch:
+ *   mean, var of the sample's rows and the group's channels (c / groups adjacent ones)
+ *   x_hat = (x - mean) / sqrt(var + eps);  y = act(x_hat weight + bias)
+ * offsets (device, int32 [samples + 1], or NULL with samples = 1: every row is of
+ * one sample): sample s is the rows offsets[s] .. offsets[s + 1] - 1, ascending, within
+ * [0, n] (others are read as if cut to it, and give wrong results). Samples may be empty;
+ * rows of no sample come out as zeros, and so do their gradients. stats (or NULL):
+ * mean and 1 / sqrt(var + eps) of each sample and group, zeros for an empty sample; a
+ * variance of zero with eps = 0 counts as 1 / sqrt 0 = 0.
+ * y may be x (equal addresses and row distances); other overlaps are refused.
+ *
+ * Backward, from x and the stats that the forward call wrote: with z = x_hat weight + bias,
+ * dz = dy act'(z) and means over the sample and group
+ *   dx = (dz weight - mean(dz weight) - x_hat mean(dz weight x_hat)) / sqrt(var + eps)
+ *   dweight = sum over rows of dz x_hat,  dbias = sum over rows of dz
+ * dx may be x or dy. n = 0 gives zero gradients of the weights. eps is not read.
+ * workspace: device memory of smc_group_norm_workspace(args), or _backward_workspace,
+ * bytes, 16-byte aligned; the queries read n, c, groups, samples and whether offsets is
+ * NULL. c <= 8192, groups <= 4096 and samples <= 65536 (else SMC_ERR_UNSUPPORTED).
+ */
+typedef struct smc_group_norm_s {
+    int64_t n;                /* rows */
+    int32_t c, groups;        /* groups divides c */
+    int32_t samples;
+    int32_t dtype;            /* SMC_DTYPE_BF16 or _F16 */
+    int32_t activation;       /* SMC_ACT_* */
+    float eps;                /* >= 0 */
+    const int32_t* offsets;   /* [samples + 1] or NULL */
+    const void* x;            /* [n, c] */
+    int64_t ldx;
+    const void* weight;       /* [c] */
+    const void* bias;         /* [c] */
+    void* y;                  /* forward: [n, c] */
+    int64_t ldy;
+    float* stats;             /* [samples, groups, 2]: written, or NULL; backward: read */
+    const void* dy;           /* backward from here on: [n, c] */
+    int64_t ld_dy;
+    void* dx;                 /* [n, c] */
+    int64_t ld_dx;
+    void* dweight;            /* [c] */
+    void* dbias;              /* [c] */
+    void* workspace;
+    size_t workspace_bytes;
+} smc_group_norm_t;
+int smc_group_norm(const smc_group_norm_t* args, void* stream);
+int smc_group_norm_backward(const smc_group_norm_t* args, void* stream);
+size_t smc_group_norm_workspace(const smc_group_norm_t* args);
+size_t smc_group_norm_backward_workspace(const smc_group_norm_t* args);
+
 #ifdef __cplusplus
 }
 #endif

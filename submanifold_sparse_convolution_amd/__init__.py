@@ -18,7 +18,7 @@ import os
 __all__ = ["KernelMap", "PackedWeights", "pack_weights", "subm_conv3d", "lib", "library_path",
            "SmconvError", "ROUTES", "EXPORTED_SYMBOLS", "use_torch_allocator", "probe_mfma_bf16",
            "probe_copy", "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated",
-           "gated_backward", "quantize_weight", "ACTIVATIONS"]
+           "gated_backward", "quantize_weight", "ACTIVATIONS", "group_norm", "group_norm_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsmconv.so")
@@ -46,6 +46,8 @@ EXPORTED_SYMBOLS = [
     "smc_rms_norm_backward_workspace", "smc_linear", "smc_gated", "smc_linear_backward",
     "smc_gated_backward", "smc_linear_workspace", "smc_gated_workspace",
     "smc_linear_backward_workspace", "smc_gated_backward_workspace", "smc_weight_quantize",
+    "smc_group_norm", "smc_group_norm_backward", "smc_group_norm_workspace",
+    "smc_group_norm_backward_workspace",
 ]
 STAGES = ["map", "neighbours", "mask_sort", "compact", "gemm", "centre"]
 
@@ -102,6 +104,19 @@ class ProductArgs(ctypes.Structure):
         ("ld_dx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("ld_dw", ctypes.c_int64),
         ("db", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GroupNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("c", ctypes.c_int32), ("groups", ctypes.c_int32),
+        ("samples", ctypes.c_int32), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("offsets", ctypes.c_void_p), ("x", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("stats", ctypes.c_void_p),
+        ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -165,12 +180,16 @@ def lib():
         getattr(L, name).restype = i32
     for name, args in (("smc_rms_norm", NormArgs), ("smc_rms_norm_backward", NormBackwardArgs),
                        ("smc_linear", ProductArgs), ("smc_gated", ProductArgs),
-                       ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs)):
+                       ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs),
+                       ("smc_group_norm", GroupNormArgs), ("smc_group_norm_backward", GroupNormArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
         getattr(L, name).restype = i32
-    for name in ("smc_linear_workspace", "smc_gated_workspace", "smc_linear_backward_workspace",
-                 "smc_gated_backward_workspace"):
-        getattr(L, name).argtypes = [ctypes.POINTER(ProductArgs)]
+    for name, args in (("smc_linear_workspace", ProductArgs), ("smc_gated_workspace", ProductArgs),
+                       ("smc_linear_backward_workspace", ProductArgs),
+                       ("smc_gated_backward_workspace", ProductArgs),
+                       ("smc_group_norm_workspace", GroupNormArgs),
+                       ("smc_group_norm_backward_workspace", GroupNormArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_size_t
     L.smc_rms_norm_backward_workspace.argtypes = [i64, i32]
     L.smc_rms_norm_backward_workspace.restype = ctypes.c_size_t
@@ -760,6 +779,82 @@ def quantize_weight(w, stream=None):
     _check(lib().smc_weight_quantize(wp, ldw, c_in, c_out, code, q.data_ptr(), c_in,
                                      scale.data_ptr(), _raw_stream(w.device)))
     return q, scale
+
+
+# ---- operators that mix rows ---------------------------------------------------
+
+
+def _group_args(x, weight, bias, groups, offsets, eps, activation):
+    import torch
+    act = _activation(activation)
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x, "x")
+    n, c = x.shape
+    xp, ldx = _rows(x, "x", dt, dev)
+    if groups < 1 or c % groups:
+        raise ValueError(f"{c} channels in {groups} groups")
+    op, samples = None, 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError(f"offsets must be [samples + 1], got {list(offsets.shape)}")
+        op, samples = _vector(offsets, "offsets", torch.int32, dev, offsets.shape[0]), offsets.shape[0] - 1
+    return GroupNormArgs(n, c, groups, samples, code, act, eps, op, xp, ldx,
+                         _vector(weight, "weight", dt, dev, c), _vector(bias, "bias", dt, dev, c))
+
+
+def group_norm(x, weight, bias, groups: int, offsets=None, eps: float = 1e-5, activation=None,
+               stats: bool = False, stream=None):
+    """y = activation((x - mean) / sqrt(var + eps) * weight + bias), mean and variance
+    over the rows of each sample and the channels of each of `groups` groups.
+
+    x: bf16 or f16 [N, C] CUDA tensor (rows may be strided), weight and bias [C],
+    offsets: int32 [samples + 1] CUDA tensor, sample s being the rows offsets[s] ..
+    offsets[s + 1] - 1 (None: one sample of all rows; rows of no sample come out as
+    zeros); activation as in linear. With stats (y, stats), stats float32 [samples,
+    groups, 2] (mean, 1 / sqrt(var + eps)), as group_norm_backward takes it."""
+    import torch
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return group_norm(x, weight, bias, groups, offsets, eps, activation, stats)
+    a = _group_args(x, weight, bias, groups, offsets, eps, activation)
+    L = lib()
+    y = x.new_empty((a.n, a.c))
+    a.y, a.ldy = y.data_ptr(), a.c
+    if stats:
+        kept = x.new_empty((a.samples, groups, 2), dtype=torch.float32)
+        a.stats = kept.data_ptr()
+    nbytes = L.smc_group_norm_workspace(a)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _check(L.smc_group_norm(a, _raw_stream(x.device)))
+    return (y, kept) if stats else y
+
+
+def group_norm_backward(dy, x, weight, bias, groups: int, stats, offsets=None, activation=None,
+                        stream=None):
+    """Gradients of group_norm for the gradient dy of its output: (dx, dweight,
+    dbias). stats: what group_norm returned for the same x, groups and offsets."""
+    import torch
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return group_norm_backward(dy, x, weight, bias, groups, stats, offsets, activation)
+    a = _group_args(x, weight, bias, groups, offsets, 0.0, activation)
+    L = lib()
+    dev, dt, shape = x.device, x.dtype, (a.n, a.c)
+    a.dy, a.ld_dy = _rows(dy, "dy", dt, dev, shape)
+    _of(stats, "stats", torch.float32, dev)
+    if stats.shape != (a.samples, groups, 2) or not stats.is_contiguous():
+        raise ValueError(f"stats must be contiguous {[a.samples, groups, 2]}, got {list(stats.shape)}")
+    a.stats = stats.data_ptr()
+    dx, dweight, dbias = x.new_empty(shape), x.new_empty(a.c), x.new_empty(a.c)
+    a.dx, a.ld_dx, a.dweight, a.dbias = dx.data_ptr(), a.c, dweight.data_ptr(), dbias.data_ptr()
+    nbytes = L.smc_group_norm_backward_workspace(a)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _check(L.smc_group_norm_backward(a, _raw_stream(dev)))
+    return dx, dweight, dbias
 
 
 def probe_mfma_bf16(iters: int, stream=None) -> float:

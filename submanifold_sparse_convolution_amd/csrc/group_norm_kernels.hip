@@ -1,0 +1,518 @@
+// Group norm of rows, channels last, with an activation, and its gradients.
+//
+//   mean, var over the rows of a sample and the channels of a group
+//   x_hat = (x - mean) rstd, rstd = 1 / sqrt(var + eps), z = x_hat w + b, y = act(z)
+//
+//   dz = dy act'(z), a = dz w
+//   dx = rstd (a - mean(a) - x_hat mean(a x_hat)), dw = sum of dz x_hat, db = sum of dz
+//
+// Two passes over the rows, one kernel each: sums of pieces, then outputs, whose
+// blocks add up the pieces of their sample first (a kernel between the two for that would
+// cost its launch). Bound by memory: x (and dy) are read twice, the second time largely from
+// the caches.
+//
+// Variances do not suffer from large means: sums are of differences from the
+// piece's first row, channel by channel, and channels and pieces are joined
+// by their means and sums of squared deviations.
+#include <algorithm>
+
+#include "mixing.h"
+#include "row_words.h"
+
+namespace smc {
+namespace {
+
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWaves = kGroupThreads / 64;
+static_assert(kMaxGroupChannels == kGroupThreads * W, "a row is held by a block");
+
+// ---- pieces --------------------------------------------------------------------
+// The rows are cut at every multiple of 2^rows_log and at the samples' borders.
+// Runs: the rows before the first sample, each sample, the rows after the last
+// (without offsets, one run). Piece number = run + multiples passed: it grows
+// with the rows, run r owns the numbers from (begin >> rows_log) + r on, one at least, and
+// what a piece holds follows from the offsets alone, however uneven they are.
+
+struct Piece {
+    int run;            // 0: before the samples, samples + 1: after them
+    int begin, end;     // rows
+    int run_begin, run_end;
+};
+
+// Offsets outside [0, n] or out of order make wrong, but valid, row ranges.
+__device__ __forceinline__ int run_start(const GroupArgs& a, int run) {
+    if (run <= 0) return 0;
+    if (run > a.samples + 1) return (int)a.n;
+    return min(max(a.offsets[run - 1], 0), (int)a.n);
+}
+
+__device__ __forceinline__ Piece piece_of(const GroupArgs& a, int number) {
+    Piece p;
+    if (!a.offsets) {
+        p.run = 1;
+        p.run_begin = 0;
+        p.run_end = (int)a.n;
+        p.begin = (int)min((int64_t)number << a.rows_log, a.n);
+        p.end = (int)min((int64_t)(number + 1) << a.rows_log, a.n);
+        return p;
+    }
+    // the last run that owns a number up to this one
+    int run = -1;
+    const int lane = threadIdx.x & 63;
+    for (int r0 = 0; r0 < a.samples + 2; r0 += 64) {
+        const int r = r0 + lane;
+        const bool in = r < a.samples + 2 && (run_start(a, r) >> a.rows_log) + r <= number;
+        run += __popcll(__ballot(in));
+    }
+    run = __builtin_amdgcn_readfirstlane(max(run, 0));
+    p.run = run;
+    p.run_begin = run_start(a, run);
+    p.run_end = max(p.run_begin, run_start(a, run + 1));
+    const int64_t cut = (int64_t)max(number - run, 0) << a.rows_log;
+    p.begin = (int)min(max((int64_t)p.run_begin, cut), (int64_t)p.run_end);
+    p.end = (int)max((int64_t)p.begin, min((int64_t)p.run_end, cut + ((int64_t)1 << a.rows_log)));
+    return p;
+}
+
+// First number of a run, and of the run's last row.
+__device__ __forceinline__ int first_piece(const GroupArgs& a, const Piece& p) {
+    return (p.run_begin >> a.rows_log) + (a.offsets ? p.run : 0);
+}
+__device__ __forceinline__ int last_piece(const GroupArgs& a, const Piece& p) {
+    const int row = max(p.run_begin, p.run_end - 1);
+    return (row >> a.rows_log) + (a.offsets ? p.run : 0);
+}
+__device__ __forceinline__ bool is_sample(const GroupArgs& a, const Piece& p) {
+    return !a.offsets || (p.run >= 1 && p.run <= a.samples);
+}
+
+// ---- sums over a block ------------------------------------------------------------
+
+// v of the threads that share `word`, rows 0 .. rows - 1 of them (thread = row words + word): the
+// sums end up in row 0. Halves are joined in a fixed order. s: N x 512 floats.
+template <int N>
+__device__ __forceinline__ void sum_rows(float (&v)[N], int rows, int words, int row, int word, float* s) {
+    while (rows > 1) {
+        const int half = (rows + 1) >> 1;
+        __syncthreads();
+        if (row >= half && row < rows)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e * (kGroupThreads / 2) + (row - half) * words + word] = v[e];
+        __syncthreads();
+        if (row + half < rows)
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] += s[e * (kGroupThreads / 2) + row * words + word];
+        rows = half;
+    }
+    __syncthreads();
+}
+
+// How a block's threads lie over rows of c channels.
+struct Lay {
+    int words, rows, word, row;
+    bool ok;
+    __device__ explicit Lay(int c) {
+        words = (c + W - 1) / W;
+        rows = kGroupThreads / words;
+        row = threadIdx.x / words;
+        word = threadIdx.x - row * words;
+        ok = row < rows;
+    }
+};
+
+// Floats of dynamic LDS: sum_rows of 2 W values, or two values a channel.
+inline size_t lds_floats(int c) { return std::max<size_t>((size_t)2 * W * kGroupThreads / 2, (size_t)2 * c); }
+
+// ---- forward -------------------------------------------------------------------------
+
+// A piece's mean and sum of squared deviations, each group.
+template <int DT, bool A>
+__global__ __launch_bounds__(kGroupThreads) void k_group_sums(GroupArgs a) {
+    extern __shared__ float s[];
+    const int number = (int)blockIdx.x;
+    const Piece p = piece_of(a, number);
+    if (!is_sample(a, p) || p.begin >= p.end) return;
+    const Lay l(a.c);
+    const int c = l.word * W, left = a.c - c;
+    float base[W], sum[2 * W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) base[e] = sum[e] = sum[W + e] = 0.f;
+    if (l.ok) {
+        load_f32<DT, A>(a.x, (int64_t)p.begin * a.ldx + c, left, base);
+#pragma unroll 4
+        for (int r = p.begin + l.row; r < p.end; r += l.rows) {
+            float v[W];
+            load_f32<DT, A>(a.x, (int64_t)r * a.ldx + c, left, v);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float d = v[e] - base[e];
+                sum[e] += d;
+                sum[W + e] += d * d;
+            }
+        }
+    }
+    sum_rows(sum, l.rows, l.words, l.row, l.word, s);
+    const float rows = (float)(p.end - p.begin);
+    if (l.ok && l.row == 0)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < left) {
+                const float off = sum[e] / rows;
+                s[c + e] = base[e] + off;                               // the channel's mean
+                s[a.c + c + e] = fmaxf(sum[W + e] - sum[e] * off, 0.f); // and squared deviations
+            }
+    __syncthreads();
+    const int per = a.c / a.groups, lane = threadIdx.x & 63;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += kGroupWaves) {
+        const float* mean_of = s + g * per;
+        const float first = mean_of[0];
+        float m = 0.f;
+        for (int k = lane; k < per; k += 64) m += mean_of[k] - first;
+        const float mean = first + lane_sum<64>(m) / (float)per;
+        float m2 = 0.f;
+        for (int k = lane; k < per; k += 64) {
+            const float d = mean_of[k] - mean;
+            m2 += mean_of[a.c + k] + rows * (d * d);
+        }
+        m2 = lane_sum<64>(m2);
+        if (lane == 0) {
+            float* o = a.by_group + ((int64_t)number * a.groups + g) * 2;
+            o[0] = mean;
+            o[1] = m2;
+        }
+    }
+}
+
+// Mean and rstd of each group of a piece's sample, from its pieces, into s_stats
+// [groups][2]. s: 2 x 1024 floats.
+__device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float* s_stats) {
+    const int first = first_piece(a, p), count = p.run_end > p.run_begin ? last_piece(a, p) - first + 1 : 0;
+    const int per = a.c / a.groups;
+    for (int g0 = 0; g0 < a.groups; g0 += kGroupThreads) {
+        const int wide = min(a.groups - g0, kGroupThreads);
+        const int parts = kGroupThreads / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
+        const bool ok = part < parts && count > 0;
+        float v[2] = {0.f, 0.f};
+        float base = 0.f;
+        if (ok) {
+            const float* from = a.by_group + ((int64_t)first * a.groups + g0 + g) * 2;
+            base = from[0];
+#pragma unroll 4
+            for (int k = part; k < count; k += parts) {
+                // rows of the piece: the run's, from one multiple to the next
+                const int64_t cut = (int64_t)((p.run_begin >> a.rows_log) + k) << a.rows_log;
+                const float rows = (float)(min((int64_t)p.run_end, cut + ((int64_t)1 << a.rows_log)) -
+                                           max((int64_t)p.run_begin, cut));
+                const float d = from[(int64_t)k * a.groups * 2] - base;
+                v[0] += rows * d;
+                v[1] += from[(int64_t)k * a.groups * 2 + 1] + rows * (float)per * (d * d);
+            }
+        }
+        int rows = min(parts, max(count, 1));
+        while (rows > 1) {
+            const int half = (rows + 1) >> 1;
+            __syncthreads();
+            if (part >= half && part < rows) {
+                s[(part - half) * wide + g] = v[0];
+                s[kGroupThreads + (part - half) * wide + g] = v[1];
+            }
+            __syncthreads();
+            if (part + half < rows) {
+                v[0] += s[part * wide + g];
+                v[1] += s[kGroupThreads + part * wide + g];
+            }
+            rows = half;
+        }
+        if (part == 0) {
+            float mean = 0.f, rstd = 0.f;
+            if (count > 0) {
+                const float n = (float)(p.run_end - p.run_begin), off = v[0] / n;
+                mean = base + off;
+                rstd = inverse_root(fmaxf(v[1] - v[0] * off * (float)per, 0.f) / (n * (float)per) + a.eps);
+            }
+            s_stats[(g0 + g) * 2] = mean;
+            s_stats[(g0 + g) * 2 + 1] = rstd;
+        }
+        __syncthreads();
+    }
+}
+
+template <int DT, bool A, int ACT>
+__device__ __forceinline__ void write_rows(const GroupArgs& a, const Piece& p, const Lay& l, const float* s_stats) {
+    if (!l.ok) return;
+    const int c = l.word * W, left = a.c - c, per = a.c / a.groups;
+    float mean[W], scale[W], shift[W];
+    load_f32<DT, A>(a.weight, c, left, scale);
+    load_f32<DT, A>(a.bias, c, left, shift);
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        const int g = (A || e < left ? c + e : c) / per;
+        mean[e] = s_stats[2 * g];
+        scale[e] *= s_stats[2 * g + 1];
+    }
+#pragma unroll 4
+    for (int r = p.begin + l.row; r < p.end; r += l.rows) {
+        float v[W];
+        load_f32<DT, A>(a.x, (int64_t)r * a.ldx + c, left, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = act_value<ACT>((v[e] - mean[e]) * scale[e] + shift[e]);
+        store_16<DT, A>(a.y, (int64_t)r * a.ldy + c, left, v);
+    }
+}
+
+template <int DT, bool A>
+__device__ __forceinline__ void write_zeros(const GroupArgs& a, const Piece& p, const Lay& l) {
+    if (!l.ok) return;
+    const float v[W] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int r = p.begin + l.row; r < p.end; r += l.rows)
+        store_16<DT, A>(a.y, (int64_t)r * a.ldy + l.word * W, a.c - l.word * W, v);
+}
+
+template <int DT, bool A>
+__global__ __launch_bounds__(kGroupThreads) void k_group_write(GroupArgs a) {
+    extern __shared__ float s[];
+    const int number = (int)blockIdx.x;
+    const Piece p = piece_of(a, number);
+    const Lay l(a.c);
+    if (!is_sample(a, p)) return write_zeros<DT, A>(a, p, l);
+    float* const s_stats = s + 2 * kGroupThreads;
+    join_pieces(a, p, s, s_stats);
+    if (a.stats && number == first_piece(a, p)) {
+        float* o = a.stats + (int64_t)(a.offsets ? p.run - 1 : 0) * a.groups * 2;
+        for (int i = threadIdx.x; i < 2 * a.groups; i += kGroupThreads) o[i] = s_stats[i];
+    }
+    with_act(a.act, [&](auto act) SMC_INLINE { write_rows<DT, A, decltype(act)::value>(a, p, l, s_stats); });
+}
+
+// ---- backward ----------------------------------------------------------------------
+
+// What a thread needs of its channels.
+struct Channels {
+    float w[W], b[W], mean[W], rstd[W];
+    template <int DT, bool A>
+    __device__ __forceinline__ void load(const GroupArgs& a, const Piece& p, int c, int left) {
+        load_f32<DT, A>(a.weight, c, left, w);
+        load_f32<DT, A>(a.bias, c, left, b);
+        const float* stats = a.stats + (int64_t)(a.offsets ? p.run - 1 : 0) * a.groups * 2;
+        const int per = a.c / a.groups;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int g = (A || e < left ? c + e : c) / per;
+            mean[e] = stats[2 * g];
+            rstd[e] = stats[2 * g + 1];
+        }
+    }
+};
+
+// x_hat and dz of an element. The same bits in both passes, and in gradient_rows a - mean(a) is
+// exactly zero in a sample of one element: no fused multiply-adds.
+template <int ACT>
+__device__ __forceinline__ void slope_of(float v, float dy, const Channels& ch, int e, float& xh, float& dz) {
+#pragma clang fp contract(off)
+    xh = (v - ch.mean[e]) * ch.rstd[e];
+    dz = dy * act_slope<ACT>(xh * ch.w[e] + ch.b[e]);
+}
+
+// A piece's sums of dz and dz x_hat, each channel; and of a and a x_hat, each group.
+template <int DT, bool A, int ACT>
+__device__ __forceinline__ void gradient_sums(const GroupArgs& a, const Piece& p, const Lay& l, float (&sum)[2 * W]) {
+    const int c = l.word * W, left = a.c - c;
+    Channels ch;
+    ch.load<DT, A>(a, p, c, left);
+#pragma unroll 2
+    for (int r = p.begin + l.row; r < p.end; r += l.rows) {
+        float v[W], dy[W];
+        load_f32<DT, A>(a.x, (int64_t)r * a.ldx + c, left, v);
+        load_f32<DT, A>(a.dy, (int64_t)r * a.lddy + c, left, dy);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            float xh, dz;
+            slope_of<ACT>(v[e], dy[e], ch, e, xh, dz);
+            sum[e] += dz;
+            sum[W + e] += dz * xh;
+        }
+    }
+}
+
+template <int DT, bool A>
+__global__ __launch_bounds__(kGroupThreads) void k_group_gradient_sums(GroupArgs a) {
+    extern __shared__ float s[];
+    const int number = (int)blockIdx.x;
+    const Piece p = piece_of(a, number);
+    const Lay l(a.c);
+    const int c = l.word * W, left = a.c - c;
+    float sum[2 * W];
+#pragma unroll
+    for (int e = 0; e < 2 * W; ++e) sum[e] = 0.f;
+    if (l.ok && is_sample(a, p) && p.begin < p.end)
+        with_act(a.act, [&](auto act) SMC_INLINE { gradient_sums<DT, A, decltype(act)::value>(a, p, l, sum); });
+    sum_rows(sum, l.rows, l.words, l.row, l.word, s);
+    if (l.ok && l.row == 0)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e < left) {
+                s[c + e] = sum[e];
+                s[a.c + c + e] = sum[W + e];
+            }
+    __syncthreads();
+    float* o = a.by_channel + (int64_t)number * 2 * a.c;
+    for (int i = threadIdx.x; i < 2 * a.c; i += kGroupThreads) o[i] = s[i];
+    const int per = a.c / a.groups, lane = threadIdx.x & 63;
+    for (int g = threadIdx.x >> 6; g < a.groups; g += kGroupWaves) {
+        float m1 = 0.f, m2 = 0.f;
+        for (int k = lane; k < per; k += 64) {
+            const float w = to_f32<DT>(static_cast<const uint16_t*>(a.weight)[g * per + k]);
+            m1 += w * s[g * per + k];
+            m2 += w * s[a.c + g * per + k];
+        }
+        m1 = lane_sum<64>(m1);
+        m2 = lane_sum<64>(m2);
+        if (lane == 0) {
+            a.by_group[((int64_t)number * a.groups + g) * 2] = m1;
+            a.by_group[((int64_t)number * a.groups + g) * 2 + 1] = m2;
+        }
+    }
+}
+
+// The means of a and a x_hat over a piece's sample, each group.
+__device__ void join_gradient_pieces(const GroupArgs& a, const Piece& p, float* s, float* s_means) {
+    const int first = first_piece(a, p), count = p.run_end > p.run_begin ? last_piece(a, p) - first + 1 : 0;
+    for (int g0 = 0; g0 < a.groups; g0 += kGroupThreads) {
+        const int wide = min(a.groups - g0, kGroupThreads);
+        const int parts = kGroupThreads / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
+        float v[2] = {0.f, 0.f};
+        if (part < parts) {
+            const float* from = a.by_group + ((int64_t)first * a.groups + g0 + g) * 2;
+#pragma unroll 4
+            for (int k = part; k < count; k += parts) {
+                v[0] += from[(int64_t)k * a.groups * 2];
+                v[1] += from[(int64_t)k * a.groups * 2 + 1];
+            }
+        }
+        int rows = min(parts, max(count, 1));
+        while (rows > 1) {
+            const int half = (rows + 1) >> 1;
+            __syncthreads();
+            if (part >= half && part < rows) {
+                s[(part - half) * wide + g] = v[0];
+                s[kGroupThreads + (part - half) * wide + g] = v[1];
+            }
+            __syncthreads();
+            if (part + half < rows) {
+                v[0] += s[part * wide + g];
+                v[1] += s[kGroupThreads + part * wide + g];
+            }
+            rows = half;
+        }
+        if (part == 0) {
+            const float n = (float)max(p.run_end - p.run_begin, 1) * (float)(a.c / a.groups);
+            s_means[(g0 + g) * 2] = v[0] / n;
+            s_means[(g0 + g) * 2 + 1] = v[1] / n;
+        }
+        __syncthreads();
+    }
+}
+
+template <int DT, bool A, int ACT>
+__device__ __forceinline__ void gradient_rows(const GroupArgs& a, const Piece& p, const Lay& l, const float* s_means) {
+#pragma clang fp contract(off)
+    if (!l.ok) return;
+    const int c = l.word * W, left = a.c - c, per = a.c / a.groups;
+    Channels ch;
+    ch.load<DT, A>(a, p, c, left);
+    float m1[W], m2[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        const int g = (A || e < left ? c + e : c) / per;
+        m1[e] = s_means[2 * g];
+        m2[e] = s_means[2 * g + 1];
+    }
+#pragma unroll 2
+    for (int r = p.begin + l.row; r < p.end; r += l.rows) {
+        float v[W], dy[W];
+        load_f32<DT, A>(a.x, (int64_t)r * a.ldx + c, left, v);
+        load_f32<DT, A>(a.dy, (int64_t)r * a.lddy + c, left, dy);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            float xh, dz;
+            slope_of<ACT>(v[e], dy[e], ch, e, xh, dz);
+            v[e] = ch.rstd[e] * ((dz * ch.w[e] - m1[e]) - xh * m2[e]);
+        }
+        store_16<DT, A>(a.y, (int64_t)r * a.ldy + c, left, v);
+    }
+}
+
+// dw and db of 8 channels: every piece's sums, in 64 strided runs joined by a tree.
+template <int DT>
+__device__ __forceinline__ void sum_channels(const GroupArgs& a, int block, float* s) {
+    const int x = threadIdx.x & 15, run = threadIdx.x >> 4;        // 8 channels of db, then of dw
+    const int c = block * 8 + (x & 7);
+    float v = 0.f;
+    if (c < a.c) {
+        const float* from = a.by_channel + (x >> 3) * a.c + c;
+#pragma unroll 8
+        for (int k = run; k < a.pieces; k += 64) v += from[(int64_t)k * 2 * a.c];
+    }
+    s[run * 17 + x] = v;
+    __syncthreads();
+    for (int o = 32; o > 0; o >>= 1) {
+        if (run < o) s[run * 17 + x] += s[(run + o) * 17 + x];
+        __syncthreads();
+    }
+    if (run == 0 && c < a.c) static_cast<uint16_t*>(x >> 3 ? a.dweight : a.dbias)[c] = (uint16_t)from_f32<DT>(s[x]);
+}
+
+// dx of a piece; the blocks after the pieces' add up dw and db.
+template <int DT, bool A>
+__global__ __launch_bounds__(kGroupThreads) void k_group_gradient_write(GroupArgs a) {
+    extern __shared__ float s[];
+    const int number = (int)blockIdx.x;
+    if (number >= a.pieces) return sum_channels<DT>(a, number - a.pieces, s);
+    const Piece p = piece_of(a, number);
+    const Lay l(a.c);
+    if (!is_sample(a, p)) return write_zeros<DT, A>(a, p, l);
+    if (p.begin >= p.end) return;
+    float* const s_means = s + 2 * kGroupThreads;
+    join_gradient_pieces(a, p, s, s_means);
+    with_act(a.act, [&](auto act) SMC_INLINE { gradient_rows<DT, A, decltype(act)::value>(a, p, l, s_means); });
+}
+
+template <int DT, bool A>
+hipError_t group_norm_t(const GroupArgs& a, hipStream_t s) {
+    launch(k_group_sums<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), lds_floats(a.c) * 4, s, a);
+    launch(k_group_write<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), (2 * kGroupThreads + 2 * (size_t)a.groups) * 4, s, a);
+    return hipGetLastError();
+}
+
+template <int DT, bool A>
+hipError_t group_norm_backward_t(const GroupArgs& a, hipStream_t s) {
+    launch(k_group_gradient_sums<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), lds_floats(a.c) * 4, s, a);
+    launch(k_group_gradient_write<DT, A>, dim3((unsigned)(a.pieces + (a.c + 7) / 8)), dim3(kGroupThreads),
+           (2 * kGroupThreads + 2 * (size_t)a.groups) * 4, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Rows of a piece: one piece a CU, but no fewer than give each thread 4 words.
+void group_plan(GroupArgs& a) {
+    const int64_t words = (a.c + W - 1) / W;
+    const int64_t rows = std::max<int64_t>((a.n + device_cus() - 1) / device_cus(), 4 * kGroupThreads / words);
+    a.rows_log = 0;
+    while (((int64_t)1 << a.rows_log) < rows) ++a.rows_log;
+    a.pieces = (int)((a.n + ((int64_t)1 << a.rows_log) - 1) >> a.rows_log);
+    if (a.offsets) a.pieces += a.samples + 2;
+    a.pieces = std::max(a.pieces, 1);
+}
+
+hipError_t launch_group_norm(const GroupArgs& a, int dt, hipStream_t s) {
+    if (dt == kF16) return a.vec ? group_norm_t<kF16, true>(a, s) : group_norm_t<kF16, false>(a, s);
+    return a.vec ? group_norm_t<kBF16, true>(a, s) : group_norm_t<kBF16, false>(a, s);
+}
+
+hipError_t launch_group_norm_backward(const GroupArgs& a, int dt, hipStream_t s) {
+    if (dt == kF16) return a.vec ? group_norm_backward_t<kF16, true>(a, s) : group_norm_backward_t<kF16, false>(a, s);
+    return a.vec ? group_norm_backward_t<kBF16, true>(a, s) : group_norm_backward_t<kBF16, false>(a, s);
+}
+
+}  // namespace smc

@@ -15,7 +15,7 @@
 // 95,000 x 128 18.5 us (5.3 TB/s) and 4.0 us for the sums of dw.
 #include <algorithm>
 
-#include "pointwise_gemm.h"
+#include "row_words.h"
 
 namespace smc {
 namespace {
@@ -23,33 +23,6 @@ namespace {
 constexpr int kNormThreads = 256;       // what grid_of counts on
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;      // 2^-126
-
-constexpr int W = 8;        // elements of a word
-
-// A word of a row as float32: elements i .. i + 7, of which `left` exist (all of
-// them where ALIGNED, which also means that the address is a multiple of 16).
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void load_f32(const void* p, int64_t i, int left, float (&v)[W]) {
-    const uint16_t* e0 = static_cast<const uint16_t*>(p) + i;
-    const u32x4 u = ALIGNED ? *reinterpret_cast<const u32x4*>(e0) : left >= W ? load_unaligned(e0) : load_tail(e0, left);
-#pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = to_f32<DT>((u[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
-}
-
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void store_16(void* p, int64_t i, int left, const float (&v)[W]) {
-    uint16_t* e0 = static_cast<uint16_t*>(p) + i;
-    const u32x4 u = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
-    if (ALIGNED) {
-        *reinterpret_cast<u32x4*>(e0) = u;
-    } else if (left >= W) {
-        __builtin_memcpy(e0, &u, 16);
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (e < left) e0[e] = (uint16_t)(u[e >> 1] >> ((e & 1) * 16));
-    }
-}
 
 template <bool ALIGNED>
 __device__ __forceinline__ void store_e4m3(void* p, int64_t i, int left, const float (&v)[W]) {
@@ -77,9 +50,6 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     const float s = __uint_as_float(amax_bits) / kE4m3Max;
     return s < kTinyScale ? kTinyScale : s;        // NaN stays
 }
-
-// 1 / sqrt(v); a row of zeros without an epsilon stays zeros.
-__device__ __forceinline__ float inverse_root(float v) { return v == 0.f ? 0.f : 1.f / sqrtf(v); }
 
 // L lanes a row, NV words of W elements a lane, the row in registers.
 template <int DT, bool A, int L, int NV>
