@@ -695,6 +695,69 @@ int smc_group_norm_backward(const smc_group_norm_t* args, void* stream);
 size_t smc_group_norm_workspace(const smc_group_norm_t* args);
 size_t smc_group_norm_backward_workspace(const smc_group_norm_t* args);
 
+/*
+ * Windows of rows, the index that attention walks: made once from the rows' order,
+ * used by every layer and both passes on the same rows.
+ * Place p of the window order is row order[p] (order NULL: row p), and window w is the
+ * places offsets[w] .. offsets[w + 1] - 1, ascending, within [0, n]. Windows may be empty;
+ * places of no window may be left before the first and after the last. order holds every
+ * row once. coords (or NULL: no bias then): each row's voxel coordinates, as smc_map_build
+ * takes them; (ex, ey, ez) is how many cells a window spans along x, y and z at most (its
+ * rows' coordinates less their lowest are within [0, ex) and so on), ex + ey + ez <= 128.
+ * The call waits for the device once and returns SMC_ERR_RANGE or SMC_ERR_DUPLICATE where
+ * any of this does not hold; the plan may not be used then. It keeps no pointer but
+ * plan's: offsets, order and coords may go, and a copy of the structure is as good as it.
+ * A plan belongs to the GPU it was made on, and may be used there from any stream.
+ */
+typedef struct smc_windows_s {
+    int64_t n;                /* rows, = places */
+    int64_t windows;          /* 0 .. 2^24 */
+    const int32_t* offsets;   /* device [windows + 1] */
+    const int32_t* order;     /* device [n] or NULL */
+    const int32_t* coords;    /* device [n, coord_cols] or NULL */
+    int32_t coord_cols;       /* 3: x, y, z; 4: b, x, y, z (b is not read) */
+    int32_t ex, ey, ez;       /* cells of a window, 0 without coords */
+    void* plan;               /* device memory of smc_windows_bytes(n, windows) bytes, 16-byte aligned */
+    size_t plan_bytes;
+    int32_t tiles64, tiles128, longest;     /* written by smc_windows_build */
+} smc_windows_t;
+size_t smc_windows_bytes(int64_t n, int64_t windows);
+int smc_windows_build(smc_windows_t* windows, void* stream);
+
+/*
+ * Attention inside windows, heads side by side in the channels: for each row i, head h and
+ * the rows j of i's window
+ *   s_ij = scale q_i . k_j + bias_ij,  P = softmax over j,  out_i = sum_j P_ij v_j
+ *   bias_ij = sum over the axes of bias[axis][reach + clamp(c_i - c_j, -reach, reach)][h]
+ * with c the rows' cells. Head h reads head h / (heads / kv_heads) of k and v. Rows of no
+ * window come out as zeros, and so does a row whose scores are all -inf. Windows do not
+ * reach each other, also where values are not finite. Infinite entries of bias count as the
+ * type's largest values; a NaN in it reaches every row of its head that lies at that
+ * distance from a cell of the window's extent.
+ * lse (or NULL): log sum_j exp(s_ij), float32 [heads, n] by place (not by row), -inf for
+ * zeros' rows; the backward pass reads it. Scores, softmax and sums are float32; P is
+ * rounded to dtype for its product with v. out may not overlap q, k or v.
+ */
+typedef struct smc_attention_s {
+    const smc_windows_t* windows;   /* host structure, built */
+    int32_t heads, kv_heads;  /* kv_heads divides heads */
+    int32_t head_dim;         /* 1 .. 128 */
+    int32_t dtype;            /* SMC_DTYPE_BF16 or _F16 */
+    float scale;              /* > 0 */
+    int32_t reach;            /* 1 .. 127 with bias */
+    const void* bias;         /* [3, 2 reach + 1, heads] or NULL */
+    const void* q;            /* [n, heads * head_dim] */
+    int64_t ldq;
+    const void* k;            /* [n, kv_heads * head_dim] */
+    int64_t ldk;
+    const void* v;            /* [n, kv_heads * head_dim] */
+    int64_t ldv;
+    void* out;                /* [n, heads * head_dim] */
+    int64_t ld_out;
+    float* lse;               /* [heads, n] or NULL */
+} smc_attention_t;
+int smc_window_attention(const smc_attention_t* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,8 @@ import os
 __all__ = ["KernelMap", "PackedWeights", "pack_weights", "subm_conv3d", "lib", "library_path",
            "SmconvError", "ROUTES", "EXPORTED_SYMBOLS", "use_torch_allocator", "probe_mfma_bf16",
            "probe_copy", "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated",
-           "gated_backward", "quantize_weight", "ACTIVATIONS", "group_norm", "group_norm_backward"]
+           "gated_backward", "quantize_weight", "ACTIVATIONS", "group_norm", "group_norm_backward",
+           "Windows", "window_attention"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsmconv.so")
@@ -47,7 +48,8 @@ EXPORTED_SYMBOLS = [
     "smc_gated_backward", "smc_linear_workspace", "smc_gated_workspace",
     "smc_linear_backward_workspace", "smc_gated_backward_workspace", "smc_weight_quantize",
     "smc_group_norm", "smc_group_norm_backward", "smc_group_norm_workspace",
-    "smc_group_norm_backward_workspace",
+    "smc_group_norm_backward_workspace", "smc_windows_bytes", "smc_windows_build",
+    "smc_window_attention",
 ]
 STAGES = ["map", "neighbours", "mask_sort", "compact", "gemm", "centre"]
 
@@ -120,6 +122,27 @@ class GroupNormArgs(ctypes.Structure):
     ]
 
 
+class WindowsArgs(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("windows", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+        ("order", ctypes.c_void_p), ("coords", ctypes.c_void_p), ("coord_cols", ctypes.c_int32),
+        ("ex", ctypes.c_int32), ("ey", ctypes.c_int32), ("ez", ctypes.c_int32),
+        ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("tiles64", ctypes.c_int32),
+        ("tiles128", ctypes.c_int32), ("longest", ctypes.c_int32),
+    ]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("windows", ctypes.POINTER(WindowsArgs)), ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("reach", ctypes.c_int32), ("bias", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p),
+        ("ldk", ctypes.c_int64), ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("lse", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -181,7 +204,8 @@ def lib():
     for name, args in (("smc_rms_norm", NormArgs), ("smc_rms_norm_backward", NormBackwardArgs),
                        ("smc_linear", ProductArgs), ("smc_gated", ProductArgs),
                        ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs),
-                       ("smc_group_norm", GroupNormArgs), ("smc_group_norm_backward", GroupNormArgs)):
+                       ("smc_group_norm", GroupNormArgs), ("smc_group_norm_backward", GroupNormArgs),
+                       ("smc_windows_build", WindowsArgs), ("smc_window_attention", AttentionArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
         getattr(L, name).restype = i32
     for name, args in (("smc_linear_workspace", ProductArgs), ("smc_gated_workspace", ProductArgs),
@@ -193,6 +217,8 @@ def lib():
         getattr(L, name).restype = ctypes.c_size_t
     L.smc_rms_norm_backward_workspace.argtypes = [i64, i32]
     L.smc_rms_norm_backward_workspace.restype = ctypes.c_size_t
+    L.smc_windows_bytes.argtypes = [i64, i64]
+    L.smc_windows_bytes.restype = ctypes.c_size_t
     L.smc_weight_quantize.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp]
     L.smc_weight_quantize.restype = i32
     _lib = L
@@ -855,6 +881,108 @@ def group_norm_backward(dy, x, weight, bias, groups: int, stats, offsets=None, a
     a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
     _check(L.smc_group_norm_backward(a, _raw_stream(dev)))
     return dx, dweight, dbias
+
+
+class Windows:
+    """The windows that window_attention works in, made once for all layers on the
+    same rows (waits for the device once).
+
+    order: int32 [N] CUDA tensor, every row once, window after window (None: the rows as
+    they lie); window w is the places offsets[w] .. offsets[w + 1] - 1 of it (int32
+    [windows + 1] CUDA tensor); places of no window may be left at both ends. For a
+    relative position bias: coords, the rows' int32 [N, 4] (b, x, y, z) or [N, 3]
+    coordinates, and extent, how many cells a window spans along x, y and z at most (128
+    in all). SmconvError where a row is listed twice, an offset or row is out of range or
+    a window is larger than that."""
+
+    def __init__(self, offsets, n: int, order=None, coords=None, extent=None, stream=None):
+        import torch
+        if not isinstance(offsets, torch.Tensor) or not offsets.is_cuda:
+            raise TypeError("offsets must be a CUDA (HIP) torch tensor")
+        dev = offsets.device
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError(f"offsets must be [windows + 1], got {list(offsets.shape)}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, offsets on {dev}")
+        if (coords is None) != (extent is None):
+            raise ValueError("coords and extent come together")
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            a = WindowsArgs(int(n), offsets.shape[0] - 1,
+                            _vector(offsets, "offsets", torch.int32, dev, offsets.shape[0]))
+            if order is not None:
+                a.order = _vector(order, "order", torch.int32, dev, a.n)
+            if coords is not None:
+                _need(coords, torch.int32, "coords", 2)
+                if coords.device != dev or coords.shape[0] != a.n or coords.shape[1] not in (3, 4):
+                    raise ValueError(f"coords must be [{a.n}, 3 or 4] on {dev}, got {list(coords.shape)}")
+                a.coords, a.coord_cols = coords.data_ptr(), coords.shape[1]
+                a.ex, a.ey, a.ez = (int(e) for e in extent)
+            a.plan_bytes = lib().smc_windows_bytes(a.n, a.windows)
+            self._plan = torch.empty(a.plan_bytes, dtype=torch.uint8, device=dev)
+            a.plan = self._plan.data_ptr()
+            _check(lib().smc_windows_build(a, _raw_stream(dev)))
+        a.offsets = a.order = a.coords = None
+        self._args, self.device, self.n = a, dev, a.n
+        self.longest = a.longest
+
+
+def _attention_args(q, k, v, windows, heads, bias, scale):
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q, "q")
+    n, c = q.shape
+    if not isinstance(windows, Windows):
+        raise TypeError("windows must be a Windows")
+    if windows.device != dev or windows.n != n:
+        raise ValueError(f"windows are of {windows.n} rows on {windows.device}, q has {n} on {dev}")
+    if heads < 1 or c % heads:
+        raise ValueError(f"{c} channels in {heads} heads")
+    dim = c // heads
+    if k.dim() != 2 or k.shape[1] < dim or k.shape[1] % dim or heads % (k.shape[1] // dim):
+        raise ValueError(f"k is {list(k.shape)}, heads are {heads} of {dim}")
+    qp, ldq = _rows(q, "q", dt, dev)
+    kp, ldk = _rows(k, "k", dt, dev, (n, k.shape[1]))
+    vp, ldv = _rows(v, "v", dt, dev, (n, k.shape[1]))
+    bp, reach = None, 0
+    if bias is not None:
+        _of(bias, "bias", dt, dev)
+        if bias.dim() != 3 or bias.shape[0] != 3 or bias.shape[1] % 2 == 0 or bias.shape[2] != heads \
+                or not bias.is_contiguous():
+            raise ValueError(f"bias must be contiguous [3, 2 reach + 1, {heads}], got {list(bias.shape)}")
+        if windows._args.ex == 0:
+            raise ValueError("a bias needs windows with coords")
+        bp, reach = bias.data_ptr(), bias.shape[1] // 2
+    return AttentionArgs(ctypes.pointer(windows._args), heads, k.shape[1] // dim, dim, code,
+                         dim ** -0.5 if scale is None else scale, reach, bp, qp, ldq, kp, ldk, vp, ldv)
+
+
+def window_attention(q, k, v, windows: Windows, heads: int, bias=None, scale=None, lse: bool = False,
+                     out=None, stream=None):
+    """out_i = sum over the rows j of i's window of softmax_j(scale q_i k_j + bias_ij) v_j,
+    head by head.
+
+    q: bf16 or f16 [N, heads D] CUDA tensor, k and v [N, kv_heads D] with kv_heads dividing
+    heads (rows of all may be strided, such as columns of one projection's output), D up to
+    128; scale: D ** -0.5 by default. bias: a learned table [3, 2 reach + 1, heads], bias_ij
+    the sum over the axes of bias[axis, reach + clamp(c_i - c_j, -reach, reach)] with c the
+    windows' coords. Rows of no window come out as zeros. With lse (out, lse), lse float32
+    [heads, N] by place of the window order, as window_attention_backward takes it."""
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return window_attention(q, k, v, windows, heads, bias, scale, lse, out)
+    a = _attention_args(q, k, v, windows, heads, bias, scale)
+    n, c = q.shape
+    if out is None:
+        out = q.new_empty((n, c))
+        a.out, a.ld_out = out.data_ptr(), c
+    else:
+        a.out, a.ld_out = _rows(out, "out", q.dtype, q.device, (n, c))
+    if lse:
+        kept = q.new_empty((heads, n), dtype=torch.float32)
+        a.lse = kept.data_ptr()
+    _check(lib().smc_window_attention(a, _raw_stream(q.device)))
+    return (out, kept) if lse else out
 
 
 def probe_mfma_bf16(iters: int, stream=None) -> float:

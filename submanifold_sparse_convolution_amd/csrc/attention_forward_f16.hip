@@ -1,0 +1,8 @@
+// Window attention on f16 rows (a file a type: they compile in parallel).
+#include "attention_forward.h"
+
+namespace smc {
+
+hipError_t launch_attention_f16(const AttentionArgs& a, bool wide, hipStream_t s) { return attention_of_type<kF16>(a, wide, s); }
+
+}  // namespace smc

@@ -39,4 +39,78 @@ void group_plan(GroupArgs& a);                  // rows_log and pieces, from n, 
 hipError_t launch_group_norm(const GroupArgs& a, int dt, hipStream_t s);
 hipError_t launch_group_norm_backward(const GroupArgs& a, int dt, hipStream_t s);
 
+// ---- windows (window_kernels.hip) ----
+// A place is a position in the window order. Header, places, tiles of 64 and of 128
+// places lie behind each other in the plan.
+struct WindowPlace {
+    int row;            // row of the tensors
+    uint32_t cells;     // x, ex + y, ex + ey + z of the row's cell in its window, 8 bits each
+};
+struct WindowTile {
+    int first, count;   // places
+    int begin, end;     // of the window; equal: the rows are in no window
+};
+struct WindowHeader {
+    uint32_t status;    // kSt* bits
+    int tiles[2];       // of 64 and of 128 places
+    int longest;        // rows of the longest window
+};
+constexpr int kMaxCells = 128;                  // ex + ey + ez
+constexpr int kMaxReach = 127;                  // cells lie no further apart
+constexpr int64_t kMaxWindows = 1 << 24;
+struct WindowLayout {
+    size_t places, tiles[2], seen, bytes;       // offsets; seen: a bit a row, scratch of the build
+    WindowLayout(int64_t n, int64_t windows) {
+        auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+        places = 256;
+        tiles[0] = places + up((size_t)n * sizeof(WindowPlace));
+        tiles[1] = tiles[0] + up((size_t)(n / 64 + windows + 2) * sizeof(WindowTile));
+        seen = tiles[1] + up((size_t)(n / 128 + windows + 2) * sizeof(WindowTile));
+        bytes = seen + up((size_t)(n + 31) / 32 * 4);
+    }
+};
+struct WindowArgs {
+    int64_t n = 0, windows = 0;
+    const int* offsets = nullptr;   // [windows + 1]
+    const int* order = nullptr;     // [n] or null
+    const int* coords = nullptr;    // [n, cols] or null, x, y, z last
+    int cols = 0;
+    int extent[3] = {0, 0, 0};
+    char* plan = nullptr;
+};
+hipError_t launch_windows(const WindowArgs& a, hipStream_t s);
+
+// ---- window attention (attention_*.hip) ----
+struct AttentionArgs {
+    int64_t n = 0;
+    int heads = 0, kv_heads = 0, dim = 0;
+    float scale = 0.f;
+    const void *q = nullptr, *k = nullptr, *v = nullptr;
+    int64_t ldq = 0, ldk = 0, ldv = 0;
+    const char* plan = nullptr;
+    const WindowPlace* places = nullptr;
+    const WindowTile* tiles = nullptr;
+    int n_tiles = 0;
+    int extent[3] = {0, 0, 0};
+    const void* table = nullptr;    // [3][2 reach + 1][heads] or null
+    int reach = 0;
+    void* out = nullptr;            // backward: read
+    int64_t ldo = 0;
+    float* lse = nullptr;           // [heads][n] by place; forward: or null
+    const void* dout = nullptr;
+    int64_t ld_dout = 0;
+    void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+    int64_t ld_dq = 0, ld_dk = 0, ld_dv = 0;
+    void* dtable = nullptr;
+    float* delta = nullptr;         // [heads][n] by place: sums of dout out
+    float* part = nullptr;          // [tiles][heads][3 (2 reach + 1)] sums of dS
+    float* range = nullptr;         // f16: [tiles of 64][heads + kv_heads] largest |dout| and |v|
+    const WindowTile* tiles64 = nullptr;
+    int n_tiles64 = 0;
+    int vec = 0;                    // every row is made of aligned 16-byte words
+};
+// wide: tiles are of 128 queries, else of 64.
+hipError_t launch_attention_bf16(const AttentionArgs& a, bool wide, hipStream_t s);
+hipError_t launch_attention_f16(const AttentionArgs& a, bool wide, hipStream_t s);
+
 }  // namespace smc

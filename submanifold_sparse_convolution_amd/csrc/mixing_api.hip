@@ -102,6 +102,139 @@ int group(const smc_group_norm_t* a, bool backward, void* stream) {
     return hip_status(launch_group_norm_backward(p, a->dtype, (hipStream_t)stream), "smc_group_norm_backward");
 }
 
+// ---- windows -----------------------------------------------------------------------
+
+int check_windows(const smc_windows_t* w) {
+    if (!w) return bad(SMC_ERR_ARG, "windows is NULL");
+    if (w->n < 0 || w->n > kMaxRows) return bad(SMC_ERR_ARG, "n = %lld", (long long)w->n);
+    if (w->windows < 0 || w->windows > kMaxWindows)
+        return bad(SMC_ERR_ARG, "windows = %lld outside [0, 2^24]", (long long)w->windows);
+    if (!w->plan || !aligned16(w->plan) || w->plan_bytes < WindowLayout(w->n, w->windows).bytes)
+        return bad(SMC_ERR_ARG, "plan: %zu bytes at %p, %zu needed, 16-byte aligned", w->plan_bytes, w->plan,
+                   WindowLayout(w->n, w->windows).bytes);
+    const int64_t cells = (int64_t)w->ex + w->ey + w->ez;
+    if (w->ex < 0 || w->ey < 0 || w->ez < 0 || (cells > 0 && (w->ex < 1 || w->ey < 1 || w->ez < 1)))
+        return bad(SMC_ERR_ARG, "extent %d x %d x %d", w->ex, w->ey, w->ez);
+    if (cells > kMaxCells)
+        return bad(SMC_ERR_UNSUPPORTED, "extent %d + %d + %d cells, more than %d", w->ex, w->ey, w->ez, kMaxCells);
+    return SMC_OK;
+}
+
+int build_windows(smc_windows_t* w, hipStream_t s) {
+    CHECK(check_windows(w));
+    if (!w->offsets || odd(w->offsets, 4)) return bad(SMC_ERR_ARG, "offsets is NULL or misaligned");
+    if (odd(w->order, 4) || odd(w->coords, 4)) return bad(SMC_ERR_ARG, "order or coords is not aligned to its elements");
+    if (w->coords && w->coord_cols != 3 && w->coord_cols != 4)
+        return bad(SMC_ERR_ARG, "coord_cols = %d", w->coord_cols);
+    if (!w->coords && w->ex > 0 && w->n > 0) return bad(SMC_ERR_ARG, "an extent needs coords");
+    if (w->coords && w->ex < 1) return bad(SMC_ERR_ARG, "coords need an extent");
+    w->tiles64 = w->tiles128 = w->longest = 0;
+    WindowArgs p;
+    p.n = w->n;
+    p.windows = w->windows;
+    p.offsets = w->offsets;
+    p.order = w->order;
+    p.coords = w->coords;
+    p.cols = w->coord_cols;
+    p.extent[0] = w->ex;
+    p.extent[1] = w->ey;
+    p.extent[2] = w->ez;
+    p.plan = static_cast<char*>(w->plan);
+    CHECK(hip_status(launch_windows(p, s), "smc_windows_build"));
+    WindowHeader h;
+    CHECK(hip_status(hipMemcpyAsync(&h, w->plan, sizeof h, hipMemcpyDeviceToHost, s), "smc_windows_build"));
+    CHECK(hip_status(hipStreamSynchronize(s), "smc_windows_build"));
+    if (h.status & kStRange)
+        return bad(SMC_ERR_RANGE, "offsets that do not ascend within [0, n], a row of order outside it, or a window of "
+                                  "more cells than its extent");
+    if (h.status & kStDuplicate) return bad(SMC_ERR_DUPLICATE, "order has a row twice");
+    w->tiles64 = h.tiles[0];
+    w->tiles128 = h.tiles[1];
+    w->longest = h.longest;
+    return SMC_OK;
+}
+
+// ---- window attention ----------------------------------------------------------------
+
+constexpr int kMaxHeadDim = 128;
+
+int check_attention(const smc_attention_t* a, bool backward) {
+    if (!a) return bad(SMC_ERR_ARG, "args is NULL");
+    CHECK(check_windows(a->windows));
+    const int64_t n = a->windows->n;
+    if (n > 0 && a->windows->tiles64 < 1) return bad(SMC_ERR_STATE, "windows is not built");
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
+        return bad(SMC_ERR_ARG, "%d heads, %d of keys and values", a->heads, a->kv_heads);
+    if (a->head_dim < 1) return bad(SMC_ERR_ARG, "head_dim = %d", a->head_dim);
+    if (a->head_dim > kMaxHeadDim) return bad(SMC_ERR_UNSUPPORTED, "head_dim = %d, more than %d", a->head_dim, kMaxHeadDim);
+    const int64_t c = (int64_t)a->heads * a->head_dim, ckv = (int64_t)a->kv_heads * a->head_dim;
+    CHECK(check_common(n, c, "heads * head_dim", a->dtype));
+    if ((int64_t)a->windows->tiles64 * a->heads >= (int64_t)1 << 31)
+        return bad(SMC_ERR_UNSUPPORTED, "%d tiles of %d heads: 2^31 or more", a->windows->tiles64, a->heads);
+    if (!(a->scale > 0.f) || a->scale > 3.4e38f) return bad(SMC_ERR_ARG, "scale = %g", (double)a->scale);
+    CHECK(check_rows("q", a->q, n, c, a->ldq));
+    CHECK(check_rows("k", a->k, n, ckv, a->ldk));
+    CHECK(check_rows("v", a->v, n, ckv, a->ldv));
+    CHECK(check_rows("out", a->out, n, c, a->ld_out));
+    if (odd(a->lse, 4)) return bad(SMC_ERR_ARG, "lse is not aligned to its elements");
+    if (a->bias) {
+        if (odd(a->bias, 2)) return bad(SMC_ERR_ARG, "bias is not aligned to its elements");
+        if (a->windows->ex < 1) return bad(SMC_ERR_STATE, "a bias needs windows with cells");
+        if (a->reach < 1 || a->reach > kMaxReach) return bad(SMC_ERR_ARG, "reach = %d outside [1, %d]", a->reach, kMaxReach);
+    }
+    if (!backward) {
+        // other blocks read the inputs' rows again
+        if (share_memory(a->out, a->ld_out, 2, a->q, a->ldq, 2, n, c, c) ||
+            share_memory(a->out, a->ld_out, 2, a->k, a->ldk, 2, n, c, ckv) ||
+            share_memory(a->out, a->ld_out, 2, a->v, a->ldv, 2, n, c, ckv))
+            return bad(SMC_ERR_ARG, "out shares memory with q, k or v");
+        return SMC_OK;
+    }
+    return SMC_OK;
+}
+
+AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
+    AttentionArgs p;
+    const smc_windows_t* w = a->windows;
+    const WindowLayout at(w->n, w->windows);
+    p.n = w->n;
+    p.heads = a->heads;
+    p.kv_heads = a->kv_heads;
+    p.dim = a->head_dim;
+    p.scale = a->scale;
+    p.q = a->q;
+    p.ldq = a->ldq;
+    p.k = a->k;
+    p.ldk = a->ldk;
+    p.v = a->v;
+    p.ldv = a->ldv;
+    const char* plan = static_cast<const char*>(w->plan);
+    p.places = reinterpret_cast<const WindowPlace*>(plan + at.places);
+    p.tiles = reinterpret_cast<const WindowTile*>(plan + at.tiles[wide ? 1 : 0]);
+    p.n_tiles = wide ? w->tiles128 : w->tiles64;
+    p.extent[0] = w->ex;
+    p.extent[1] = w->ey;
+    p.extent[2] = w->ez;
+    p.table = a->bias;
+    p.reach = a->reach;
+    p.out = a->out;
+    p.ldo = a->ld_out;
+    p.lse = a->lse;
+    p.vec = a->head_dim % 8 == 0 && words16(a->q, a->ldq) && words16(a->k, a->ldk) && words16(a->v, a->ldv) &&
+            words16(a->out, a->ld_out);
+    return p;
+}
+
+int attention(const smc_attention_t* a, void* stream) {
+    CHECK(check_attention(a, false));
+    if (a->windows->n == 0) return SMC_OK;
+    const bool wide = a->windows->windows > 0 && a->windows->n / a->windows->windows >= 256;
+    const AttentionArgs p = attention_args(a, wide);
+    const hipStream_t s = (hipStream_t)stream;
+    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_f16(p, wide, s) : launch_attention_bf16(p, wide, s),
+                      "smc_window_attention");
+}
+
 }  // namespace
 
 extern "C" {
@@ -110,5 +243,13 @@ int smc_group_norm(const smc_group_norm_t* a, void* stream) { return group(a, fa
 int smc_group_norm_backward(const smc_group_norm_t* a, void* stream) { return group(a, true, stream); }
 size_t smc_group_norm_workspace(const smc_group_norm_t* a) { return group_workspace(a, false); }
 size_t smc_group_norm_backward_workspace(const smc_group_norm_t* a) { return group_workspace(a, true); }
+
+size_t smc_windows_bytes(int64_t n, int64_t windows) {
+    if (n < 0 || n > kMaxRows || windows < 0 || windows > kMaxWindows) return 0;
+    return WindowLayout(n, windows).bytes;
+}
+int smc_windows_build(smc_windows_t* w, void* stream) { return build_windows(w, (hipStream_t)stream); }
+
+int smc_window_attention(const smc_attention_t* a, void* stream) { return attention(a, stream); }
 
 }  // extern "C"
