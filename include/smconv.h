@@ -737,6 +737,17 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  * lse (or NULL): log sum_j exp(s_ij), float32 [heads, n] by place (not by row), -inf for
  * zeros' rows; the backward pass reads it. Scores, softmax and sums are float32; P is
  * rounded to dtype for its product with v. out may not overlap q, k or v.
+ *
+ * Backward, from the same inputs and what the forward call wrote to out and lse, for the
+ * gradient dout of out; P is computed again:
+ *   delta_i = dout_i . out_i,  dS = P (dout v^T - delta),  dq = scale dS k,
+ *   dk = scale dS^T q,  dv = P^T dout (sums over the heads that share them),
+ *   dbias[axis][b][h] = sum of dS over the pairs of the bucket, all windows and rows.
+ * P and dS are rounded to dtype as operands of products (f16: dS times a power of two found
+ * on the device, so that finite gradients that fit f16 come out finite). Gradients of rows
+ * of no window are zeros. dq, dk and dv may be columns of one buffer; they may not overlap
+ * an input or each other. workspace: smc_window_attention_backward_workspace(args) bytes,
+ * 16-byte aligned; the query reads windows, heads, kv_heads, dtype, bias and reach.
  */
 typedef struct smc_attention_s {
     const smc_windows_t* windows;   /* host structure, built */
@@ -754,9 +765,22 @@ typedef struct smc_attention_s {
     int64_t ldv;
     void* out;                /* [n, heads * head_dim] */
     int64_t ld_out;
-    float* lse;               /* [heads, n] or NULL */
+    float* lse;               /* [heads, n] or NULL; backward: read, as out */
+    const void* dout;         /* backward from here on: [n, heads * head_dim] */
+    int64_t ld_dout;
+    void* dq;                 /* [n, heads * head_dim] */
+    int64_t ld_dq;
+    void* dk;                 /* [n, kv_heads * head_dim] */
+    int64_t ld_dk;
+    void* dv;                 /* [n, kv_heads * head_dim] */
+    int64_t ld_dv;
+    void* dbias;              /* [3, 2 reach + 1, heads]; with bias */
+    void* workspace;
+    size_t workspace_bytes;
 } smc_attention_t;
 int smc_window_attention(const smc_attention_t* args, void* stream);
+int smc_window_attention_backward(const smc_attention_t* args, void* stream);
+size_t smc_window_attention_backward_workspace(const smc_attention_t* args);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,7 @@ __all__ = ["KernelMap", "PackedWeights", "pack_weights", "subm_conv3d", "lib", "
            "SmconvError", "ROUTES", "EXPORTED_SYMBOLS", "use_torch_allocator", "probe_mfma_bf16",
            "probe_copy", "rms_norm", "rms_norm_backward", "linear", "linear_backward", "gated",
            "gated_backward", "quantize_weight", "ACTIVATIONS", "group_norm", "group_norm_backward",
-           "Windows", "window_attention"]
+           "Windows", "window_attention", "window_attention_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsmconv.so")
@@ -49,7 +49,8 @@ EXPORTED_SYMBOLS = [
     "smc_linear_backward_workspace", "smc_gated_backward_workspace", "smc_weight_quantize",
     "smc_group_norm", "smc_group_norm_backward", "smc_group_norm_workspace",
     "smc_group_norm_backward_workspace", "smc_windows_bytes", "smc_windows_build",
-    "smc_window_attention",
+    "smc_window_attention", "smc_window_attention_backward",
+    "smc_window_attention_backward_workspace",
 ]
 STAGES = ["map", "neighbours", "mask_sort", "compact", "gemm", "centre"]
 
@@ -140,6 +141,10 @@ class AttentionArgs(ctypes.Structure):
         ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p),
         ("ldk", ctypes.c_int64), ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
         ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("lse", ctypes.c_void_p),
+        ("dout", ctypes.c_void_p), ("ld_dout", ctypes.c_int64), ("dq", ctypes.c_void_p),
+        ("ld_dq", ctypes.c_int64), ("dk", ctypes.c_void_p), ("ld_dk", ctypes.c_int64),
+        ("dv", ctypes.c_void_p), ("ld_dv", ctypes.c_int64), ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -205,14 +210,16 @@ def lib():
                        ("smc_linear", ProductArgs), ("smc_gated", ProductArgs),
                        ("smc_linear_backward", ProductArgs), ("smc_gated_backward", ProductArgs),
                        ("smc_group_norm", GroupNormArgs), ("smc_group_norm_backward", GroupNormArgs),
-                       ("smc_windows_build", WindowsArgs), ("smc_window_attention", AttentionArgs)):
+                       ("smc_windows_build", WindowsArgs), ("smc_window_attention", AttentionArgs),
+                       ("smc_window_attention_backward", AttentionArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
         getattr(L, name).restype = i32
     for name, args in (("smc_linear_workspace", ProductArgs), ("smc_gated_workspace", ProductArgs),
                        ("smc_linear_backward_workspace", ProductArgs),
                        ("smc_gated_backward_workspace", ProductArgs),
                        ("smc_group_norm_workspace", GroupNormArgs),
-                       ("smc_group_norm_backward_workspace", GroupNormArgs)):
+                       ("smc_group_norm_backward_workspace", GroupNormArgs),
+                       ("smc_window_attention_backward_workspace", AttentionArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_size_t
     L.smc_rms_norm_backward_workspace.argtypes = [i64, i32]
@@ -983,6 +990,41 @@ def window_attention(q, k, v, windows: Windows, heads: int, bias=None, scale=Non
         a.lse = kept.data_ptr()
     _check(lib().smc_window_attention(a, _raw_stream(q.device)))
     return (out, kept) if lse else out
+
+
+def window_attention_backward(dout, q, k, v, out, lse, windows: Windows, heads: int, bias=None,
+                              scale=None, grads=None, stream=None):
+    """Gradients of window_attention for the gradient dout of its output: (dq, dk,
+    dv, dbias), dbias None without a bias. out and lse: what window_attention returned for
+    the same inputs. grads: (dq, dk, dv) to write to, which may be columns of one buffer
+    (the gradient of a projection's output)."""
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return window_attention_backward(dout, q, k, v, out, lse, windows, heads, bias, scale, grads)
+    a = _attention_args(q, k, v, windows, heads, bias, scale)
+    dev, dt, n = q.device, q.dtype, q.shape[0]
+    a.dout, a.ld_dout = _rows(dout, "dout", dt, dev, q.shape)
+    a.out, a.ld_out = _rows(out, "out", dt, dev, q.shape)
+    _of(lse, "lse", torch.float32, dev)
+    if lse.shape != (heads, n) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous {[heads, n]}, got {list(lse.shape)}")
+    a.lse = lse.data_ptr()
+    dq, dk, dv = grads if grads is not None else (q.new_empty(t.shape) for t in (q, k, v))
+    a.dq, a.ld_dq = _rows(dq, "dq", dt, dev, q.shape)
+    a.dk, a.ld_dk = _rows(dk, "dk", dt, dev, k.shape)
+    a.dv, a.ld_dv = _rows(dv, "dv", dt, dev, v.shape)
+    dbias = None
+    if bias is not None:
+        dbias = torch.empty_like(bias)
+        a.dbias = dbias.data_ptr()
+    L = lib()
+    nbytes = L.smc_window_attention_backward_workspace(a)
+    ws = q.new_empty(nbytes, dtype=torch.uint8)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+    _check(L.smc_window_attention_backward(a, _raw_stream(dev)))
+    return dq, dk, dv, dbias
 
 
 def probe_mfma_bf16(iters: int, stream=None) -> float:

@@ -1,0 +1,10 @@
+// Gradients of window attention on f16 rows (a file a type: they compile in parallel).
+#include "attention_backward.h"
+
+namespace smc {
+
+hipError_t launch_attention_backward_f16(const AttentionArgs& a, bool wide, hipStream_t s) {
+    return attention_backward_of_type<kF16>(a, wide, s);
+}
+
+}  // namespace smc

@@ -112,5 +112,7 @@ struct AttentionArgs {
 // wide: tiles are of 128 queries, else of 64.
 hipError_t launch_attention_bf16(const AttentionArgs& a, bool wide, hipStream_t s);
 hipError_t launch_attention_f16(const AttentionArgs& a, bool wide, hipStream_t s);
+hipError_t launch_attention_backward_bf16(const AttentionArgs& a, bool wide, hipStream_t s);
+hipError_t launch_attention_backward_f16(const AttentionArgs& a, bool wide, hipStream_t s);
 
 }  // namespace smc

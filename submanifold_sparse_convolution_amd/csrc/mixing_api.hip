@@ -190,6 +190,29 @@ int check_attention(const smc_attention_t* a, bool backward) {
             return bad(SMC_ERR_ARG, "out shares memory with q, k or v");
         return SMC_OK;
     }
+    if (!a->lse && n > 0) return bad(SMC_ERR_ARG, "lse is NULL");
+    CHECK(check_rows("dout", a->dout, n, c, a->ld_dout));
+    CHECK(check_rows("dq", a->dq, n, c, a->ld_dq));
+    CHECK(check_rows("dk", a->dk, n, ckv, a->ld_dk));
+    CHECK(check_rows("dv", a->dv, n, ckv, a->ld_dv));
+    if (a->bias && (!a->dbias || odd(a->dbias, 2))) return bad(SMC_ERR_ARG, "dbias is NULL or misaligned");
+    struct Rows {
+        const char* name;
+        const void* p;
+        int64_t ld, cols;
+    };
+    const Rows in[] = {{"q", a->q, a->ldq, c}, {"k", a->k, a->ldk, ckv}, {"v", a->v, a->ldv, ckv},
+                       {"out", a->out, a->ld_out, c}, {"dout", a->dout, a->ld_dout, c}};
+    const Rows to[] = {{"dq", a->dq, a->ld_dq, c}, {"dk", a->dk, a->ld_dk, ckv}, {"dv", a->dv, a->ld_dv, ckv}};
+    auto shared = [n](const Rows& x, const Rows& y) {
+        return share_memory(x.p, x.ld, 2, y.p, y.ld, 2, n, x.cols, y.cols);
+    };
+    for (int i = 0; i < 3; ++i) {
+        for (const Rows& r : in)
+            if (shared(to[i], r)) return bad(SMC_ERR_ARG, "%s shares memory with %s", to[i].name, r.name);
+        for (int j = 0; j < i; ++j)
+            if (shared(to[i], to[j])) return bad(SMC_ERR_ARG, "%s shares memory with %s", to[i].name, to[j].name);
+    }
     return SMC_OK;
 }
 
@@ -212,6 +235,8 @@ AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
     p.places = reinterpret_cast<const WindowPlace*>(plan + at.places);
     p.tiles = reinterpret_cast<const WindowTile*>(plan + at.tiles[wide ? 1 : 0]);
     p.n_tiles = wide ? w->tiles128 : w->tiles64;
+    p.tiles64 = reinterpret_cast<const WindowTile*>(plan + at.tiles[0]);
+    p.n_tiles64 = w->tiles64;
     p.extent[0] = w->ex;
     p.extent[1] = w->ey;
     p.extent[2] = w->ez;
@@ -225,14 +250,68 @@ AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
     return p;
 }
 
+// Tiles of 128 queries (or keys) where windows are long.
+bool wide_tiles(const smc_attention_t* a) {
+    return a->windows->windows > 0 && a->windows->n / a->windows->windows >= 256;
+}
+
 int attention(const smc_attention_t* a, void* stream) {
     CHECK(check_attention(a, false));
     if (a->windows->n == 0) return SMC_OK;
-    const bool wide = a->windows->windows > 0 && a->windows->n / a->windows->windows >= 256;
+    const bool wide = wide_tiles(a);
     const AttentionArgs p = attention_args(a, wide);
     const hipStream_t s = (hipStream_t)stream;
     return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_f16(p, wide, s) : launch_attention_bf16(p, wide, s),
                       "smc_window_attention");
+}
+
+// Scratch of a backward pass: delta, the blocks' buckets, and f16's maxima.
+struct AttentionScratch {
+    size_t delta = 0, part = 0, range = 0, bytes = 0;       // offsets
+    explicit AttentionScratch(const smc_attention_t* a) {
+        const smc_windows_t* w = a->windows;
+        part = round_up((size_t)a->heads * w->n * 4);
+        const int64_t tiles = wide_tiles(a) ? w->tiles128 : w->tiles64;
+        range = part + (a->bias ? round_up((size_t)tiles * a->heads * 3 * (2 * a->reach + 1) * 4) : 0);
+        bytes = range + (a->dtype == SMC_DTYPE_F16 ? round_up((size_t)w->tiles64 * (a->heads + a->kv_heads) * 4) : 0);
+    }
+};
+
+size_t attention_workspace(const smc_attention_t* a) {
+    if (!a || !a->windows || a->windows->n < 0 || a->windows->n > kMaxRows || a->windows->windows < 0 || a->heads < 1 ||
+        a->heads > kMaxDim || a->kv_heads < 1 || a->kv_heads > a->heads || a->reach < 0 || a->reach > kMaxReach ||
+        a->windows->tiles64 < 0 || a->windows->tiles128 < 0)
+        return 0;
+    return AttentionScratch(a).bytes;
+}
+
+int attention_backward(const smc_attention_t* a, void* stream) {
+    CHECK(check_attention(a, true));
+    const AttentionScratch at(a);
+    if (a->windows->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < at.bytes))
+        return bad(SMC_ERR_ARG, "workspace: %zu bytes at %p, %zu needed, 16-byte aligned", a->workspace_bytes,
+                   a->workspace, at.bytes);
+    const bool wide = wide_tiles(a);
+    AttentionArgs p = attention_args(a, wide);
+    char* const ws = static_cast<char*>(a->workspace);
+    p.dout = a->dout;
+    p.ld_dout = a->ld_dout;
+    p.dq = a->dq;
+    p.ld_dq = a->ld_dq;
+    p.dk = a->dk;
+    p.ld_dk = a->ld_dk;
+    p.dv = a->dv;
+    p.ld_dv = a->ld_dv;
+    p.dtable = a->dbias;
+    p.delta = reinterpret_cast<float*>(ws);
+    p.part = reinterpret_cast<float*>(ws + at.part);
+    p.range = reinterpret_cast<float*>(ws + at.range);
+    p.vec = p.vec && words16(a->dout, a->ld_dout) && words16(a->dq, a->ld_dq) && words16(a->dk, a->ld_dk) &&
+            words16(a->dv, a->ld_dv);
+    const hipStream_t s = (hipStream_t)stream;
+    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_backward_f16(p, wide, s)
+                                                : launch_attention_backward_bf16(p, wide, s),
+                      "smc_window_attention_backward");
 }
 
 }  // namespace
@@ -251,5 +330,7 @@ size_t smc_windows_bytes(int64_t n, int64_t windows) {
 int smc_windows_build(smc_windows_t* w, void* stream) { return build_windows(w, (hipStream_t)stream); }
 
 int smc_window_attention(const smc_attention_t* a, void* stream) { return attention(a, stream); }
+int smc_window_attention_backward(const smc_attention_t* a, void* stream) { return attention_backward(a, stream); }
+size_t smc_window_attention_backward_workspace(const smc_attention_t* a) { return attention_workspace(a); }
 
 }  // extern "C"

@@ -97,3 +97,24 @@ def test_forward(name):
     assert torch.equal(got[none], wl[none])
     ro.check(torch.where(none, torch.zeros_like(got), got), torch.where(none, torch.zeros_like(wl), wl), el, "lse")
     assert torch.equal(smc.window_attention(q, k, v, c.windows, c.heads, bias=table), out)
+
+
+def backward(c, q, k, v, table, dout=None):
+    """The kernels' gradients, from the formula's out and lse (rounded)."""
+    want, _, lse, _ = mx.attention(*c.formula())
+    dout = c.dout if dout is None else dout
+    return smc.window_attention_backward(dout.cuda(), q, k, v, want.to(c.dt).cuda(), lse.float().cuda(), c.windows, c.heads,
+                                         bias=table)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_backward(name):
+    c = Case(**CASES[name])
+    q, k, v, table = c.device()
+    got = backward(c, q, k, v, table)
+    want = mx.attention_backward(c.dout.double(), *c.formula())
+    for t, (w, bound), label in zip(got, want, ("dq", "dk", "dv", "dbias")):
+        ro.check(t, w, bound, label)
+    assert (got[3] is None) == (table is None)
+    again = backward(c, q, k, v, table)
+    assert all(torch.equal(a, b) for a, b in zip(got, again) if a is not None)
