@@ -703,7 +703,8 @@ size_t smc_group_norm_backward_workspace(const smc_group_norm_t* args);
  * places of no window may be left before the first and after the last. order holds every
  * row once. coords (or NULL: no bias then): each row's voxel coordinates, as smc_map_build
  * takes them; (ex, ey, ez) is how many cells a window spans along x, y and z at most (its
- * rows' coordinates less their lowest are within [0, ex) and so on), ex + ey + ez <= 128.
+ * rows' coordinates less their lowest are within [0, ex) and so on); ex, ey and ez, each
+ * rounded up to a multiple of 4, may add up to 128.
  * The call waits for the device once and returns SMC_ERR_RANGE or SMC_ERR_DUPLICATE where
  * any of this does not hold; the plan may not be used then. It keeps no pointer but
  * plan's: offsets, order and coords may go, and a copy of the structure is as good as it.
@@ -719,7 +720,7 @@ typedef struct smc_windows_s {
     int32_t ex, ey, ez;       /* cells of a window, 0 without coords */
     void* plan;               /* device memory of smc_windows_bytes(n, windows) bytes, 16-byte aligned */
     size_t plan_bytes;
-    int32_t tiles64, tiles128, longest;     /* written by smc_windows_build */
+    int32_t tiles32, tiles64, tiles128, longest;    /* written by smc_windows_build */
 } smc_windows_t;
 size_t smc_windows_bytes(int64_t n, int64_t windows);
 int smc_windows_build(smc_windows_t* windows, void* stream);

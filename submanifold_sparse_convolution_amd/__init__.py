@@ -128,8 +128,8 @@ class WindowsArgs(ctypes.Structure):
         ("n", ctypes.c_int64), ("windows", ctypes.c_int64), ("offsets", ctypes.c_void_p),
         ("order", ctypes.c_void_p), ("coords", ctypes.c_void_p), ("coord_cols", ctypes.c_int32),
         ("ex", ctypes.c_int32), ("ey", ctypes.c_int32), ("ez", ctypes.c_int32),
-        ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("tiles64", ctypes.c_int32),
-        ("tiles128", ctypes.c_int32), ("longest", ctypes.c_int32),
+        ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("tiles32", ctypes.c_int32),
+        ("tiles64", ctypes.c_int32), ("tiles128", ctypes.c_int32), ("longest", ctypes.c_int32),
     ]
 
 
@@ -898,8 +898,8 @@ class Windows:
     they lie); window w is the places offsets[w] .. offsets[w + 1] - 1 of it (int32
     [windows + 1] CUDA tensor); places of no window may be left at both ends. For a
     relative position bias: coords, the rows' int32 [N, 4] (b, x, y, z) or [N, 3]
-    coordinates, and extent, how many cells a window spans along x, y and z at most (128
-    in all). SmconvError where a row is listed twice, an offset or row is out of range or
+    coordinates, and extent, how many cells a window spans along x, y and z at most (each
+    rounded up to a multiple of 4, 128 in all). SmconvError where a row is listed twice, an offset or row is out of range or
     a window is larger than that."""
 
     def __init__(self, offsets, n: int, order=None, coords=None, extent=None, stream=None):

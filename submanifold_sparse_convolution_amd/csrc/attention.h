@@ -11,7 +11,7 @@
 //
 // Bias. bias_ij = sum over the axes of T[clamp(x_i - x_j, -R, R)] is a product too: B_i, the
 // table seen from cell x_i (one entry for each cell x of the window's extent), times E_j, one-hot
-// at x_j; the axes' cells lie side by side in the contraction. Table entries are exact in
+// at x_j; the axes' cells lie side by side in the contraction, each axis at a multiple of 4. Table entries are exact in
 // the rows' type, so the sum is float32's. The gradient of B is dS E, by the same tiles.
 // (Looking entries up costs three LDS reads and nine vector operations a score, more than
 // the rest of the softmax.) Infinities would make 0 x inf: they count as the type's
@@ -24,7 +24,6 @@
 namespace smc {
 namespace {
 
-constexpr int kAttentionThreads = 256;
 constexpr int kKeys = 64;               // rows of a tile in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -52,12 +51,18 @@ __device__ __forceinline__ u32x4 tile_columns(const char* tile, int piece, int r
     return (u32x4){v[0].x, v[0].y, v[1].x, v[1].y};
 }
 
-// Elements i .. i + 7 of a row, zeros from `left` on.
-__device__ __forceinline__ u32x4 row_word(const void* base, int64_t i, int left, int vec) {
-    if (left <= 0) return (u32x4){0u, 0u, 0u, 0u};
+// Elements i .. i + 7 of a row, zeros from `left` on (ALIGNED: all of them or none, and no
+// branch that a load would be waited for at).
+template <bool ALIGNED>
+__device__ __forceinline__ u32x4 row_word(const void* base, int64_t i, int left) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + i;
-    if (vec) return *reinterpret_cast<const u32x4*>(p);
-    return left >= W ? load_unaligned(p) : load_tail(p, left);
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (ALIGNED) {
+        if (left > 0) w = *reinterpret_cast<const u32x4*>(p);
+    } else if (left > 0) {
+        w = left >= W ? load_unaligned(p) : load_tail(p, left);
+    }
+    return w;
 }
 
 // One-hot row: word `word` of a row with a one at each of the three cells.
@@ -75,39 +80,54 @@ __device__ __forceinline__ u32x4 one_hot(uint32_t cells, int word) {
     return (u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-// A head's table by distance: [axis][128 + distance], distances clamped to the reach.
-constexpr int kDistances = 256;
-template <int DT>
+// A head's table by distance, 2 `up` entries for an axis of `up` elements (see Cells): entry m is
+// T[up - m], or T[m - up] where MIRROR, clamped to the reach. The entries lie twice, the second
+// time one further, so that two neighbouring ones are an aligned word whatever the first.
+template <int EXT>
+constexpr int kTableEntries = 2 * EXT + 2;      // of one copy
+template <int DT, int EXT, int THREADS, bool MIRROR>
 __device__ __forceinline__ void load_table(const AttentionArgs& a, int head, uint16_t* s_table) {
     const uint16_t* t = static_cast<const uint16_t*>(a.table);
-    for (int i = threadIdx.x; i < 3 * kDistances; i += kAttentionThreads) {
-        const int axis = i / kDistances, d = min(max(i % kDistances - 128, -a.reach), a.reach);
+    const Cells cells(a.extent);
+#pragma unroll
+    for (int k = 0; k < (2 * EXT + THREADS - 1) / THREADS; ++k) {
+        const int i = k * THREADS + threadIdx.x, axis = cells.axis_of_entry(i);
+        if (i >= 2 * cells.all()) continue;
+        const int away = cells.pick(cells.up, axis) - (i - 2 * cells.pick(cells.first, axis));
+        const int d = min(max(MIRROR ? -away : away, -a.reach), a.reach);
         uint16_t v = t[(int64_t)(axis * (2 * a.reach + 1) + a.reach + d) * a.heads + head];
         const uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
         if ((v & 0x7fff) == inf) v -= 1;
         s_table[i] = v;
+        s_table[kTableEntries<EXT> + i + 1] = v;
     }
 }
 
-// Word of B: contraction elements i .. i + 7 of the table seen from `cells`. SIGN +1: entries
-// T[own cell - cell], -1: T[cell - own cell].
-template <int SIGN>
-__device__ __forceinline__ u32x4 table_word(const AttentionArgs& a, const uint16_t* s_table, uint32_t cells, int i) {
-    u32x4 w;
-    const int y0 = a.extent[0], z0 = y0 + a.extent[1], end = z0 + a.extent[2];
+// The table seen from the cells `own`: elements 32 c + 8 q .. + 7 of the contraction, each chunk c.
+// Element e of axis d is entry 2 first + up - own + e; four elements lie on one axis.
+template <int EXT>
+__device__ __forceinline__ void table_words(const AttentionArgs& a, const uint16_t* s_table, uint32_t own, int q,
+                                            u32x4 (&w)[EXT ? EXT / 32 : 1]) {
+    const Cells cells(a.extent);
+    int at[3];                  // bytes from the table's start to element 0
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        uint32_t v = 0;
+    for (int d = 0; d < 3; ++d) {
+        const int m = 2 * cells.first[d] + cells.up[d] - (int)((own >> (8 * d)) & 255u);
+        at[d] = 2 * m + ((m & 1) ? 2 * kTableEntries<EXT> + 2 : 0);
+    }
+    const char* table = reinterpret_cast<const char*>(s_table);
+#pragma unroll
+    for (int c = 0; c < EXT / 32; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int c = i + 2 * d + h, axis = (c >= y0) + (c >= z0);
-            const int away = SIGN * ((int)((cells >> (8 * axis)) & 255u) - c);
-            const uint32_t e = c < end ? s_table[axis * kDistances + 128 + away] : 0;
-            v |= e << (16 * h);
+            const int e = 32 * c + 8 * q + 4 * h;
+            const bool in = e < cells.all();
+            const int from = (e < cells.first[1] ? at[0] : e < cells.first[2] ? at[1] : at[2]) + 2 * e;
+            const uint32_t lo = *reinterpret_cast<const uint32_t*>(table + (in ? from : 0));
+            const uint32_t hi = *reinterpret_cast<const uint32_t*>(table + (in ? from + 4 : 0));
+            w[c][2 * h] = in ? lo : 0u;
+            w[c][2 * h + 1] = in ? hi : 0u;
         }
-        w[d] = v;
-    }
-    return w;
 }
 
 // The block's tile and head: consecutive ones lie on one XCD, whose L2 then holds the other
@@ -136,11 +156,13 @@ __device__ __forceinline__ float quad_sum(float v) {
     return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
+__device__ __forceinline__ bool any_lane(bool v) { return __ballot(v) != 0; }
+
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // acc[d][e]: column 16 d + 4 q + e of the lane's row, times f, into the row at `to` of `dim` elements.
-template <int DT, int DP>
-__device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, void* to, int64_t i, int dim, int lane, int vec) {
+template <int DT, int DP, bool ALIGNED>
+__device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, void* to, int64_t i, int dim, int lane) {
     const int q = lane >> 4;
 #pragma unroll
     for (int d = 0; d < DP / 16; d += 2) {
@@ -152,7 +174,7 @@ __device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, 
         const int c = 16 * (d + (q & 1)) + 8 * (q >> 1), left = dim - c;
         if (left <= 0 || i < 0) continue;
         uint16_t* p = static_cast<uint16_t*>(to) + i + c;
-        if (vec) {
+        if (ALIGNED) {
             *reinterpret_cast<u32x4*>(p) = u;
         } else if (left >= W) {
             store_unaligned(p, u);
@@ -166,47 +188,104 @@ __device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, 
 
 // Rows of a tile on their way from memory to LDS: 16-byte words, kLoads a thread, of the
 // rows s_places[0 .. 63] (row < 0: zeros).
-template <int RW>
+template <int RW, int THREADS, bool ALIGNED>
 struct RowLoads {
-    static constexpr int kLoads = kKeys * RW / kAttentionThreads;
+    static constexpr int kLoads = kKeys * RW / THREADS;
     u32x4 w[kLoads];
-    __device__ __forceinline__ void load(const void* base, int64_t ld, int column, int dim, const WindowPlace* s_places, int vec) {
+    __device__ __forceinline__ void load(const void* base, int64_t ld, int column, int dim, const WindowPlace* s_places) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int id = i * kAttentionThreads + threadIdx.x, r = id / RW, word = id % RW;
+            const int id = i * THREADS + threadIdx.x, r = id / RW, word = id % RW;
             const int row = s_places[r].row;
-            w[i] = row_word(base, (int64_t)row * ld + column + word * W, row < 0 ? 0 : dim - word * W, vec);
+            w[i] = row_word<ALIGNED>(base, (int64_t)row * ld + column + word * W, row < 0 ? 0 : dim - word * W);
         }
     }
     __device__ __forceinline__ void commit(char* tile) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int id = i * kAttentionThreads + threadIdx.x;
+            const int id = i * THREADS + threadIdx.x;
             *reinterpret_cast<u32x4*>(tile + tile_word<RW>(id / RW, id % RW)) = w[i];
         }
     }
 };
 
 // The one-hot rows of a tile (row < 0: zeros).
-template <int DT, int RW>
+template <int DT, int RW, int THREADS>
 __device__ __forceinline__ void commit_cells(char* tile, const WindowPlace* s_places) {
 #pragma unroll
-    for (int i = 0; i < kKeys * RW / kAttentionThreads; ++i) {
-        const int id = i * kAttentionThreads + threadIdx.x, r = id / RW, word = id % RW;
+    for (int i = 0; i < kKeys * RW / THREADS; ++i) {
+        const int id = i * THREADS + threadIdx.x, r = id / RW, word = id % RW;
         const WindowPlace p = s_places[r];
         const u32x4 none = {0u, 0u, 0u, 0u};
         *reinterpret_cast<u32x4*>(tile + tile_word<RW>(r, word)) = p.row < 0 ? none : one_hot<DT>(p.cells, word);
     }
 }
 
-// WindowPlace `at` of a tile's window, no row beyond its end.
+// Waves and columns a wave of a block. Short windows: 32 queries by one wave (a block's latency is
+// what they cost, and smaller blocks leave fewer waves without queries); long ones: 128, so that
+// what is read from LDS serves two columns.
+template <int WAVES_, int COLUMNS_>
+struct Block {
+    static constexpr int kWaves = WAVES_, kColumns = COLUMNS_, kThreads = 64 * WAVES_;
+    static constexpr int kRows = 16 * WAVES_ * COLUMNS_;        // queries (or keys)
+    static constexpr bool kSkips = WAVES_ <= 2;                 // 16 keys past a window's end are left out
+};
+template <int DP>
+using BlockShort = Block<DP <= 64 ? 1 : 2, DP <= 64 ? 2 : 1>;
+typedef Block<4, 1> BlockMid;
+typedef Block<4, 2> BlockLong;
+
+// Place `at` of a tile's window, no row beyond its end.
 __device__ __forceinline__ WindowPlace place_at(const AttentionArgs& a, int at, int end) {
     return at < end ? a.places[at] : WindowPlace{-1, 0u};
 }
 
-// Row and cells of a lane's own query or key.
+// Two tiles of a window's rows (keys and values, or queries and dout) and their one-hot cells, 64 rows
+// a step: a step's rows are loaded while the one before is worked on, and go to LDS after it, with two
+// buffers without waiting for the other waves' reads of it.
+template <int DT, int DP, int EXT, bool A, class B, int NB>
+struct Walk {
+    static constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, TH = B::kThreads;
+    struct Memory {
+        char x[NB][kKeys * DP * 2], y[NB][kKeys * DP * 2], e[NB][EXT ? kKeys * EXT * 2 : 16];
+        WindowPlace places[2][kKeys];
+    };
+    RowLoads<RW, TH, A> lx, ly;
+    WindowPlace next;
+    // The first step's loads. (Every thread calls these.)
+    __device__ __forceinline__ void start(const AttentionArgs& a, Memory& m, const WindowTile& t, const void* x, int64_t ldx,
+                                          const void* y, int64_t ldy, int column) {
+        const int i = threadIdx.x & (kKeys - 1);
+        if (threadIdx.x < kKeys) m.places[0][i] = place_at(a, t.begin + i, t.end);
+        if (TH == kKeys || (threadIdx.x >= kKeys && threadIdx.x < 2 * kKeys)) m.places[1][i] = place_at(a, t.begin + kKeys + i, t.end);
+        next = place_at(a, t.begin + 2 * kKeys + i, t.end);
+        __syncthreads();
+        load(a, m, 0, x, ldx, y, ldy, column);
+    }
+    __device__ __forceinline__ void load(const AttentionArgs& a, const Memory& m, int step, const void* x, int64_t ldx,
+                                         const void* y, int64_t ldy, int column) {
+        lx.load(x, ldx, column, a.dim, m.places[step & 1]);
+        ly.load(y, ldy, column, a.dim, m.places[step & 1]);
+    }
+    // The loaded step to LDS; `step` is its number.
+    __device__ __forceinline__ void commit(const AttentionArgs& a, Memory& m, int step, const WindowTile& t) {
+        const int buf = NB == 2 ? step & 1 : 0;
+        if (NB == 1) __syncthreads();
+        lx.commit(m.x[buf]);
+        ly.commit(m.y[buf]);
+        if (EXT) commit_cells<DT, RE, TH>(m.e[buf], m.places[step & 1]);
+        if (step > 0) {
+            const int i = threadIdx.x & (kKeys - 1);
+            if (threadIdx.x < kKeys) m.places[(step + 1) & 1][i] = next;        // of the step before
+            next = place_at(a, t.begin + (step + 2) * kKeys + i, t.end);
+        }
+        __syncthreads();
+    }
+};
+
+// Row and cells of a lane's own query or key (the lowest cells where there is none).
 __device__ __forceinline__ WindowPlace own_place(const AttentionArgs& a, const WindowTile& t, int i) {
-    return i < t.count ? a.places[t.first + i] : WindowPlace{-1, 0u};
+    return i < t.count ? a.places[t.first + i] : WindowPlace{-1, Cells(a.extent).lowest()};
 }
 
 }  // namespace

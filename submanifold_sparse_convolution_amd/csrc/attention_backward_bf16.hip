@@ -3,8 +3,8 @@
 
 namespace smc {
 
-hipError_t launch_attention_backward_bf16(const AttentionArgs& a, bool wide, hipStream_t s) {
-    return attention_backward_of_type<kBF16>(a, wide, s);
+hipError_t launch_attention_backward_bf16(const AttentionArgs& a, int lengths, hipStream_t s) {
+    return attention_backward_of_type<kBF16>(a, lengths, s);
 }
 
 }  // namespace smc

@@ -3,6 +3,6 @@
 
 namespace smc {
 
-hipError_t launch_attention_f16(const AttentionArgs& a, bool wide, hipStream_t s) { return attention_of_type<kF16>(a, wide, s); }
+hipError_t launch_attention_f16(const AttentionArgs& a, int lengths, hipStream_t s) { return attention_of_type<kF16>(a, lengths, s); }
 
 }  // namespace smc

@@ -40,11 +40,28 @@ hipError_t launch_group_norm(const GroupArgs& a, int dt, hipStream_t s);
 hipError_t launch_group_norm_backward(const GroupArgs& a, int dt, hipStream_t s);
 
 // ---- windows (window_kernels.hip) ----
-// A place is a position in the window order. Header, places, tiles of 64 and of 128
+// A place is a position in the window order. Header, places and tiles of 32, 64 and 128
 // places lie behind each other in the plan.
 struct WindowPlace {
     int row;            // row of the tensors
-    uint32_t cells;     // x, ex + y, ex + ey + z of the row's cell in its window, 8 bits each
+    uint32_t cells;     // of the row in its window, x, y and z as elements of Cells, 8 bits each
+};
+// The axes' cells side by side, each axis at a multiple of 4.
+struct Cells {
+    int up[3], first[3];        // elements of an axis, the first of them
+    __host__ __device__ explicit Cells(const int (&extent)[3]) {
+        int at = 0;
+        for (int d = 0; d < 3; ++d) {
+            up[d] = (extent[d] + 3) & ~3;
+            first[d] = at;
+            at += up[d];
+        }
+    }
+    __host__ __device__ int all() const { return first[2] + up[2]; }
+    // twice as many entries by distance (see load_table)
+    __host__ __device__ int axis_of_entry(int i) const { return (i >= 2 * first[1]) + (i >= 2 * first[2]); }
+    __host__ __device__ static int pick(const int (&v)[3], int axis) { return axis == 0 ? v[0] : axis == 1 ? v[1] : v[2]; }
+    __host__ __device__ uint32_t lowest() const { return (uint32_t)first[1] << 8 | (uint32_t)first[2] << 16; }
 };
 struct WindowTile {
     int first, count;   // places
@@ -52,20 +69,23 @@ struct WindowTile {
 };
 struct WindowHeader {
     uint32_t status;    // kSt* bits
-    int tiles[2];       // of 64 and of 128 places
+    int tiles[3];       // of 32, 64 and 128 places
     int longest;        // rows of the longest window
 };
-constexpr int kMaxCells = 128;                  // ex + ey + ez
+constexpr int kMaxCells = 128;                  // elements of Cells
 constexpr int kMaxReach = 127;                  // cells lie no further apart
 constexpr int64_t kMaxWindows = 1 << 24;
 struct WindowLayout {
-    size_t places, tiles[2], seen, bytes;       // offsets; seen: a bit a row, scratch of the build
+    size_t places, tiles[3], seen, bytes;       // offsets; seen: a bit a row, scratch of the build
     WindowLayout(int64_t n, int64_t windows) {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
         places = 256;
-        tiles[0] = places + up((size_t)n * sizeof(WindowPlace));
-        tiles[1] = tiles[0] + up((size_t)(n / 64 + windows + 2) * sizeof(WindowTile));
-        seen = tiles[1] + up((size_t)(n / 128 + windows + 2) * sizeof(WindowTile));
+        size_t at = places + up((size_t)n * sizeof(WindowPlace));
+        for (int k = 0; k < 3; ++k) {
+            tiles[k] = at;
+            at += up((size_t)(n / (32 << k) + windows + 2) * sizeof(WindowTile));
+        }
+        seen = at;
         bytes = seen + up((size_t)(n + 31) / 32 * 4);
     }
 };
@@ -109,10 +129,11 @@ struct AttentionArgs {
     int n_tiles64 = 0;
     int vec = 0;                    // every row is made of aligned 16-byte words
 };
-// wide: tiles are of 128 queries, else of 64.
-hipError_t launch_attention_bf16(const AttentionArgs& a, bool wide, hipStream_t s);
-hipError_t launch_attention_f16(const AttentionArgs& a, bool wide, hipStream_t s);
-hipError_t launch_attention_backward_bf16(const AttentionArgs& a, bool wide, hipStream_t s);
-hipError_t launch_attention_backward_f16(const AttentionArgs& a, bool wide, hipStream_t s);
+// By the windows' mean length, which a launch's blocks fit; the tiles are of 32, 64 and 128 places.
+enum : int { kShortWindows = 0, kMidWindows = 1, kLongWindows = 2 };
+hipError_t launch_attention_bf16(const AttentionArgs& a, int lengths, hipStream_t s);
+hipError_t launch_attention_f16(const AttentionArgs& a, int lengths, hipStream_t s);
+hipError_t launch_attention_backward_bf16(const AttentionArgs& a, int lengths, hipStream_t s);
+hipError_t launch_attention_backward_f16(const AttentionArgs& a, int lengths, hipStream_t s);
 
 }  // namespace smc

@@ -112,11 +112,12 @@ int check_windows(const smc_windows_t* w) {
     if (!w->plan || !aligned16(w->plan) || w->plan_bytes < WindowLayout(w->n, w->windows).bytes)
         return bad(SMC_ERR_ARG, "plan: %zu bytes at %p, %zu needed, 16-byte aligned", w->plan_bytes, w->plan,
                    WindowLayout(w->n, w->windows).bytes);
-    const int64_t cells = (int64_t)w->ex + w->ey + w->ez;
-    if (w->ex < 0 || w->ey < 0 || w->ez < 0 || (cells > 0 && (w->ex < 1 || w->ey < 1 || w->ez < 1)))
+    if (w->ex < 0 || w->ey < 0 || w->ez < 0 || ((w->ex | w->ey | w->ez) && (w->ex < 1 || w->ey < 1 || w->ez < 1)))
         return bad(SMC_ERR_ARG, "extent %d x %d x %d", w->ex, w->ey, w->ez);
-    if (cells > kMaxCells)
-        return bad(SMC_ERR_UNSUPPORTED, "extent %d + %d + %d cells, more than %d", w->ex, w->ey, w->ez, kMaxCells);
+    const int extent[3] = {w->ex, w->ey, w->ez};
+    if (w->ex > kMaxCells || w->ey > kMaxCells || w->ez > kMaxCells || Cells(extent).all() > kMaxCells)
+        return bad(SMC_ERR_UNSUPPORTED, "extent %d, %d, %d: more than %d cells in all, each rounded up to a multiple of 4",
+                   w->ex, w->ey, w->ez, kMaxCells);
     return SMC_OK;
 }
 
@@ -128,7 +129,7 @@ int build_windows(smc_windows_t* w, hipStream_t s) {
         return bad(SMC_ERR_ARG, "coord_cols = %d", w->coord_cols);
     if (!w->coords && w->ex > 0 && w->n > 0) return bad(SMC_ERR_ARG, "an extent needs coords");
     if (w->coords && w->ex < 1) return bad(SMC_ERR_ARG, "coords need an extent");
-    w->tiles64 = w->tiles128 = w->longest = 0;
+    w->tiles32 = w->tiles64 = w->tiles128 = w->longest = 0;
     WindowArgs p;
     p.n = w->n;
     p.windows = w->windows;
@@ -148,8 +149,9 @@ int build_windows(smc_windows_t* w, hipStream_t s) {
         return bad(SMC_ERR_RANGE, "offsets that do not ascend within [0, n], a row of order outside it, or a window of "
                                   "more cells than its extent");
     if (h.status & kStDuplicate) return bad(SMC_ERR_DUPLICATE, "order has a row twice");
-    w->tiles64 = h.tiles[0];
-    w->tiles128 = h.tiles[1];
+    w->tiles32 = h.tiles[0];
+    w->tiles64 = h.tiles[1];
+    w->tiles128 = h.tiles[2];
     w->longest = h.longest;
     return SMC_OK;
 }
@@ -169,8 +171,8 @@ int check_attention(const smc_attention_t* a, bool backward) {
     if (a->head_dim > kMaxHeadDim) return bad(SMC_ERR_UNSUPPORTED, "head_dim = %d, more than %d", a->head_dim, kMaxHeadDim);
     const int64_t c = (int64_t)a->heads * a->head_dim, ckv = (int64_t)a->kv_heads * a->head_dim;
     CHECK(check_common(n, c, "heads * head_dim", a->dtype));
-    if ((int64_t)a->windows->tiles64 * a->heads >= (int64_t)1 << 31)
-        return bad(SMC_ERR_UNSUPPORTED, "%d tiles of %d heads: 2^31 or more", a->windows->tiles64, a->heads);
+    if ((int64_t)a->windows->tiles32 * a->heads >= (int64_t)1 << 31)
+        return bad(SMC_ERR_UNSUPPORTED, "%d tiles of %d heads: 2^31 or more", a->windows->tiles32, a->heads);
     if (!(a->scale > 0.f) || a->scale > 3.4e38f) return bad(SMC_ERR_ARG, "scale = %g", (double)a->scale);
     CHECK(check_rows("q", a->q, n, c, a->ldq));
     CHECK(check_rows("k", a->k, n, ckv, a->ldk));
@@ -216,7 +218,24 @@ int check_attention(const smc_attention_t* a, bool backward) {
     return SMC_OK;
 }
 
-AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
+bool attention_words(const smc_attention_t* a, bool backward) {
+    return a->head_dim % 8 == 0 && words16(a->q, a->ldq) && words16(a->k, a->ldk) && words16(a->v, a->ldv) &&
+           words16(a->out, a->ld_out) &&
+           (!backward || (words16(a->dout, a->ld_dout) && words16(a->dq, a->ld_dq) && words16(a->dk, a->ld_dk) &&
+                          words16(a->dv, a->ld_dv)));
+}
+
+int window_lengths(const smc_attention_t* a, bool backward) {
+    if (!attention_words(a, backward)) return kMidWindows;
+    const int64_t mean = a->windows->windows > 0 ? a->windows->n / a->windows->windows : 0;
+    return mean < 40 ? kShortWindows : mean < 160 ? kMidWindows : kLongWindows;
+}
+
+int tiles_of(const smc_windows_t* w, int lengths) {
+    return lengths == kShortWindows ? w->tiles32 : lengths == kMidWindows ? w->tiles64 : w->tiles128;
+}
+
+AttentionArgs attention_args(const smc_attention_t* a, int lengths, bool backward) {
     AttentionArgs p;
     const smc_windows_t* w = a->windows;
     const WindowLayout at(w->n, w->windows);
@@ -233,9 +252,9 @@ AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
     p.ldv = a->ldv;
     const char* plan = static_cast<const char*>(w->plan);
     p.places = reinterpret_cast<const WindowPlace*>(plan + at.places);
-    p.tiles = reinterpret_cast<const WindowTile*>(plan + at.tiles[wide ? 1 : 0]);
-    p.n_tiles = wide ? w->tiles128 : w->tiles64;
-    p.tiles64 = reinterpret_cast<const WindowTile*>(plan + at.tiles[0]);
+    p.tiles = reinterpret_cast<const WindowTile*>(plan + at.tiles[lengths]);
+    p.n_tiles = tiles_of(w, lengths);
+    p.tiles64 = reinterpret_cast<const WindowTile*>(plan + at.tiles[1]);
     p.n_tiles64 = w->tiles64;
     p.extent[0] = w->ex;
     p.extent[1] = w->ey;
@@ -245,23 +264,17 @@ AttentionArgs attention_args(const smc_attention_t* a, bool wide) {
     p.out = a->out;
     p.ldo = a->ld_out;
     p.lse = a->lse;
-    p.vec = a->head_dim % 8 == 0 && words16(a->q, a->ldq) && words16(a->k, a->ldk) && words16(a->v, a->ldv) &&
-            words16(a->out, a->ld_out);
+    p.vec = attention_words(a, backward);
     return p;
-}
-
-// Tiles of 128 queries (or keys) where windows are long.
-bool wide_tiles(const smc_attention_t* a) {
-    return a->windows->windows > 0 && a->windows->n / a->windows->windows >= 256;
 }
 
 int attention(const smc_attention_t* a, void* stream) {
     CHECK(check_attention(a, false));
     if (a->windows->n == 0) return SMC_OK;
-    const bool wide = wide_tiles(a);
-    const AttentionArgs p = attention_args(a, wide);
+    const int lengths = window_lengths(a, false);
+    const AttentionArgs p = attention_args(a, lengths, false);
     const hipStream_t s = (hipStream_t)stream;
-    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_f16(p, wide, s) : launch_attention_bf16(p, wide, s),
+    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_f16(p, lengths, s) : launch_attention_bf16(p, lengths, s),
                       "smc_window_attention");
 }
 
@@ -271,7 +284,7 @@ struct AttentionScratch {
     explicit AttentionScratch(const smc_attention_t* a) {
         const smc_windows_t* w = a->windows;
         part = round_up((size_t)a->heads * w->n * 4);
-        const int64_t tiles = wide_tiles(a) ? w->tiles128 : w->tiles64;
+        const int64_t tiles = tiles_of(w, window_lengths(a, true));
         range = part + (a->bias ? round_up((size_t)tiles * a->heads * 3 * (2 * a->reach + 1) * 4) : 0);
         bytes = range + (a->dtype == SMC_DTYPE_F16 ? round_up((size_t)w->tiles64 * (a->heads + a->kv_heads) * 4) : 0);
     }
@@ -280,7 +293,7 @@ struct AttentionScratch {
 size_t attention_workspace(const smc_attention_t* a) {
     if (!a || !a->windows || a->windows->n < 0 || a->windows->n > kMaxRows || a->windows->windows < 0 || a->heads < 1 ||
         a->heads > kMaxDim || a->kv_heads < 1 || a->kv_heads > a->heads || a->reach < 0 || a->reach > kMaxReach ||
-        a->windows->tiles64 < 0 || a->windows->tiles128 < 0)
+        a->windows->tiles32 < 0 || a->windows->tiles64 < 0 || a->windows->tiles128 < 0)
         return 0;
     return AttentionScratch(a).bytes;
 }
@@ -291,8 +304,8 @@ int attention_backward(const smc_attention_t* a, void* stream) {
     if (a->windows->n > 0 && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < at.bytes))
         return bad(SMC_ERR_ARG, "workspace: %zu bytes at %p, %zu needed, 16-byte aligned", a->workspace_bytes,
                    a->workspace, at.bytes);
-    const bool wide = wide_tiles(a);
-    AttentionArgs p = attention_args(a, wide);
+    const int lengths = window_lengths(a, true);
+    AttentionArgs p = attention_args(a, lengths, true);
     char* const ws = static_cast<char*>(a->workspace);
     p.dout = a->dout;
     p.ld_dout = a->ld_dout;
@@ -306,11 +319,9 @@ int attention_backward(const smc_attention_t* a, void* stream) {
     p.delta = reinterpret_cast<float*>(ws);
     p.part = reinterpret_cast<float*>(ws + at.part);
     p.range = reinterpret_cast<float*>(ws + at.range);
-    p.vec = p.vec && words16(a->dout, a->ld_dout) && words16(a->dq, a->ld_dq) && words16(a->dk, a->ld_dk) &&
-            words16(a->dv, a->ld_dv);
     const hipStream_t s = (hipStream_t)stream;
-    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_backward_f16(p, wide, s)
-                                                : launch_attention_backward_bf16(p, wide, s),
+    return hip_status(a->dtype == SMC_DTYPE_F16 ? launch_attention_backward_f16(p, lengths, s)
+                                                : launch_attention_backward_bf16(p, lengths, s),
                       "smc_window_attention_backward");
 }
 

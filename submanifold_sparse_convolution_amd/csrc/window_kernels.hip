@@ -1,5 +1,5 @@
 // The index of windows that attention walks: for every place of the window order
-// its row and cell, and the tiles of 64 and of 128 places, none of which has rows of
+// its row and cell, and the tiles of 32, 64 and 128 places, none of which has rows of
 // two windows (so nothing of one window, not a NaN either, reaches another).
 // Made once for all layers on the same windows.
 #include <algorithm>
@@ -27,7 +27,7 @@ __device__ __forceinline__ int window_end(const WindowArgs& a, int64_t w) {
 __global__ __launch_bounds__(256) void k_windows_clear(WindowArgs a, uint32_t* seen, int64_t words) {
     const int64_t i = block_number() * 256 + threadIdx.x;
     if (i < words) seen[i] = 0;
-    if (i == 0) *header_of(a) = WindowHeader{0, {0, 0}, 0};
+    if (i == 0) *header_of(a) = WindowHeader{0, {0, 0, 0}, 0};
 }
 
 // Rows of the places: within [0, n), none twice.
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void k_windows_rows(WindowArgs a, WindowPlace*
     } else if (atomicOr(seen + (row >> 5), 1u << (row & 31)) >> (row & 31) & 1u) {
         status = kStDuplicate;
     }
-    places[i] = WindowPlace{row, 0u};
+    places[i] = WindowPlace{row, Cells(a.extent).lowest()};
     if (status) atomicOr(&header_of(a)->status, status);
 }
 
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void k_windows_cells(WindowArgs a, WindowPlace
         uint32_t status = 0;
         for (int i = begin + threadIdx.x; i < end; i += 256) {
             uint32_t cells = 0;
-            int before = 0;
+            const Cells at(a.extent);
 #pragma unroll
             for (int d = 0; d < 3; ++d) {
                 const int lowest = min(min(s_low[d][0], s_low[d][1]), min(s_low[d][2], s_low[d][3]));
@@ -75,8 +75,7 @@ __global__ __launch_bounds__(256) void k_windows_cells(WindowArgs a, WindowPlace
                     status = kStRange;
                     cell = 0;
                 }
-                cells |= (cell + before) << (8 * d);
-                before += a.extent[d];
+                cells |= (cell + at.first[d]) << (8 * d);
             }
             places[i].cells = cells;
         }
@@ -86,12 +85,13 @@ __global__ __launch_bounds__(256) void k_windows_cells(WindowArgs a, WindowPlace
 
 // The tiles, window by window, by one block: counts of 1,024 windows at a time
 // and their running sum. Offsets out of order are told by the way.
-__global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile* tiles64, WindowTile* tiles128) {
-    __shared__ int s_sum[2][1024];
+__global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile* tiles32, WindowTile* tiles64,
+                                                        WindowTile* tiles128) {
+    __shared__ int s_sum[3][1024];
     __shared__ int s_longest, s_bad;
     if (threadIdx.x == 0) s_longest = s_bad = 0;
     __syncthreads();
-    int done[2] = {0, 0};
+    int done[3] = {0, 0, 0};
     for (int64_t w0 = -1; w0 <= a.windows; w0 += 1024) {
         const int64_t w = w0 + threadIdx.x;
         int begin = 0, end = 0;
@@ -104,29 +104,29 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
                 if (w < a.windows) atomicMax(&s_longest, end - begin);
             }
         }
-        int count[2];
+        int count[3];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int size = 64 << k;
+        for (int k = 0; k < 3; ++k) {
+            const int size = 32 << k;
             count[k] = (int)(((int64_t)end - begin + size - 1) / size);
             s_sum[k][threadIdx.x] = count[k];
         }
         __syncthreads();
         for (int o = 1; o < 1024; o <<= 1) {
-            int before[2] = {0, 0};
+            int before[3] = {0, 0, 0};
             if (threadIdx.x >= o)
-                for (int k = 0; k < 2; ++k) before[k] = s_sum[k][threadIdx.x - o];
+                for (int k = 0; k < 3; ++k) before[k] = s_sum[k][threadIdx.x - o];
             __syncthreads();
-            for (int k = 0; k < 2; ++k) s_sum[k][threadIdx.x] += before[k];
+            for (int k = 0; k < 3; ++k) s_sum[k][threadIdx.x] += before[k];
             __syncthreads();
         }
         const bool inside = w >= 0 && w < a.windows;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int size = 64 << k;
+        for (int k = 0; k < 3; ++k) {
+            const int size = 32 << k;
             // offsets out of order could make more tiles than there is room for
             const int64_t most = a.n / size + a.windows + 2;
-            WindowTile* to = k ? tiles128 : tiles64;
+            WindowTile* to = k == 0 ? tiles32 : k == 1 ? tiles64 : tiles128;
             int64_t at = (int64_t)done[k] + s_sum[k][threadIdx.x] - count[k];
             for (int i = 0; i < count[k] && at + i < most; ++i) {
                 const int first = begin + i * size;
@@ -138,8 +138,7 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
     }
     if (threadIdx.x == 0) {
         WindowHeader* h = header_of(a);
-        h->tiles[0] = done[0];
-        h->tiles[1] = done[1];
+        for (int k = 0; k < 3; ++k) h->tiles[k] = done[k];
         h->longest = s_longest;
         if (s_bad) atomicOr(&h->status, (uint32_t)kStRange);
     }
@@ -156,8 +155,9 @@ hipError_t launch_windows(const WindowArgs& a, hipStream_t s) {
     if (a.n > 0) launch(k_windows_rows, grid_of((a.n + 255) / 256), dim3(256), 0, s, a, places, seen);
     if (a.n > 0 && a.coords && a.windows > 0)
         launch(k_windows_cells, dim3((unsigned)std::min<int64_t>(a.windows, 1 << 16)), dim3(256), 0, s, a, places);
-    launch(k_windows_tiles, dim3(1), dim3(1024), 0, s, a, reinterpret_cast<WindowTile*>(a.plan + at.tiles[0]),
-           reinterpret_cast<WindowTile*>(a.plan + at.tiles[1]));
+    WindowTile* tiles[3];
+    for (int k = 0; k < 3; ++k) tiles[k] = reinterpret_cast<WindowTile*>(a.plan + at.tiles[k]);
+    launch(k_windows_tiles, dim3(1), dim3(1024), 0, s, a, tiles[0], tiles[1], tiles[2]);
     return hipGetLastError();
 }
 
