@@ -720,7 +720,8 @@ typedef struct smc_windows_s {
     int32_t ex, ey, ez;       /* cells of a window, 0 without coords */
     void* plan;               /* device memory of smc_windows_bytes(n, windows) bytes, 16-byte aligned */
     size_t plan_bytes;
-    int32_t tiles32, tiles64, tiles128, longest;    /* written by smc_windows_build */
+    int32_t tiles32, tiles64, tiles128, longest;    /* from here on written by smc_windows_build */
+    int64_t pairs;            /* sum of the squares of the windows' rows */
 } smc_windows_t;
 size_t smc_windows_bytes(int64_t n, int64_t windows);
 int smc_windows_build(smc_windows_t* windows, void* stream);

@@ -130,6 +130,7 @@ class WindowsArgs(ctypes.Structure):
         ("ex", ctypes.c_int32), ("ey", ctypes.c_int32), ("ez", ctypes.c_int32),
         ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("tiles32", ctypes.c_int32),
         ("tiles64", ctypes.c_int32), ("tiles128", ctypes.c_int32), ("longest", ctypes.c_int32),
+        ("pairs", ctypes.c_int64),
     ]
 
 

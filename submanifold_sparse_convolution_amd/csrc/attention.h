@@ -18,38 +18,53 @@
 // largest values, whose exponentials are the same.
 #pragma once
 
+#include <algorithm>
+
 #include "mixing.h"
 #include "row_words.h"
 
 namespace smc {
 namespace {
 
+// for loads and stores through pointers that are picked by a condition, which the compiler else takes for
+// pointers to any memory
+#define SMC_GLOBAL __attribute__((address_space(1)))
+
 constexpr int kKeys = 64;               // rows of a tile in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// A tile: rows of RW 16-byte words, permuted so that 8 rows read along, and 4 rows read by a
-// transposing read (32 bytes each), lie in different banks.
+// A tile: rows of RW 16-byte words, 32-byte pieces of a row permuted by its number so that what is read at
+// a time lies in different banks of the 64 (256 bytes): by 16-byte reads, lanes 0 .. 3, 12 .. 15 of one word
+// and 4 .. 11 of the next (or the other way round), each lane a row; by transposing reads, 8 rows' pieces.
 template <int RW>
 __device__ __forceinline__ int tile_word(int row, int word) {
-    const int f = RW == 4 ? (row & 2) | ((row >> 2) & 1) : ((row & 3) << 1) | ((row >> 2) & 1);
-    return (row * RW + (word ^ f)) * 16;
+    const int f = RW == 16 ? row & 7 : RW == 8 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return (row * RW + (word ^ (2 * f))) * 16;
 }
+// A lane's places in a tile, which do not depend on the step: word 4 c + lane / 16 of the row lane % 16 (rows
+// 16 b + that are a constant further), and its 8 bytes of a transposing read of the columns 16 piece ..
+// + 15 of the rows 4 (lane / 16) .. + 3.
 template <int RW>
-__device__ __forceinline__ u32x4 tile_row(const char* tile, int row, int word) {
-    return *reinterpret_cast<const u32x4*>(tile + tile_word<RW>(row, word));
-}
-// Columns 16 piece + lane % 16 of the rows r0 .. r0 + 3 and r1 .. r1 + 3 (the lane's own).
-template <int RW>
-__device__ __forceinline__ u32x4 tile_columns(const char* tile, int piece, int r0, int r1, int lane) {
-    const int s = lane & 15;
-    u32x2 v[2];
+struct TileLane {
+    int row[(RW + 3) / 4], column[RW / 2];
+    __device__ __forceinline__ explicit TileLane(int lane) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const char* p = tile + tile_word<RW>((t ? r1 : r0) + (s >> 2), 2 * piece + ((s >> 1) & 1)) + (s & 1) * 8;
-        v[t] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SMC_LDS s16x4*)(p)));
+        for (int c = 0; c < RW / 4; ++c) row[c] = tile_word<RW>(lane & 15, 4 * c + (lane >> 4));
+#pragma unroll
+        for (int d = 0; d < RW / 2; ++d)
+            column[d] = tile_word<RW>(4 * (lane >> 4) + ((lane & 15) >> 2), 2 * d + ((lane >> 1) & 1)) + (lane & 1) * 8;
     }
-    return (u32x4){v[0].x, v[0].y, v[1].x, v[1].y};
-}
+    __device__ __forceinline__ u32x4 along(const char* tile, int row16, int c) const {
+        return *reinterpret_cast<const u32x4*>(tile + row[c] + row16 * (RW * 16));
+    }
+    // (rows r .. of the lanes' first four, and 16 further)
+    __device__ __forceinline__ u32x4 across(const char* tile, int piece, int r) const {
+        const char* p = tile + column[piece] + r * (RW * 16);
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SMC_LDS s16x4*)(p)));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SMC_LDS s16x4*)(p + 16 * RW * 16)));
+        return (u32x4){lo.x, lo.y, hi.x, hi.y};
+    }
+};
 
 // Elements i .. i + 7 of a row, zeros from `left` on (ALIGNED: all of them or none, and no
 // branch that a load would be waited for at).
@@ -58,7 +73,7 @@ __device__ __forceinline__ u32x4 row_word(const void* base, int64_t i, int left)
     const uint16_t* p = static_cast<const uint16_t*>(base) + i;
     u32x4 w = {0u, 0u, 0u, 0u};
     if (ALIGNED) {
-        if (left > 0) w = *reinterpret_cast<const u32x4*>(p);
+        if (left > 0) w = *(const SMC_GLOBAL u32x4*)(p);
     } else if (left > 0) {
         w = left >= W ? load_unaligned(p) : load_tail(p, left);
     }
@@ -86,21 +101,45 @@ __device__ __forceinline__ u32x4 one_hot(uint32_t cells, int word) {
 template <int EXT>
 constexpr int kTableEntries = 2 * EXT + 2;      // of one copy
 template <int DT, int EXT, int THREADS, bool MIRROR>
-__device__ __forceinline__ void load_table(const AttentionArgs& a, int head, uint16_t* s_table) {
-    const uint16_t* t = static_cast<const uint16_t*>(a.table);
-    const Cells cells(a.extent);
+struct TableLoads {
+    static constexpr int kLoads = EXT ? (2 * EXT + THREADS - 1) / THREADS : 1;
+    uint16_t v[kLoads];
+    __device__ __forceinline__ void load(const AttentionArgs& a, int head) {
+        const uint16_t* t = static_cast<const uint16_t*>(a.table);
+        const Cells cells(a.extent);
 #pragma unroll
-    for (int k = 0; k < (2 * EXT + THREADS - 1) / THREADS; ++k) {
-        const int i = k * THREADS + threadIdx.x, axis = cells.axis_of_entry(i);
-        if (i >= 2 * cells.all()) continue;
-        const int away = cells.pick(cells.up, axis) - (i - 2 * cells.pick(cells.first, axis));
-        const int d = min(max(MIRROR ? -away : away, -a.reach), a.reach);
-        uint16_t v = t[(int64_t)(axis * (2 * a.reach + 1) + a.reach + d) * a.heads + head];
-        const uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
-        if ((v & 0x7fff) == inf) v -= 1;
-        s_table[i] = v;
-        s_table[kTableEntries<EXT> + i + 1] = v;
+        for (int k = 0; k < kLoads; ++k) {
+            const int i = k * THREADS + threadIdx.x, axis = cells.axis_of_entry(i);
+            const int away = cells.pick(cells.up, axis) - (i - 2 * cells.pick(cells.first, axis));
+            const int d = min(max(MIRROR ? -away : away, -a.reach), a.reach);
+            v[k] = 0;
+            if (i < 2 * cells.all()) v[k] = t[(int64_t)(axis * (2 * a.reach + 1) + a.reach + d) * a.heads + head];
+        }
     }
+    __device__ __forceinline__ void commit(const AttentionArgs& a, uint16_t* s_table) const {
+        const uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int i = k * THREADS + threadIdx.x;
+            if (i >= 2 * EXT) continue;
+            const uint16_t e = (v[k] & 0x7fff) == inf ? v[k] - 1 : v[k];
+            s_table[i] = e;
+            s_table[kTableEntries<EXT> + i + 1] = e;
+        }
+    }
+};
+
+// The tables of up to HEADS heads, every load before the first is waited for.
+template <int DT, int EXT, int THREADS, int HEADS>
+__device__ __forceinline__ void load_tables(const AttentionArgs& a, int head, int heads,
+                                            uint16_t (&s_table)[HEADS][EXT ? 2 * kTableEntries<EXT> : 2]) {
+    TableLoads<DT, EXT, THREADS, false> t[HEADS];
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h)
+        if (h < heads) t[h].load(a, head + h);
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h)
+        if (h < heads) t[h].commit(a, s_table[h]);
 }
 
 // The table seen from the cells `own`: elements 32 c + 8 q .. + 7 of the contraction, each chunk c.
@@ -130,17 +169,27 @@ __device__ __forceinline__ void table_words(const AttentionArgs& a, const uint16
         }
 }
 
-// The block's tile and head: consecutive ones lie on one XCD, whose L2 then holds the other
-// heads' columns of the rows that are read (blocks go round the 8 XCDs in turn).
-__device__ __forceinline__ bool tile_and_head(int n_tiles, int heads, int& tile, int& head) {
-    const uint32_t b = (uint32_t)block_number(), total = (uint32_t)n_tiles * (uint32_t)heads, each = (total + 7) / 8;
-    const uint32_t i = (b & 7) * each + (b >> 3);
-    if ((b >> 3) >= each || i >= total) return false;
-    tile = (int)(i / (uint32_t)heads);
-    head = (int)(i % (uint32_t)heads);
+// The block's tile and heads, `each` of them from `head` on: consecutive blocks lie on one XCD, whose L2
+// then holds the other heads' columns of the rows that are read (blocks go round the 8 XCDs in turn).
+__device__ __forceinline__ bool tile_and_head(int n_tiles, int heads, int each, int& tile, int& head) {
+    const uint32_t groups = (uint32_t)(heads + each - 1) / (uint32_t)each;
+    const uint32_t b = (uint32_t)block_number(), total = (uint32_t)n_tiles * groups, an_xcd = (total + 7) / 8;
+    const uint32_t i = (b & 7) * an_xcd + (b >> 3);
+    if ((b >> 3) >= an_xcd || i >= total) return false;
+    tile = (int)(i / groups);
+    head = (int)(i % groups) * each;
     return true;
 }
-inline dim3 attention_grid(int64_t n_tiles, int heads) { return grid_of((n_tiles * heads + 7) / 8 * 8); }
+inline dim3 attention_grid(int64_t n_tiles, int heads, int each) {
+    return grid_of((n_tiles * ((heads + each - 1) / each) + 7) / 8 * 8);
+}
+
+// Heads a block: two where one would make more than 16 blocks a CU. Forward / backward in us, one, two and
+// four: 91,000 rows, 14,208 blocks 53.6, 47.3, 50.1 / 200.8, 187.6, 200.0; 40,000 in windows of 24, 6,668
+// 20.3, 17.2, 17.0 / 85.1, 80.4, 81.7; of 60, 2,668 13.7, 15.2, 15.2 / 47.2, 51.2, 48.9.
+inline int heads_a_block(int64_t n_tiles, int heads, int most) {
+    return n_tiles * heads >= 16 * device_cus() ? std::min(heads, most) : 1;
+}
 
 // v over the four lanes of a query.
 __device__ __forceinline__ float quad_max(float v) {
@@ -175,7 +224,7 @@ __device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, 
         if (left <= 0 || i < 0) continue;
         uint16_t* p = static_cast<uint16_t*>(to) + i + c;
         if (ALIGNED) {
-            *reinterpret_cast<u32x4*>(p) = u;
+            *(SMC_GLOBAL u32x4*)(p) = u;
         } else if (left >= W) {
             store_unaligned(p, u);
         } else {
@@ -186,58 +235,27 @@ __device__ __forceinline__ void store_row(const f32x4 (&acc)[DP / 16], float f, 
     }
 }
 
-// Rows of a tile on their way from memory to LDS: 16-byte words, kLoads a thread, of the
-// rows s_places[0 .. 63] (row < 0: zeros).
-template <int RW, int THREADS, bool ALIGNED>
-struct RowLoads {
-    static constexpr int kLoads = kKeys * RW / THREADS;
-    u32x4 w[kLoads];
-    __device__ __forceinline__ void load(const void* base, int64_t ld, int column, int dim, const WindowPlace* s_places) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int id = i * THREADS + threadIdx.x, r = id / RW, word = id % RW;
-            const int row = s_places[r].row;
-            w[i] = row_word<ALIGNED>(base, (int64_t)row * ld + column + word * W, row < 0 ? 0 : dim - word * W);
-        }
-    }
-    __device__ __forceinline__ void commit(char* tile) const {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int id = i * THREADS + threadIdx.x;
-            *reinterpret_cast<u32x4*>(tile + tile_word<RW>(id / RW, id % RW)) = w[i];
-        }
-    }
-};
-
-// The one-hot rows of a tile (row < 0: zeros).
-template <int DT, int RW, int THREADS>
-__device__ __forceinline__ void commit_cells(char* tile, const WindowPlace* s_places) {
-#pragma unroll
-    for (int i = 0; i < kKeys * RW / THREADS; ++i) {
-        const int id = i * THREADS + threadIdx.x, r = id / RW, word = id % RW;
-        const WindowPlace p = s_places[r];
-        const u32x4 none = {0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4*>(tile + tile_word<RW>(r, word)) = p.row < 0 ? none : one_hot<DT>(p.cells, word);
-    }
-}
-
-// Waves and columns a wave of a block. Short windows: 32 queries by one wave (a block's latency is
-// what they cost, and smaller blocks leave fewer waves without queries); long ones: 128, so that
-// what is read from LDS serves two columns.
-template <int WAVES_, int COLUMNS_>
+// Waves, columns a wave and heads a block. Short windows: 32 queries and several heads, so that what
+// does not depend on the head (places, cells, addresses), half of the work, is done once, and the
+// next head's rows are on their way while one is worked on; long ones: 128 queries, so that what is
+// read from LDS serves two columns.
+template <int WAVES_, int COLUMNS_, int HEADS_>
 struct Block {
     static constexpr int kWaves = WAVES_, kColumns = COLUMNS_, kThreads = 64 * WAVES_;
     static constexpr int kRows = 16 * WAVES_ * COLUMNS_;        // queries (or keys)
+    static constexpr int kHeads = HEADS_;                       // at most
     static constexpr bool kSkips = WAVES_ <= 2;                 // 16 keys past a window's end are left out
+    static constexpr bool kHalves = COLUMNS_ == 1;              // 32 keys at a time, none past a window's end
 };
-template <int DP>
-using BlockShort = Block<DP <= 64 ? 1 : 2, DP <= 64 ? 2 : 1>;
-typedef Block<4, 1> BlockMid;
-typedef Block<4, 2> BlockLong;
+typedef Block<2, 1, 2> BlockShort;
+typedef Block<4, 1, 2> BlockMid;
+typedef Block<4, 2, 1> BlockLong;
 
-// Place `at` of a tile's window, no row beyond its end.
+// Place `at` of a tile's window, no row beyond its end (and cells that are none).
 __device__ __forceinline__ WindowPlace place_at(const AttentionArgs& a, int at, int end) {
-    return at < end ? a.places[at] : WindowPlace{-1, 0u};
+    WindowPlace p = {-1, 0xffffffffu};
+    if (at < end) p = a.places[at];
+    return p;
 }
 
 // Two tiles of a window's rows (keys and values, or queries and dout) and their one-hot cells, 64 rows
@@ -246,39 +264,74 @@ __device__ __forceinline__ WindowPlace place_at(const AttentionArgs& a, int at, 
 template <int DT, int DP, int EXT, bool A, class B, int NB>
 struct Walk {
     static constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, TH = B::kThreads;
+    static constexpr int kWords = kKeys * RW / TH, kCells = EXT ? kKeys * RE / TH : 1;      // a thread's
     struct Memory {
         char x[NB][kKeys * DP * 2], y[NB][kKeys * DP * 2], e[NB][EXT ? kKeys * EXT * 2 : 16];
-        WindowPlace places[2][kKeys];
     };
-    RowLoads<RW, TH, A> lx, ly;
-    WindowPlace next;
-    // The first step's loads. (Every thread calls these.)
-    __device__ __forceinline__ void start(const AttentionArgs& a, Memory& m, const WindowTile& t, const void* x, int64_t ldx,
-                                          const void* y, int64_t ldy, int column) {
-        const int i = threadIdx.x & (kKeys - 1);
-        if (threadIdx.x < kKeys) m.places[0][i] = place_at(a, t.begin + i, t.end);
-        if (TH == kKeys || (threadIdx.x >= kKeys && threadIdx.x < 2 * kKeys)) m.places[1][i] = place_at(a, t.begin + kKeys + i, t.end);
-        next = place_at(a, t.begin + 2 * kKeys + i, t.end);
-        __syncthreads();
-        load(a, m, 0, x, ldx, y, ldy, column);
+    u32x4 wx[kWords], wy[kWords];
+    const char *px, *py;        // this thread's word of row 0, of the head whose rows are loaded
+    int rows[kWords];           // of the step to load
+    uint32_t cells[kCells], held[kCells];       // of that step, and of the step loaded
+    bool whole;                 // the step to load has 64 rows, of DP elements
+
+    __device__ static int word() { return (int)threadIdx.x % RW * W; }
+    __device__ __forceinline__ void point(const void* x, const void* y, int column) {
+        px = static_cast<const char*>(x) + 2 * (int64_t)(column + word());
+        py = static_cast<const char*>(y) + 2 * (int64_t)(column + word());
     }
-    __device__ __forceinline__ void load(const AttentionArgs& a, const Memory& m, int step, const void* x, int64_t ldx,
-                                         const void* y, int64_t ldy, int column) {
-        lx.load(x, ldx, column, a.dim, m.places[step & 1]);
-        ly.load(y, ldy, column, a.dim, m.places[step & 1]);
-    }
-    // The loaded step to LDS; `step` is its number.
-    __device__ __forceinline__ void commit(const AttentionArgs& a, Memory& m, int step, const WindowTile& t) {
-        const int buf = NB == 2 ? step & 1 : 0;
-        if (NB == 1) __syncthreads();
-        lx.commit(m.x[buf]);
-        ly.commit(m.y[buf]);
-        if (EXT) commit_cells<DT, RE, TH>(m.e[buf], m.places[step & 1]);
-        if (step > 0) {
-            const int i = threadIdx.x & (kKeys - 1);
-            if (threadIdx.x < kKeys) m.places[(step + 1) & 1][i] = next;        // of the step before
-            next = place_at(a, t.begin + (step + 2) * kKeys + i, t.end);
+    __device__ __forceinline__ void places(const AttentionArgs& a, const WindowTile& t, int step) {
+        const int first = t.begin + step * kKeys;
+        whole = A && first + kKeys <= t.end && a.dim == DP;
+        if (whole) {
+            const SMC_GLOBAL WindowPlace* p = (const SMC_GLOBAL WindowPlace*)a.places + first;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) rows[i] = p[(i * TH + (int)threadIdx.x) / RW].row;
+            if (EXT)
+#pragma unroll
+                for (int i = 0; i < kCells; ++i) cells[i] = p[(i * TH + (int)threadIdx.x) / RE].cells;
+            return;
         }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) rows[i] = place_at(a, first + (i * TH + (int)threadIdx.x) / RW, t.end).row;
+        if (EXT)
+#pragma unroll
+            for (int i = 0; i < kCells; ++i) cells[i] = place_at(a, first + (i * TH + (int)threadIdx.x) / RE, t.end).cells;
+    }
+    __device__ __forceinline__ void load(const AttentionArgs& a, int64_t ldx, int64_t ldy) {
+        const uint32_t bx = (uint32_t)ldx * 2, by = (uint32_t)ldy * 2;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                wx[i] = *(const SMC_GLOBAL u32x4*)(px + (uint64_t)(uint32_t)rows[i] * bx);
+                wy[i] = *(const SMC_GLOBAL u32x4*)(py + (uint64_t)(uint32_t)rows[i] * by);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int left = rows[i] < 0 ? 0 : a.dim - word();
+                wx[i] = row_word<A>(px + (uint64_t)(uint32_t)rows[i] * bx, 0, left);
+                wy[i] = row_word<A>(py + (uint64_t)(uint32_t)rows[i] * by, 0, left);
+            }
+        }
+        if (EXT)
+#pragma unroll
+            for (int i = 0; i < kCells; ++i) held[i] = cells[i];
+    }
+    // The loaded step to LDS.
+    __device__ __forceinline__ void commit(Memory& m, int buf, bool with_cells) {
+        if (NB == 1) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const int id = i * TH + threadIdx.x, at = tile_word<RW>(id / RW, id % RW);
+            *reinterpret_cast<u32x4*>(m.x[buf] + at) = wx[i];
+            *reinterpret_cast<u32x4*>(m.y[buf] + at) = wy[i];
+        }
+        if (EXT && with_cells)
+#pragma unroll
+            for (int i = 0; i < kCells; ++i) {
+                const int id = i * TH + threadIdx.x;
+                *reinterpret_cast<u32x4*>(m.e[buf] + tile_word<RE>(id / RE, id % RE)) = one_hot<DT>(held[i], id % RE);
+            }
         __syncthreads();
     }
 };

@@ -58,17 +58,10 @@ __global__ __launch_bounds__(256) void k_attention_range(AttentionArgs a) {
 template <int THREADS>
 __device__ __forceinline__ float gradient_scale(const AttentionArgs& a, const WindowTile& t, int head, int kv) {
     __shared__ uint32_t s_most[2][THREADS / 64];
-    // the window's tiles of 64 lie behind each other; find its first by its place
-    int lo = 0, hi = a.n_tiles64 - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.tiles64[mid].first < t.begin) lo = mid + 1;
-        else hi = mid;
-    }
     const int count = (t.end - t.begin + 63) / 64, all = a.heads + a.kv_heads;
     uint32_t most[2] = {0u, 0u};
     for (int i = threadIdx.x; i < count; i += THREADS) {
-        const uint32_t* r = reinterpret_cast<const uint32_t*>(a.range) + (int64_t)(lo + i) * all;
+        const uint32_t* r = reinterpret_cast<const uint32_t*>(a.range) + (int64_t)(t.first64 + i) * all;
         most[0] = max(most[0], r[head]);
         most[1] = max(most[1], r[a.heads + kv]);
     }
@@ -93,69 +86,77 @@ __device__ __forceinline__ float gradient_scale(const AttentionArgs& a, const Wi
 __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads) void k_attention_queries(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_queries(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16, ET16 = EXT / 16;
     constexpr int NQ = B::kColumns, TH = B::kThreads, kBins = EXT ? EXT / 32 : 1;
     constexpr bool kOwnDelta = B::kRows <= 64;          // (see the top)
     typedef Walk<DT, DP, EXT, A, B, 1> Keys;
     __shared__ __align__(16) typename Keys::Memory s_keys;
-    __shared__ __align__(16) uint16_t s_table[EXT ? 2 * kTableEntries<EXT> : 2];
+    __shared__ __align__(16) uint16_t s_table[B::kHeads][EXT ? 2 * kTableEntries<EXT> : 2];
     // dB of 16 queries a wave (rows 4 floats longer than their cells), then the waves' sums by distance
     __shared__ __align__(16) float s_db[EXT ? B::kWaves * 16 * (EXT + 4) : 1];
     int tile, head;
-    if (!tile_and_head(a.n_tiles, a.heads, tile, head)) return;
+    if (!tile_and_head(a.n_tiles, a.heads, a.heads_each, tile, head)) return;
     const WindowTile t = a.tiles[tile];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-    const int kv = head / (a.heads / a.kv_heads);
-    if (EXT) load_table<DT, EXT, TH, false>(a, head, s_table);
-    const float grow = DT == kF16 ? gradient_scale<TH>(a, t, head, kv) : 1.f;
-    const float shrink = 1.f / grow;                    // (a power of two)
+    const int share = a.heads / a.kv_heads, first_head = head, heads = min(a.heads_each, a.heads - head);
+    const int length = t.end - t.begin;
+    const bool active = wave * NQ * 16 < t.count, one = length <= kKeys;    // one step a head
     const float to_log2 = EXT ? kLog2e : a.scale * kLog2e;
-    const bool one = t.end - t.begin <= kKeys;
-    // a window of one row: P is 1 whatever q, k and the bias are
-    const float keep = t.end - t.begin == 1 ? 0.f : grow;
-    float bins[kBins];                                  // sums of dS by distance, 64 of them a word: a lane each
-#pragma unroll
-    for (int i = 0; i < kBins; ++i) bins[i] = 0.f;
-
-    const bool active = wave * NQ * 16 < t.count;
+    const TileLane<RW> at(lane);
+    const TileLane<RE> at_cells(lane);
     WindowPlace own[NQ];
-    float base[NQ], delta[NQ];
-    u32x4 fq[NQ][CK], fo[NQ][CK], fb[NQ][CE ? CE : 1];
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        const int i = (wave * NQ + u) * 16 + col;
-        own[u] = own_place(a, t, i);
-        base[u] = own[u].row < 0 ? INFINITY : lse_base(a.lse[(int64_t)head * a.n + t.first + i]);
-        delta[u] = 0.f;
-#pragma unroll
-        for (int c = 0; c < CK; ++c) {
-            const int at = head * a.dim + 32 * c + 8 * q, left = own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q;
-            fq[u][c] = row_word<A>(a.q, (int64_t)own[u].row * a.ldq + at, left);
-            fo[u][c] = row_word<A>(a.dout, (int64_t)own[u].row * a.ld_dout + at, left);
-            if (kOwnDelta && one) continue;
-            const u32x4 out = row_word<A>(a.out, (int64_t)own[u].row * a.ldo + at, left);
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                delta[u] += to_f32<DT>(out[d] & 0xffffu) * to_f32<DT>(fo[u][c][d] & 0xffffu) +
-                            to_f32<DT>(out[d] >> 16) * to_f32<DT>(fo[u][c][d] >> 16);
-        }
-    }
+    for (int u = 0; u < NQ; ++u) own[u] = own_place(a, t, (wave * NQ + u) * 16 + col);
     Keys keys;
-    keys.start(a, s_keys, t, a.k, a.ldk, a.v, a.ldv, kv * a.dim);
-    if (EXT)
+    keys.places(a, t, 0);
+    if (EXT) load_tables<DT, EXT, TH, B::kHeads>(a, head, heads, s_table);
+    u32x4 fq[NQ][CK], fo[NQ][CK], fb[NQ][CE ? CE : 1];
+    float base[NQ], delta[NQ], grow = 1.f, keep = 1.f;
+    auto load_queries = [&](int h, u32x4 (&f)[NQ][CK], u32x4 (&g)[NQ][CK], float (&lse)[NQ]) SMC_INLINE {
 #pragma unroll
-        for (int u = 0; u < NQ; ++u)
-                table_words<EXT>(a, s_table, own[u].cells, q, fb[u]);
+        for (int u = 0; u < NQ; ++u) {
+            lse[u] = -INFINITY;
+            if (own[u].row >= 0) lse[u] = a.lse[(int64_t)h * a.n + t.first + (wave * NQ + u) * 16 + col];
+#pragma unroll
+            for (int c = 0; c < CK; ++c) {
+                const int c0 = h * a.dim + 32 * c + 8 * q, left = own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q;
+                f[u][c] = row_word<A>(a.q, (int64_t)own[u].row * a.ldq + c0, left);
+                g[u][c] = row_word<A>(a.dout, (int64_t)own[u].row * a.ld_dout + c0, left);
+            }
+        }
+    };
+    load_queries(head, fq, fo, base);
+    keys.point(a.k, a.v, head / share * a.dim);
+    keys.load(a, a.ldk, a.ldv);
+    if (!one) keys.places(a, t, 1);
     f32x4 dq[NQ][DT16], db[NQ][ET16 ? ET16 : 1];
+    auto begin_head = [&]() SMC_INLINE {
+        if (DT == kF16) grow = gradient_scale<TH>(a, t, head, head / share);
+        keep = length == 1 ? 0.f : grow;        // a window of one row: P is 1 whatever q, k and the bias are
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        delta[u] = quad_sum(delta[u]);
+        for (int u = 0; u < NQ; ++u) {
+            base[u] = lse_base(base[u]);
+            delta[u] = 0.f;
+            if (!kOwnDelta || !one) {
 #pragma unroll
-        for (int d = 0; d < DT16; ++d) dq[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < CK; ++c) {
+                    const u32x4 out = row_word<A>(a.out, (int64_t)own[u].row * a.ldo + head * a.dim + 32 * c + 8 * q,
+                                                  own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q);
 #pragma unroll
-        for (int d = 0; d < ET16; ++d) db[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
+                    for (int d = 0; d < 4; ++d)
+                        delta[u] += to_f32<DT>(out[d] & 0xffffu) * to_f32<DT>(fo[u][c][d] & 0xffffu) +
+                                    to_f32<DT>(out[d] >> 16) * to_f32<DT>(fo[u][c][d] >> 16);
+                }
+                delta[u] = quad_sum(delta[u]);
+            }
+            if (EXT) table_words<EXT>(a, s_table[head - first_head], own[u].cells, q, fb[u]);
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) dq[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < ET16; ++d) db[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        }
+    };
     // 64 keys, or the window's last `left`
     const char *const s_k = s_keys.x[0], *const s_v = s_keys.y[0], *const s_e = s_keys.e[0];
     auto step = [&](int left) SMC_INLINE {
@@ -165,8 +166,8 @@ __global__ __launch_bounds__(B::kThreads) void k_attention_queries(AttentionArgs
             for (int u = 0; u < NQ; ++u) s[u] = dp[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < CK; ++c) {
-                const u32x4 fk = tile_row<RW>(s_k, 16 * b + col, 4 * c + q);
-                const u32x4 fv = tile_row<RW>(s_v, 16 * b + col, 4 * c + q);
+                const u32x4 fk = at.along(s_k, 16 * b, c);
+                const u32x4 fv = at.along(s_v, 16 * b, c);
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) {
                     s[u] = mfma16<DT>(fk, fq[u][c], s[u]);
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(B::kThreads) void k_attention_queries(AttentionArgs
                 for (int u = 0; u < NQ; ++u) s[u] *= a.scale;
 #pragma unroll
                 for (int c = 0; c < CE; ++c) {
-                    const u32x4 fe = tile_row<RE>(s_e, 16 * b + col, 4 * c + q);
+                    const u32x4 fe = at_cells.along(s_e, 16 * b, c);
 #pragma unroll
                     for (int u = 0; u < NQ; ++u) s[u] = mfma16<DT>(fe, fb[u][c], s[u]);
                 }
@@ -203,14 +204,14 @@ __global__ __launch_bounds__(B::kThreads) void k_attention_queries(AttentionArgs
         auto products = [&](int h, const u32x4 (&g)[NQ]) SMC_INLINE {
 #pragma unroll
             for (int d = 0; d < DT16; ++d) {
-                const u32x4 f = tile_columns<RW>(s_k, d, 32 * h + 4 * q, 32 * h + 16 + 4 * q, lane);
+                const u32x4 f = at.across(s_k, d, 32 * h);
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) dq[u][d] = mfma16<DT>(f, g[u], dq[u][d]);
             }
             if (EXT)
 #pragma unroll
                 for (int d = 0; d < ET16; ++d) {
-                    const u32x4 f = tile_columns<RE>(s_e, d, 32 * h + 4 * q, 32 * h + 16 + 4 * q, lane);
+                    const u32x4 f = at_cells.across(s_e, d, 32 * h);
 #pragma unroll
                     for (int u = 0; u < NQ; ++u) db[u][d] = mfma16<DT>(f, g[u], db[u][d]);
                 }
@@ -262,215 +263,287 @@ __global__ __launch_bounds__(B::kThreads) void k_attention_queries(AttentionArgs
             }
         }
     };
-    const int length = t.end - t.begin;
-    if (length > 0) keys.commit(a, s_keys, 0, t);
-    for (int i = 0; i * kKeys < length; ++i) {
-        const int left = length - i * kKeys;
-        if (left > kKeys) keys.load(a, s_keys, i + 1, a.k, a.ldk, a.v, a.ldv, kv * a.dim);
-        if (active) step(left);
-        if (left > kKeys) keys.commit(a, s_keys, i + 1, t);
-    }
+    auto end_head = [&]() SMC_INLINE {
+        const float shrink = 1.f / grow;        // (a power of two)
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        if (q == 0 && own[u].row >= 0)
-            a.delta[(int64_t)head * a.n + t.first + (wave * NQ + u) * 16 + col] = delta[u];
-        store_row<DT, DP, A>(dq[u], a.scale * shrink, a.dq,
-                          own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dq + head * a.dim, a.dim, lane);
-    }
-    if constexpr (EXT > 0) {
-        // 16 queries at a time: dB to LDS, then each lane adds what lies at its distances, query
-        // after query
-        const Cells cells(a.extent);
-        float* const mine = s_db + wave * 16 * (EXT + 4);
-        if (active)
-#pragma unroll
-            for (int u = 0; u < NQ; ++u) {
-                const int rows = min(16, t.count - (wave * NQ + u) * 16);
-                if (rows <= 0) continue;
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int d = 0; d < ET16; ++d) *reinterpret_cast<f32x4*>(mine + col * (EXT + 4) + 16 * d + 4 * q) = db[u][d];
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int i = 0; i < kBins; ++i) {
-                    const int bin = 64 * i + lane, axis = cells.axis_of_entry(bin), first = cells.pick(cells.first, axis);
-                    const int away = cells.pick(cells.up, axis) - (bin - 2 * first), extent = cells.pick(a.extent, axis);
-                    float v = 0.f;
-                    if (64 * i < 2 * cells.all())
-                        for (int r = 0; r < rows; ++r) {
-                            const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)own[u].cells, r);
-                            const int c = (int)((at >> (8 * axis)) & 255u) - away;      // the key's cell
-                            const bool in = c >= first && c < first + extent;
-                            const float x = mine[r * (EXT + 4) + (in ? c : 0)];
-                            v += in ? x : 0.f;
-                        }
-                    bins[i] += bin < 2 * cells.all() ? v : 0.f;
-                }
-            }
-    }
-    if constexpr (EXT > 0) {
-        // the waves' sums, then buckets: the outermost ones hold every distance beyond them
-        float* const s_by = s_db;                       // [wave][64 kBins]
-        static_assert(B::kWaves * 64 * kBins <= B::kWaves * 16 * (EXT + 4), "room");
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kBins; ++i) s_by[(wave * kBins + i) * 64 + lane] = bins[i];
-        __syncthreads();
-        const int buckets = 2 * a.reach + 1;
-        float* const part = a.part + ((int64_t)tile * a.heads + head) * 3 * buckets;
-        for (int i = threadIdx.x; i < 3 * buckets; i += TH) {
-            const Cells cells(a.extent);
-            const int axis = i / buckets, d = i % buckets - a.reach, far = cells.pick(a.extent, axis) - 1;
-            const int zero = 2 * cells.pick(cells.first, axis) + cells.pick(cells.up, axis);
-            const int from = d == -a.reach ? -far : max(d, -far), to = d == a.reach ? far : min(d, far);
-            float v = 0.f;
-            for (int k = from; k <= to; ++k)
-#pragma unroll
-                for (int w = 0; w < B::kWaves; ++w) v += s_by[w * kBins * 64 + zero - k];
-            part[i] = v * shrink;
+        for (int u = 0; u < NQ; ++u) {
+            if (q == 0 && own[u].row >= 0)
+                a.delta[(int64_t)head * a.n + t.first + (wave * NQ + u) * 16 + col] = delta[u];
+            store_row<DT, DP, A>(dq[u], a.scale * shrink, a.dq,
+                                 own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dq + head * a.dim, a.dim, lane);
         }
+        if constexpr (EXT > 0) {
+            // 16 queries at a time: dB to LDS, then each lane adds what lies at its distances (64 a
+            // word of bins, as load_table counts them), query after query
+            const Cells cells(a.extent);
+            float* const mine = s_db + wave * 16 * (EXT + 4);
+            float bins[kBins];
+#pragma unroll
+            for (int i = 0; i < kBins; ++i) bins[i] = 0.f;
+            if (active)
+#pragma unroll
+                for (int u = 0; u < NQ; ++u) {
+                    const int rows = min(16, t.count - (wave * NQ + u) * 16);
+                    if (rows <= 0) continue;
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int d = 0; d < ET16; ++d) *reinterpret_cast<f32x4*>(mine + col * (EXT + 4) + 16 * d + 4 * q) = db[u][d];
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int i = 0; i < kBins; ++i) {
+                        const int bin = 64 * i + lane, axis = cells.axis_of_entry(bin), first = cells.pick(cells.first, axis);
+                        const int away = cells.pick(cells.up, axis) - (bin - 2 * first), extent = cells.pick(a.extent, axis);
+                        float v = 0.f;
+                        if (64 * i < 2 * cells.all())
+                            for (int r = 0; r < rows; ++r) {
+                                const uint32_t seen = (uint32_t)__builtin_amdgcn_readlane((int)own[u].cells, r);
+                                const int c = (int)((seen >> (8 * axis)) & 255u) - away;      // the key's cell
+                                const bool in = c >= first && c < first + extent;
+                                const float x = mine[r * (EXT + 4) + (in ? c : 0)];
+                                v += in ? x : 0.f;
+                            }
+                        bins[i] += bin < 2 * cells.all() ? v : 0.f;
+                    }
+                }
+            // the waves' sums, then buckets: the outermost ones hold every distance beyond them
+            float* const s_by = s_db;                       // [wave][64 kBins]
+            static_assert(64 * kBins <= 16 * (EXT + 4), "room");
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kBins; ++i) s_by[(wave * kBins + i) * 64 + lane] = bins[i];
+            __syncthreads();
+            const int buckets = 2 * a.reach + 1;
+            float* const part = a.part + ((int64_t)tile * a.heads + head) * 3 * buckets;
+            for (int i = threadIdx.x; i < 3 * buckets; i += TH) {
+                const int axis = i / buckets, d = i % buckets - a.reach, far = cells.pick(a.extent, axis) - 1;
+                const int zero = 2 * cells.pick(cells.first, axis) + cells.pick(cells.up, axis);
+                const int from = d == -a.reach ? -far : max(d, -far), to = d == a.reach ? far : min(d, far);
+                float v = 0.f;
+                for (int k = from; k <= to; ++k)
+#pragma unroll
+                    for (int w = 0; w < B::kWaves; ++w) v += s_by[w * kBins * 64 + zero - k];
+                part[i] = v * shrink;
+            }
+        }
+    };
+    int i = 0;                          // the step of the head
+    keys.commit(s_keys, 0, true);
+    begin_head();
+    for (;;) {
+        const int left = length - i * kKeys;
+        const bool last = left <= kKeys, more = !last || head + 1 < first_head + heads;
+        u32x4 fq_next[B::kHeads > 1 ? NQ : 1][CK], fo_next[B::kHeads > 1 ? NQ : 1][CK];
+        float base_next[B::kHeads > 1 ? NQ : 1];
+        if (more) {
+            if constexpr (B::kHeads > 1)
+                if (last) {
+                    keys.point(a.k, a.v, (head + 1) / share * a.dim);
+                    load_queries(head + 1, fq_next, fo_next, base_next);
+                }
+            keys.load(a, a.ldk, a.ldv);
+            if (!one) keys.places(a, t, (last ? 1 : i + 2) * kKeys < length ? (last ? 1 : i + 2) : 0);
+        }
+        if (active) step(left);
+        if (last) end_head();
+        if (!more) break;
+        keys.commit(s_keys, 0, !one);
+        ++i;
+        if constexpr (B::kHeads > 1)
+            if (last) {
+                i = 0;
+                ++head;
+#pragma unroll
+                for (int u = 0; u < NQ; ++u) {
+                    base[u] = base_next[u];
+#pragma unroll
+                    for (int c = 0; c < CK; ++c) {
+                        fq[u][c] = fq_next[u][c];
+                        fo[u][c] = fo_next[u][c];
+                    }
+                }
+                begin_head();
+            }
     }
 }
 
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads) void k_attention_keys(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_keys(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NK = B::kColumns, TH = B::kThreads;
     typedef Walk<DT, DP, EXT, A, B, 1> Queries;
     __shared__ __align__(16) typename Queries::Memory s_queries;
     __shared__ __align__(16) float s_base[kKeys], s_delta[kKeys];
     __shared__ __align__(16) uint16_t s_table[EXT ? 2 * kTableEntries<EXT> : 2];
-    int tile, kv;
-    if (!tile_and_head(a.n_tiles, a.kv_heads, tile, kv)) return;
+    int tile, kv;                       // the block's heads: those of `heads_each` heads of k and v from kv on
+    if (!tile_and_head(a.n_tiles, a.kv_heads, a.heads_each, tile, kv)) return;
     const WindowTile t = a.tiles[tile];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-    const int each = a.heads / a.kv_heads;
-    float grow = 1.f;
-    if (DT == kF16) {                           // the smallest factor of the group's heads serves all
-        grow = gradient_scale<TH>(a, t, kv * each, kv);
-        for (int i = 1; i < each; ++i) grow = fminf(grow, gradient_scale<TH>(a, t, kv * each + i, kv));
-    }
+    const int share = a.heads / a.kv_heads, end_head = min(kv + a.heads_each, a.kv_heads) * share;
+    const int length = t.end - t.begin;
+    const bool active = wave * NK * 16 < t.count, one = length <= kKeys;    // one step a head
     const float to_log2 = EXT ? kLog2e : a.scale * kLog2e;
-    // a window of one row: P is 1 whatever q, k and the bias are
-    const float keep = t.end - t.begin == 1 ? 0.f : grow;
-    const bool active = wave * NK * 16 < t.count;
+    const TileLane<RW> at(lane);
+    const TileLane<RE> at_cells(lane);
     WindowPlace own[NK];
 #pragma unroll
     for (int u = 0; u < NK; ++u) own[u] = own_place(a, t, (wave * NK + u) * 16 + col);
+    Queries queries;
+    queries.places(a, t, 0);
     u32x4 fk[NK][CK], fv[NK][CK], fb[NK][CE ? CE : 1];
+    auto load_keys = [&](int h, u32x4 (&f)[NK][CK], u32x4 (&g)[NK][CK]) SMC_INLINE {
 #pragma unroll
-    for (int u = 0; u < NK; ++u)
+        for (int u = 0; u < NK; ++u)
 #pragma unroll
-        for (int c = 0; c < CK; ++c) {
-            const int at = kv * a.dim + 32 * c + 8 * q, left = own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q;
-            fk[u][c] = row_word<A>(a.k, (int64_t)own[u].row * a.ldk + at, left);
-            fv[u][c] = row_word<A>(a.v, (int64_t)own[u].row * a.ldv + at, left);
-        }
+            for (int c = 0; c < CK; ++c) {
+                const int c0 = h * a.dim + 32 * c + 8 * q, left = own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q;
+                f[u][c] = row_word<A>(a.k, (int64_t)own[u].row * a.ldk + c0, left);
+                g[u][c] = row_word<A>(a.v, (int64_t)own[u].row * a.ldv + c0, left);
+            }
+    };
+    int head = kv * share, i = 0;       // the head, and its step
+    bool with_cells = true;             // a window of one step has the same for every head
+    TableLoads<DT, EXT, TH, true> table;
+    float grow = 1.f, keep = 1.f, base = INFINITY, delta = 0.f;     // (of this thread's query, in the first 64)
     f32x4 dk[NK][DT16], dv[NK][DT16];
+    auto begin_keys = [&]() SMC_INLINE {
+        if (DT == kF16) {                       // the smallest factor of the heads that share them serves all
+            grow = gradient_scale<TH>(a, t, head, kv);
+            for (int h = 1; h < share; ++h) grow = fminf(grow, gradient_scale<TH>(a, t, head + h, kv));
+        }
+        keep = length == 1 ? 0.f : grow;        // a window of one row: P is 1 whatever q, k and the bias are
 #pragma unroll
-    for (int u = 0; u < NK; ++u)
+        for (int u = 0; u < NK; ++u)
 #pragma unroll
-        for (int d = 0; d < DT16; ++d) dk[u][d] = dv[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int head = kv * each; head < (kv + 1) * each; ++head) {
-        __syncthreads();                        // (the tiles and the table of the head before)
-        if (EXT) load_table<DT, EXT, TH, true>(a, head, s_table);
-        Queries queries;
-        queries.start(a, s_queries, t, a.q, a.ldq, a.dout, a.ld_dout, head * a.dim);
-        if (EXT)
+            for (int d = 0; d < DT16; ++d) dk[u][d] = dv[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    };
+    auto end_keys = [&]() SMC_INLINE {
+        const float f = a.scale / grow;
+#pragma unroll
+        for (int u = 0; u < NK; ++u) {
+            const int c0 = kv * a.dim;
+            store_row<DT, DP, A>(dk[u], f, a.dk, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dk + c0, a.dim, lane);
+            store_row<DT, DP, A>(dv[u], 1.f, a.dv, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dv + c0, a.dim, lane);
+        }
+    };
+    auto load = [&](int h, int step) SMC_INLINE {
+        if (step == 0) {
+            queries.point(a.q, a.dout, h * a.dim);
+            if (EXT) table.load(a, h);
+        }
+        queries.load(a, a.ldq, a.ld_dout);
+        const int place = t.begin + step * kKeys + (int)threadIdx.x;
+        base = -INFINITY;                       // past the end: P is 0
+        delta = 0.f;
+        if (threadIdx.x < kKeys && place < t.end) {
+            base = a.lse[(int64_t)h * a.n + place];
+            delta = a.delta[(int64_t)h * a.n + place];
+        }
+    };
+    auto commit = [&](bool first) SMC_INLINE {      // (first: of a head)
+        __syncthreads();
+        if (threadIdx.x < kKeys) {
+            s_base[threadIdx.x] = lse_base(base);
+            s_delta[threadIdx.x] = delta * keep;
+        }
+        if (EXT && first) table.commit(a, s_table);
+        queries.commit(s_queries, 0, with_cells);
+        with_cells = !one;
+        if (EXT && first)
 #pragma unroll
             for (int u = 0; u < NK; ++u) table_words<EXT>(a, s_table, own[u].cells, q, fb[u]);
-        const float* const lse = a.lse + (int64_t)head * a.n;
-        const float* const deltas = a.delta + (int64_t)head * a.n;
-        float base = INFINITY, delta = 0.f;     // of this thread's query, in the first 64 threads
-        auto load_query = [&](int i) SMC_INLINE {
-            const int at = t.begin + i * kKeys + (int)threadIdx.x;
-            const bool in = threadIdx.x < kKeys && at < t.end;
-            base = in ? lse_base(lse[at]) : INFINITY;       // past the end: P is 0
-            delta = in ? deltas[at] * keep : 0.f;
-        };
-        auto commit = [&](int i) SMC_INLINE {
-            __syncthreads();
-            if (threadIdx.x < kKeys) {
-                s_base[threadIdx.x] = base;
-                s_delta[threadIdx.x] = delta;
+    };
+    load_keys(kv, fk, fv);
+    load(head, 0);
+    if (!one) queries.places(a, t, 1);
+    begin_keys();
+    commit(true);
+    const char *const s_q = s_queries.x[0], *const s_o = s_queries.y[0], *const s_e = s_queries.e[0];
+    for (;;) {
+        const bool last = length - i * kKeys <= kKeys, more = !last || head + 1 < end_head;
+        const bool turns = last && head + 1 == (kv + 1) * share;        // other keys and values next
+        u32x4 fk_next[B::kHeads > 1 ? NK : 1][CK], fv_next[B::kHeads > 1 ? NK : 1][CK];
+        if (more) {
+            load(last ? head + 1 : head, last ? 0 : i + 1);
+            if constexpr (B::kHeads > 1)
+                if (turns) load_keys(kv + 1, fk_next, fv_next);
+            if (!one) queries.places(a, t, (last ? 1 : i + 2) * kKeys < length ? (last ? 1 : i + 2) : 0);
+        }
+        if (active)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 p[NK], g[NK];
+#pragma unroll
+            for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                f32x4 s[NK], dp[NK];
+#pragma unroll
+                for (int u = 0; u < NK; ++u) s[u] = dp[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < CK; ++c) {
+                    const u32x4 fq = at.along(s_q, 16 * b, c);
+                    const u32x4 fo = at.along(s_o, 16 * b, c);
+#pragma unroll
+                    for (int u = 0; u < NK; ++u) {
+                        s[u] = mfma16<DT>(fq, fk[u][c], s[u]);
+                        dp[u] = mfma16<DT>(fo, fv[u][c], dp[u]);
+                    }
+                }
+                if (EXT) {
+#pragma unroll
+                    for (int u = 0; u < NK; ++u) s[u] *= a.scale;
+#pragma unroll
+                    for (int c = 0; c < CE; ++c) {
+                        const u32x4 fe = at_cells.along(s_e, 16 * b, c);
+#pragma unroll
+                        for (int u = 0; u < NK; ++u) s[u] = mfma16<DT>(fe, fb[u][c], s[u]);
+                    }
+                }
+                const f32x4 bs = *reinterpret_cast<const f32x4*>(s_base + 16 * b + 4 * q);
+                const f32x4 dl = *reinterpret_cast<const f32x4*>(s_delta + 16 * b + 4 * q);
+#pragma unroll
+                for (int u = 0; u < NK; ++u) {
+                    float v[4], w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = exp2_of(s[u][e] * to_log2 - bs[e]);
+                        w[e] = v[e] * fmaf(dp[u][e], keep, -dl[e]);
+                    }
+                    p[u][2 * (b & 1)] = pack2<DT>(v[0], v[1]);
+                    p[u][2 * (b & 1) + 1] = pack2<DT>(v[2], v[3]);
+                    g[u][2 * (b & 1)] = pack2<DT>(w[0], w[1]);
+                    g[u][2 * (b & 1) + 1] = pack2<DT>(w[2], w[3]);
+                }
             }
-            queries.commit(a, s_queries, i, t);
-        };
-        load_query(0);
-        const int length = t.end - t.begin;
-        if (length > 0) commit(0);
-        for (int i = 0; i * kKeys < length; ++i) {
-            const int left = length - i * kKeys;
-            if (left > kKeys) {
-                queries.load(a, s_queries, i + 1, a.q, a.ldq, a.dout, a.ld_dout, head * a.dim);
-                load_query(i + 1);
+#pragma unroll
+            for (int d = 0; d < DT16; ++d) {
+                const u32x4 fo = at.across(s_o, d, 32 * h);
+                const u32x4 fq = at.across(s_q, d, 32 * h);
+#pragma unroll
+                for (int u = 0; u < NK; ++u) {
+                    dv[u][d] = mfma16<DT>(fo, p[u], dv[u][d]);
+                    dk[u][d] = mfma16<DT>(fq, g[u], dk[u][d]);
+                }
             }
-            const char *const s_q = s_queries.x[0], *const s_o = s_queries.y[0], *const s_e = s_queries.e[0];
-            if (active)
+        }
+        if (turns) end_keys();
+        if (!more) break;
+        ++i;
+        if (last) {
+            i = 0;
+            ++head;
+        }
+        if constexpr (B::kHeads > 1)
+            if (turns) {
+                ++kv;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 p[NK], g[NK];
-#pragma unroll
-                for (int b = 2 * h; b < 2 * h + 2; ++b) {
-                    f32x4 s[NK], dp[NK];
-#pragma unroll
-                    for (int u = 0; u < NK; ++u) s[u] = dp[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+                for (int u = 0; u < NK; ++u)
 #pragma unroll
                     for (int c = 0; c < CK; ++c) {
-                        const u32x4 fq = tile_row<RW>(s_q, 16 * b + col, 4 * c + q);
-                        const u32x4 fo = tile_row<RW>(s_o, 16 * b + col, 4 * c + q);
-#pragma unroll
-                        for (int u = 0; u < NK; ++u) {
-                            s[u] = mfma16<DT>(fq, fk[u][c], s[u]);
-                            dp[u] = mfma16<DT>(fo, fv[u][c], dp[u]);
-                        }
+                        fk[u][c] = fk_next[u][c];
+                        fv[u][c] = fv_next[u][c];
                     }
-                    if (EXT) {
-#pragma unroll
-                        for (int u = 0; u < NK; ++u) s[u] *= a.scale;
-#pragma unroll
-                        for (int c = 0; c < CE; ++c) {
-                            const u32x4 fe = tile_row<RE>(s_e, 16 * b + col, 4 * c + q);
-#pragma unroll
-                            for (int u = 0; u < NK; ++u) s[u] = mfma16<DT>(fe, fb[u][c], s[u]);
-                        }
-                    }
-                    const f32x4 bs = *reinterpret_cast<const f32x4*>(s_base + 16 * b + 4 * q);
-                    const f32x4 dl = *reinterpret_cast<const f32x4*>(s_delta + 16 * b + 4 * q);
-#pragma unroll
-                    for (int u = 0; u < NK; ++u) {
-                        float v[4], w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v[e] = exp2_of(s[u][e] * to_log2 - bs[e]);
-                            w[e] = v[e] * fmaf(dp[u][e], keep, -dl[e]);
-                        }
-                        p[u][2 * (b & 1)] = pack2<DT>(v[0], v[1]);
-                        p[u][2 * (b & 1) + 1] = pack2<DT>(v[2], v[3]);
-                        g[u][2 * (b & 1)] = pack2<DT>(w[0], w[1]);
-                        g[u][2 * (b & 1) + 1] = pack2<DT>(w[2], w[3]);
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < DT16; ++d) {
-                    const u32x4 fo = tile_columns<RW>(s_o, d, 32 * h + 4 * q, 32 * h + 16 + 4 * q, lane);
-                    const u32x4 fq = tile_columns<RW>(s_q, d, 32 * h + 4 * q, 32 * h + 16 + 4 * q, lane);
-#pragma unroll
-                    for (int u = 0; u < NK; ++u) {
-                        dv[u][d] = mfma16<DT>(fo, p[u], dv[u][d]);
-                        dk[u][d] = mfma16<DT>(fq, g[u], dk[u][d]);
-                    }
-                }
+                begin_keys();
             }
-            if (left > kKeys) commit(i + 1);
-        }
-    }
-    const float f = a.scale / grow;
-#pragma unroll
-    for (int u = 0; u < NK; ++u) {
-        const int at = kv * a.dim;
-        store_row<DT, DP, A>(dk[u], f, a.dk, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dk + at, a.dim, lane);
-        store_row<DT, DP, A>(dv[u], 1.f, a.dv, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dv + at, a.dim, lane);
+        commit(last);
     }
 }
 
@@ -498,13 +571,17 @@ template <int DT, int DP, int EXT, bool A, class BQ, class BK>
 hipError_t attention_backward_t(const AttentionArgs& a, hipStream_t s) {
     if (a.n_tiles > 0) {
         if (DT == kF16) launch(k_attention_range<DT, A>, grid_of(a.n_tiles64), dim3(256), 0, s, a);
-        launch(k_attention_queries<DT, DP, EXT, A, BQ>, attention_grid(a.n_tiles, a.heads), dim3(BQ::kThreads), 0, s, a);
         AttentionArgs b = a;
+        b.heads_each = heads_a_block(a.n_tiles, a.heads, BQ::kHeads);
+        launch(k_attention_queries<DT, DP, EXT, A, BQ>, attention_grid(a.n_tiles, a.heads, b.heads_each), dim3(BQ::kThreads), 0,
+               s, b);
         if (BK::kRows == 64) {
             b.tiles = a.tiles64;
             b.n_tiles = a.n_tiles64;
         }
-        launch(k_attention_keys<DT, DP, EXT, A, BK>, attention_grid(b.n_tiles, a.kv_heads), dim3(BK::kThreads), 0, s, b);
+        b.heads_each = heads_a_block(b.n_tiles, a.kv_heads, BK::kHeads);
+        launch(k_attention_keys<DT, DP, EXT, A, BK>, attention_grid(b.n_tiles, a.kv_heads, b.heads_each), dim3(BK::kThreads), 0,
+               s, b);
     }
     if (EXT)
         launch(k_table_sum<DT>, dim3((unsigned)((3 * (2 * a.reach + 1) + 15) / 16), (unsigned)a.heads), dim3(1024), 0, s, a);
@@ -515,7 +592,7 @@ template <int DT, int DP, int EXT>
 hipError_t attention_backward_by_length(const AttentionArgs& a, int lengths, hipStream_t s) {
     // (of 128 keys of 128 elements, two gradients do not fit the registers)
     typedef typename std::conditional<DP == 128, BlockMid, BlockLong>::type BlockKeys;
-    if (lengths == kShortWindows) return attention_backward_t<DT, DP, EXT, true, BlockShort<DP>, BlockShort<DP>>(a, s);
+    if (lengths == kShortWindows) return attention_backward_t<DT, DP, EXT, true, BlockShort, BlockShort>(a, s);
     if (lengths == kMidWindows) return attention_backward_t<DT, DP, EXT, true, BlockMid, BlockMid>(a, s);
     return attention_backward_t<DT, DP, EXT, true, BlockLong, BlockKeys>(a, s);
 }

@@ -15,7 +15,7 @@ namespace smc {
 namespace {
 
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads) void k_attention(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 2 : 1) void k_attention(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NQ = B::kColumns, TH = B::kThreads;
     // two buffers cost registers (addresses): us for windows of 1,000, 16,000 x 8 heads of 64 without and 40,000 x 4 of 32
@@ -23,54 +23,59 @@ __global__ __launch_bounds__(B::kThreads) void k_attention(AttentionArgs a) {
     constexpr int kBuffers = B::kWaves > 2 && (NQ == 1 || EXT == 0) ? 2 : 1;
     typedef Walk<DT, DP, EXT, A, B, kBuffers> Keys;
     __shared__ __align__(16) typename Keys::Memory s_keys;
-    __shared__ __align__(16) uint16_t s_table[EXT ? 2 * kTableEntries<EXT> : 2];
+    __shared__ __align__(16) uint16_t s_table[B::kHeads][EXT ? 2 * kTableEntries<EXT> : 2];
     int tile, head;
-    if (!tile_and_head(a.n_tiles, a.heads, tile, head)) return;
+    if (!tile_and_head(a.n_tiles, a.heads, a.heads_each, tile, head)) return;
     const WindowTile t = a.tiles[tile];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-    const int kv = head / (a.heads / a.kv_heads);
-    if (EXT) load_table<DT, EXT, TH, false>(a, head, s_table);
+    const int share = a.heads / a.kv_heads, first_head = head, heads = min(a.heads_each, a.heads - head);
+    const int length = t.end - t.begin;
+    const bool active = wave * NQ * 16 < t.count, one = length <= kKeys;    // one step a head
     // exponents in base 2: of the products times their scale, or of the scaled sums
     const float to_log2 = EXT ? kLog2e : a.scale * kLog2e;
-    const bool active = wave * NQ * 16 < t.count;
+    const TileLane<RW> at(lane);
+    const TileLane<RE> at_cells(lane);
     WindowPlace own[NQ];
-    u32x4 fq[NQ][CK], fb[NQ][CE ? CE : 1];
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        own[u] = own_place(a, t, (wave * NQ + u) * 16 + col);
-#pragma unroll
-        for (int c = 0; c < CK; ++c)
-            fq[u][c] = row_word<A>(a.q, (int64_t)own[u].row * a.ldq + head * a.dim + 32 * c + 8 * q,
-                                own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q);
-    }
+    for (int u = 0; u < NQ; ++u) own[u] = own_place(a, t, (wave * NQ + u) * 16 + col);
     Keys keys;
-    keys.start(a, s_keys, t, a.k, a.ldk, a.v, a.ldv, kv * a.dim);
-    if (EXT)
+    keys.places(a, t, 0);
+    if (EXT) load_tables<DT, EXT, TH, B::kHeads>(a, head, heads, s_table);
+    u32x4 fq[NQ][CK], fb[NQ][CE ? CE : 1];
+    auto load_queries = [&](int h, u32x4 (&f)[NQ][CK]) SMC_INLINE {
 #pragma unroll
         for (int u = 0; u < NQ; ++u)
-            table_words<EXT>(a, s_table, own[u].cells, q, fb[u]);
-    float top[NQ], sum[NQ];
+#pragma unroll
+            for (int c = 0; c < CK; ++c)
+                f[u][c] = row_word<A>(a.q, (int64_t)own[u].row * a.ldq + h * a.dim + 32 * c + 8 * q,
+                                      own[u].row < 0 ? 0 : a.dim - 32 * c - 8 * q);
+    };
+    load_queries(head, fq);
+    keys.point(a.k, a.v, head / share * a.dim);
+    keys.load(a, a.ldk, a.ldv);
+    if (!one) keys.places(a, t, 1);
+    float top[NQ], base[NQ], sum[NQ];
     f32x4 o[NQ][DT16];
+    auto begin_head = [&]() SMC_INLINE {
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        top[u] = -INFINITY;
-        sum[u] = 0.f;
+        for (int u = 0; u < NQ; ++u) {
+            top[u] = -INFINITY;
+            base[u] = sum[u] = 0.f;
 #pragma unroll
-        for (int d = 0; d < DT16; ++d) o[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
-    // 64 keys, or the window's last `left`
-    auto step = [&](int left, const char* s_k, const char* s_v, const char* s_e) SMC_INLINE {
-        f32x4 s[4][NQ];
+            for (int d = 0; d < DT16; ++d) o[u][d] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (EXT) table_words<EXT>(a, s_table[head - first_head], own[u].cells, q, fb[u]);
+        }
+    };
+    // A step's 16 KB keys from 16 b0 on, of which `left` are the window's: scores, then softmax and out
+    constexpr int KB = B::kHalves ? 2 : 4;
+    auto scores = [&](f32x4 (&s)[KB][NQ], int b0, int left, const char* s_k, const char* s_e) SMC_INLINE {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int u = 0; u < NQ; ++u) s[b][u] = (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (B::kSkips && 16 * b >= left) continue;
+        for (int b = 0; b < KB; ++b) {
 #pragma unroll
             for (int u = 0; u < NQ; ++u) s[b][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < CK; ++c) {
-                const u32x4 fk = tile_row<RW>(s_k, 16 * b + col, 4 * c + q);
+                const u32x4 fk = at.along(s_k, 16 * (b0 + b), c);
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) s[b][u] = mfma16<DT>(fk, fq[u][c], s[b][u]);
             }
@@ -79,48 +84,64 @@ __global__ __launch_bounds__(B::kThreads) void k_attention(AttentionArgs a) {
                 for (int u = 0; u < NQ; ++u) s[b][u] *= a.scale;
 #pragma unroll
                 for (int c = 0; c < CE; ++c) {
-                    const u32x4 fe = tile_row<RE>(s_e, 16 * b + col, 4 * c + q);
+                    const u32x4 fe = at_cells.along(s_e, 16 * (b0 + b), c);
 #pragma unroll
                     for (int u = 0; u < NQ; ++u) s[b][u] = mfma16<DT>(fe, fb[u][c], s[b][u]);
                 }
             }
         }
-        if (left < kKeys)                           // keys past the window's end
+    };
+    auto cut = [&](f32x4 (&s)[KB][NQ], int left) SMC_INLINE {      // keys past the window's end
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u) s[b][u][e] = 16 * b + 4 * q + e < left ? s[b][u][e] : -INFINITY;
-        u32x4 p[NQ][2];
-        float most[NQ], base[NQ];
+                for (int u = 0; u < NQ; ++u) s[b][u][e] = 16 * b + 4 * q + e < left ? s[b][u][e] : -INFINITY;
+    };
+    // The base of the exponentials follows the maximum only where that is 2^8 above it: P then stays below 2^8,
+    // as exact as below 1, and out and the sums are seldom rescaled.
+    auto maxima = [&](const f32x4 (&s)[KB][NQ]) SMC_INLINE {
+        float most[NQ];
         bool grows = false;
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
-            float m = top[u];
+            float m = s[0][u][0];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) m = fmaxf(m, s[b][u][e]);
             most[u] = quad_max(m);
-            base[u] = most[u] == -INFINITY ? 0.f : most[u] * to_log2;       // (every score -inf so far)
-            grows |= most[u] > top[u];
+            grows |= most[u] > top[u] + 8.f / to_log2;
         }
         if (any_lane(grows))
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
-                const float shrink = exp2_of(top[u] * to_log2 - base[u]);
+                const float m = fmaxf(top[u], most[u]), next = m == -INFINITY ? 0.f : m * to_log2;     // (every score -inf so far)
+                const float shrink = exp2_of(top[u] * to_log2 - next);
                 sum[u] *= shrink;
 #pragma unroll
                 for (int d = 0; d < DT16; ++d) o[u][d] *= shrink;
-                top[u] = most[u];
+                top[u] = m;
+                base[u] = next;
             }
+    };
+    auto products = [&](f32x4 (&s)[KB][NQ], int b0, const char* s_v) SMC_INLINE {
+        u32x4 p[NQ][KB / 2];
+        // values before the exponentials, which cover their latency (else read two at a time, when they are needed)
+        constexpr bool kEarly = DP <= 64 && EXT == 0;
+        u32x4 fv[kEarly ? KB / 2 : 1][DT16];
+        if (kEarly) {
 #pragma unroll
-        for (int u = 0; u < NQ; ++u) {
+            for (int h = 0; h < KB / 2; ++h)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                p[u][b >> 1][2 * (b & 1)] = p[u][b >> 1][2 * (b & 1) + 1] = 0u;
-                if (B::kSkips && 16 * b >= left) continue;
+                for (int d = 0; d < DT16; ++d) fv[kEarly ? h : 0][d] = at.across(s_v, d, 16 * b0 + 32 * h);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int u = 0; u < NQ; ++u) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[b][u][e] = exp2_of(s[b][u][e] * to_log2 - base[u]);
@@ -129,36 +150,77 @@ __global__ __launch_bounds__(B::kThreads) void k_attention(AttentionArgs a) {
                 p[u][b >> 1][2 * (b & 1)] = pack2<DT>(s[b][u][0], s[b][u][1]);
                 p[u][b >> 1][2 * (b & 1) + 1] = pack2<DT>(s[b][u][2], s[b][u][3]);
             }
-        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (B::kSkips && 32 * h >= left) continue;
+        for (int h = 0; h < KB / 2; ++h)
 #pragma unroll
             for (int d = 0; d < DT16; ++d) {
-                const u32x4 fv = tile_columns<RW>(s_v, d, 32 * h + 4 * q, 32 * h + 16 + 4 * q, lane);
+                if (!kEarly) fv[0][d] = at.across(s_v, d, 16 * b0 + 32 * h);
 #pragma unroll
-                for (int u = 0; u < NQ; ++u) o[u][d] = mfma16<DT>(fv, p[u][h], o[u][d]);
+                for (int u = 0; u < NQ; ++u) o[u][d] = mfma16<DT>(fv[kEarly ? h : 0][d], p[u][h], o[u][d]);
             }
+    };
+    auto step = [&](int b0, int left, const char* s_k, const char* s_v, const char* s_e) SMC_INLINE {
+        f32x4 s[KB][NQ];
+        scores(s, b0, left, s_k, s_e);
+        if (left < 16 * KB) cut(s, left);
+        maxima(s);
+        products(s, b0, s_v);
+    };
+    auto end_head = [&]() SMC_INLINE {
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+            const float total = quad_sum(sum[u]);
+            // no key, or every score -inf: zeros
+            store_row<DT, DP, A>(o[u], total == 0.f ? 0.f : 1.f / total, a.out,
+                                 own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ldo + head * a.dim, a.dim, lane);
+            if (a.lse && q == 0 && own[u].row >= 0)
+                a.lse[(int64_t)head * a.n + t.first + (wave * NQ + u) * 16 + col] =
+                    total == 0.f ? -INFINITY : top[u] * (EXT ? 1.f : a.scale) + logf(total);
         }
     };
-    const int length = t.end - t.begin;
-    if (length > 0) keys.commit(a, s_keys, 0, t);
-    for (int i = 0; i * kKeys < length; ++i) {
-        const int left = length - i * kKeys, buf = kBuffers == 2 ? i & 1 : 0;
-        if (left > kKeys) keys.load(a, s_keys, i + 1, a.k, a.ldk, a.v, a.ldv, kv * a.dim);
-        if (active) step(left, s_keys.x[buf], s_keys.y[buf], s_keys.e[buf]);
-        if (left > kKeys) keys.commit(a, s_keys, i + 1, t);
-    }
+    int i = 0, buf = 0;                 // the step of the head, and its buffer
+    keys.commit(s_keys, buf, true);
+    begin_head();
+    for (;;) {
+        const int left = length - i * kKeys;
+        const bool last = left <= kKeys, more = !last || head + 1 < first_head + heads;
+        u32x4 fq_next[B::kHeads > 1 ? NQ : 1][CK];
+        if (more) {
+            if constexpr (B::kHeads > 1)
+                if (last) {
+                    keys.point(a.k, a.v, (head + 1) / share * a.dim);
+                    load_queries(head + 1, fq_next);
+                }
+            keys.load(a, a.ldk, a.ldv);
+            if (!one) keys.places(a, t, (last ? 1 : i + 2) * kKeys < length ? (last ? 1 : i + 2) : 0);
+        }
+        // (the cells of a window of one step lie in the first buffer)
+        if (active)
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-        const float total = quad_sum(sum[u]);
-        // no key, or every score -inf: zeros
-        store_row<DT, DP, A>(o[u], total == 0.f ? 0.f : 1.f / total, a.out,
-                          own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ldo + head * a.dim, a.dim, lane);
-        if (a.lse && q == 0 && own[u].row >= 0)
-            a.lse[(int64_t)head * a.n + t.first + (wave * NQ + u) * 16 + col] =
-                total == 0.f ? -INFINITY : top[u] * (EXT ? 1.f : a.scale) + logf(total);
+            for (int b0 = 0; b0 < 4; b0 += KB)
+                if (b0 == 0 || 16 * b0 < left) step(b0, left - 16 * b0, s_keys.x[buf], s_keys.y[buf], s_keys.e[one ? 0 : buf]);
+        if (last) end_head();
+        if (!more) break;
+        if (kBuffers == 2) buf ^= 1;
+        keys.commit(s_keys, buf, !one);
+        ++i;
+        if constexpr (B::kHeads > 1)
+            if (last) {
+                i = 0;
+                ++head;
+#pragma unroll
+                for (int u = 0; u < NQ; ++u)
+#pragma unroll
+                    for (int c = 0; c < CK; ++c) fq[u][c] = fq_next[u][c];
+                begin_head();
+            }
     }
+}
+
+template <int DT, int DP, int EXT, bool A, class B>
+void attention_t(AttentionArgs a, hipStream_t s) {
+    a.heads_each = heads_a_block(a.n_tiles, a.heads, B::kHeads);
+    launch(k_attention<DT, DP, EXT, A, B>, attention_grid(a.n_tiles, a.heads, a.heads_each), dim3(B::kThreads), 0, s, a);
 }
 
 // Rows that are no whole 16-byte words take one kernel a width: their loads cost more than a better
@@ -166,11 +228,10 @@ __global__ __launch_bounds__(B::kThreads) void k_attention(AttentionArgs a) {
 template <int DT, int DP>
 hipError_t attention_by_cells(const AttentionArgs& a, int lengths, hipStream_t s) {
     const int cells = a.table ? Cells(a.extent).all() : 0;
-    const dim3 grid = attention_grid(a.n_tiles, a.heads);
-#define SMC_GO(EXT, A, B) launch(k_attention<DT, DP, EXT, A, B>, grid, dim3(B::kThreads), 0, s, a)
+    #define SMC_GO(EXT, A, B) attention_t<DT, DP, EXT, A, B>(a, s)
 #define SMC_CELLS(EXT)                                                         \
     do {                                                                       \
-        if (lengths == kShortWindows) SMC_GO(EXT, true, BlockShort<DP>);       \
+        if (lengths == kShortWindows) SMC_GO(EXT, true, BlockShort);       \
         else if (lengths == kMidWindows) SMC_GO(EXT, true, BlockMid);          \
         else SMC_GO(EXT, true, BlockLong);                                     \
     } while (0)

@@ -66,11 +66,14 @@ struct Cells {
 struct WindowTile {
     int first, count;   // places
     int begin, end;     // of the window; equal: the rows are in no window
+    int first64;        // the window's first tile of 64 places
+    int unused[3];
 };
 struct WindowHeader {
     uint32_t status;    // kSt* bits
     int tiles[3];       // of 32, 64 and 128 places
     int longest;        // rows of the longest window
+    unsigned long long pairs;   // sum of the squares of the windows' rows
 };
 constexpr int kMaxCells = 128;                  // elements of Cells
 constexpr int kMaxReach = 127;                  // cells lie no further apart
@@ -104,6 +107,7 @@ hipError_t launch_windows(const WindowArgs& a, hipStream_t s);
 struct AttentionArgs {
     int64_t n = 0;
     int heads = 0, kv_heads = 0, dim = 0;
+    int heads_each = 1;             // of a block
     float scale = 0.f;
     const void *q = nullptr, *k = nullptr, *v = nullptr;
     int64_t ldq = 0, ldk = 0, ldv = 0;

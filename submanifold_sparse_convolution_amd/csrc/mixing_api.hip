@@ -130,6 +130,7 @@ int build_windows(smc_windows_t* w, hipStream_t s) {
     if (!w->coords && w->ex > 0 && w->n > 0) return bad(SMC_ERR_ARG, "an extent needs coords");
     if (w->coords && w->ex < 1) return bad(SMC_ERR_ARG, "coords need an extent");
     w->tiles32 = w->tiles64 = w->tiles128 = w->longest = 0;
+    w->pairs = 0;
     WindowArgs p;
     p.n = w->n;
     p.windows = w->windows;
@@ -153,6 +154,7 @@ int build_windows(smc_windows_t* w, hipStream_t s) {
     w->tiles64 = h.tiles[1];
     w->tiles128 = h.tiles[2];
     w->longest = h.longest;
+    w->pairs = (int64_t)h.pairs;
     return SMC_OK;
 }
 
@@ -225,10 +227,23 @@ bool attention_words(const smc_attention_t* a, bool backward) {
                           words16(a->dv, a->ld_dv)));
 }
 
+// Blocks by the windows' lengths: short where they are short on average, long where the rows are mostly in
+// long ones (pairs / rows) and there are blocks for the device. Forward / backward in us, short, mid and long:
+//   40,000 rows x 4 heads of 32, cells, windows of 24   13.8, 17.0, 29.4 / 61.4, 79.9, 114.5
+//                                                  60   15.5, 13.4, 16.8 / 56.8, 46.9, 62.4
+//                                                 100   25.0, 19.0, 18.2 / 87.3, 67.2, 60.4
+//                                                 400   51.5, 37.3, 37.2 / 147.9, 111.7, 104.2
+//   16,000 x 8 heads of 64, windows of             24   15.6, 17.1, 26.5 / 44.4, 58.1, 84.6
+//                                                  60   16.5, 13.9, 16.3 / 45.7, 41.1, 50.5
+//                                                 100   22.2, 18.7, 18.1 / 62.7, 58.8, 54.7
+//                                                 400   45.5, 34.1, 31.4 / 135.8, 108.1, 97.5
+//   91,000 x 4 of 32, cells, 2,905 windows of 1 .. 160  50.5, 48.9, 67.5 / 172.2, 186.6, 227.4
+// Rows that are no whole 16-byte words have mid blocks only.
 int window_lengths(const smc_attention_t* a, bool backward) {
-    if (!attention_words(a, backward)) return kMidWindows;
-    const int64_t mean = a->windows->windows > 0 ? a->windows->n / a->windows->windows : 0;
-    return mean < 40 ? kShortWindows : mean < 160 ? kMidWindows : kLongWindows;
+    const smc_windows_t* w = a->windows;
+    if (!attention_words(a, backward) || w->windows < 1) return kMidWindows;
+    if (w->n / w->windows < 40) return kShortWindows;
+    return w->pairs / w->n < 96 || (int64_t)w->tiles128 * a->heads < device_cus() ? kMidWindows : kLongWindows;
 }
 
 int tiles_of(const smc_windows_t* w, int lengths) {

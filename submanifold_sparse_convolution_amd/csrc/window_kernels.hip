@@ -27,7 +27,7 @@ __device__ __forceinline__ int window_end(const WindowArgs& a, int64_t w) {
 __global__ __launch_bounds__(256) void k_windows_clear(WindowArgs a, uint32_t* seen, int64_t words) {
     const int64_t i = block_number() * 256 + threadIdx.x;
     if (i < words) seen[i] = 0;
-    if (i == 0) *header_of(a) = WindowHeader{0, {0, 0, 0}, 0};
+    if (i == 0) *header_of(a) = WindowHeader{0, {0, 0, 0}, 0, 0};
 }
 
 // Rows of the places: within [0, n), none twice.
@@ -89,7 +89,11 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
                                                         WindowTile* tiles128) {
     __shared__ int s_sum[3][1024];
     __shared__ int s_longest, s_bad;
-    if (threadIdx.x == 0) s_longest = s_bad = 0;
+    __shared__ unsigned long long s_pairs;
+    if (threadIdx.x == 0) {
+        s_longest = s_bad = 0;
+        s_pairs = 0;
+    }
     __syncthreads();
     int done[3] = {0, 0, 0};
     for (int64_t w0 = -1; w0 <= a.windows; w0 += 1024) {
@@ -101,7 +105,10 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
             if (w >= 0) {
                 const int raw = a.offsets[w];
                 if (raw != begin || (w < a.windows && a.offsets[w + 1] < raw)) atomicOr(&s_bad, 1);
-                if (w < a.windows) atomicMax(&s_longest, end - begin);
+                if (w < a.windows) {
+                    atomicMax(&s_longest, end - begin);
+                    atomicAdd(&s_pairs, (unsigned long long)(end - begin) * (unsigned long long)(end - begin));
+                }
             }
         }
         int count[3];
@@ -121,6 +128,7 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
             __syncthreads();
         }
         const bool inside = w >= 0 && w < a.windows;
+        const int first64 = (int)min((int64_t)done[1] + s_sum[1][threadIdx.x] - count[1], a.n / 64 + a.windows + 1);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const int size = 32 << k;
@@ -130,7 +138,7 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
             int64_t at = (int64_t)done[k] + s_sum[k][threadIdx.x] - count[k];
             for (int i = 0; i < count[k] && at + i < most; ++i) {
                 const int first = begin + i * size;
-                to[at + i] = WindowTile{first, min(size, end - first), inside ? begin : 0, inside ? end : 0};
+                to[at + i] = WindowTile{first, min(size, end - first), inside ? begin : 0, inside ? end : 0, first64, {0, 0, 0}};
             }
             done[k] = (int)min((int64_t)done[k] + s_sum[k][1023], most);
         }
@@ -140,6 +148,7 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
         WindowHeader* h = header_of(a);
         for (int k = 0; k < 3; ++k) h->tiles[k] = done[k];
         h->longest = s_longest;
+        h->pairs = s_pairs;
         if (s_bad) atomicOr(&h->status, (uint32_t)kStRange);
     }
 }
