@@ -8,8 +8,14 @@
 //
 // Two passes over the rows, one kernel each: sums of pieces, then outputs, whose
 // blocks add up the pieces of their sample first (a kernel between the two for that would
-// cost its launch). Bound by memory: x (and dy) are read twice, the second time largely from
-// the caches.
+// cost its launch). x (and dy) are read twice, the second time largely from the caches.
+//
+// 91,000 x 128 bf16 in six samples: 10.0 us of sums and 13.8 of outputs, 22.1 us a call (70 MB:
+// 9.1 at the rate of a large copy, x counted once); backward, 95,000 x 128 in two: 15.0 and 18.0,
+// 32.3 a call. A thread's rows are few there (192 x 16 words on 512 threads: 6), and what bounds
+// the kernels is latency: the loads', the tree's over a block's rows, the joining of pieces.
+// Without gain: six rows of a thread fetched before the pieces are joined (23.1 us); columns
+// summed by a thread each in place of the tree (25.7 for 24.2).
 //
 // Variances do not suffer from large means: sums are of differences from the
 // piece's first row, channel by channel, and channels and pieces are joined
@@ -22,15 +28,15 @@
 namespace smc {
 namespace {
 
-constexpr int kGroupThreads = 1024;
-constexpr int kGroupWaves = kGroupThreads / 64;
-static_assert(kMaxGroupChannels == kGroupThreads * W, "a row is held by a block");
+// Threads of a block: a row is held by one, 8 channels a thread.
+constexpr int kThreads = 512, kThreadsWide = 1024;
+static_assert(kMaxGroupChannels == kThreadsWide * W, "a row is held by a block");
 
 // ---- pieces --------------------------------------------------------------------
-// The rows are cut at every multiple of 2^rows_log and at the samples' borders.
+// The rows are cut at every multiple of `rows_each` and at the samples' borders.
 // Runs: the rows before the first sample, each sample, the rows after the last
 // (without offsets, one run). Piece number = run + multiples passed: it grows
-// with the rows, run r owns the numbers from (begin >> rows_log) + r on, one at least, and
+// with the rows, run r owns the numbers from begin / rows_each + r on, one at least, and
 // what a piece holds follows from the offsets alone, however uneven they are.
 
 struct Piece {
@@ -46,14 +52,18 @@ __device__ __forceinline__ int run_start(const GroupArgs& a, int run) {
     return min(max(a.offsets[run - 1], 0), (int)a.n);
 }
 
+__device__ __forceinline__ int multiples(const GroupArgs& a, int row) {
+    return (int)((uint32_t)row / (uint32_t)a.rows_each);
+}
+
 __device__ __forceinline__ Piece piece_of(const GroupArgs& a, int number) {
     Piece p;
     if (!a.offsets) {
         p.run = 1;
         p.run_begin = 0;
         p.run_end = (int)a.n;
-        p.begin = (int)min((int64_t)number << a.rows_log, a.n);
-        p.end = (int)min((int64_t)(number + 1) << a.rows_log, a.n);
+        p.begin = (int)min((int64_t)number * a.rows_each, a.n);
+        p.end = (int)min((int64_t)(number + 1) * a.rows_each, a.n);
         return p;
     }
     // the last run that owns a number up to this one
@@ -61,26 +71,26 @@ __device__ __forceinline__ Piece piece_of(const GroupArgs& a, int number) {
     const int lane = threadIdx.x & 63;
     for (int r0 = 0; r0 < a.samples + 2; r0 += 64) {
         const int r = r0 + lane;
-        const bool in = r < a.samples + 2 && (run_start(a, r) >> a.rows_log) + r <= number;
+        const bool in = r < a.samples + 2 && multiples(a, run_start(a, r)) + r <= number;
         run += __popcll(__ballot(in));
     }
     run = __builtin_amdgcn_readfirstlane(max(run, 0));
     p.run = run;
     p.run_begin = run_start(a, run);
     p.run_end = max(p.run_begin, run_start(a, run + 1));
-    const int64_t cut = (int64_t)max(number - run, 0) << a.rows_log;
+    const int64_t cut = (int64_t)max(number - run, 0) * a.rows_each;
     p.begin = (int)min(max((int64_t)p.run_begin, cut), (int64_t)p.run_end);
-    p.end = (int)max((int64_t)p.begin, min((int64_t)p.run_end, cut + ((int64_t)1 << a.rows_log)));
+    p.end = (int)max((int64_t)p.begin, min((int64_t)p.run_end, cut + a.rows_each));
     return p;
 }
 
 // First number of a run, and of the run's last row.
 __device__ __forceinline__ int first_piece(const GroupArgs& a, const Piece& p) {
-    return (p.run_begin >> a.rows_log) + (a.offsets ? p.run : 0);
+    return multiples(a, p.run_begin) + (a.offsets ? p.run : 0);
 }
 __device__ __forceinline__ int last_piece(const GroupArgs& a, const Piece& p) {
     const int row = max(p.run_begin, p.run_end - 1);
-    return (row >> a.rows_log) + (a.offsets ? p.run : 0);
+    return multiples(a, row) + (a.offsets ? p.run : 0);
 }
 __device__ __forceinline__ bool is_sample(const GroupArgs& a, const Piece& p) {
     return !a.offsets || (p.run >= 1 && p.run <= a.samples);
@@ -88,51 +98,48 @@ __device__ __forceinline__ bool is_sample(const GroupArgs& a, const Piece& p) {
 
 // ---- sums over a block ------------------------------------------------------------
 
-// v of the threads that share `word`, rows 0 .. rows - 1 of them (thread = row words + word): the
-// sums end up in row 0. Halves are joined in a fixed order. s: N x 512 floats.
-template <int N>
-__device__ __forceinline__ void sum_rows(float (&v)[N], int rows, int words, int row, int word, float* s) {
-    while (rows > 1) {
-        const int half = (rows + 1) >> 1;
-        __syncthreads();
-        if (row >= half && row < rows)
-#pragma unroll
-            for (int e = 0; e < N; ++e) s[e * (kGroupThreads / 2) + (row - half) * words + word] = v[e];
-        __syncthreads();
-        if (row + half < rows)
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[e] += s[e * (kGroupThreads / 2) + row * words + word];
-        rows = half;
-    }
-    __syncthreads();
-}
-
 // How a block's threads lie over rows of c channels.
+template <int T>
 struct Lay {
     int words, rows, word, row;
     bool ok;
     __device__ explicit Lay(int c) {
         words = (c + W - 1) / W;
-        rows = kGroupThreads / words;
+        rows = T / words;
         row = threadIdx.x / words;
         word = threadIdx.x - row * words;
         ok = row < rows;
     }
 };
 
+// The threads' values added over the rows of the block: in row 0 of them at the end. Halves are
+// joined in a fixed order. s: N x T / 2 floats.
+template <int T, int N>
+__device__ __forceinline__ void sum_rows(float (&v)[N], const Lay<T>& l, float* s) {
+    for (int rows = l.rows; rows > 1;) {
+        const int half = (rows + 1) >> 1;
+        __syncthreads();
+        if (l.row >= half && l.row < rows)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e * (T / 2) + (l.row - half) * l.words + l.word] = v[e];
+        __syncthreads();
+        if (l.row + half < rows)
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] += s[e * (T / 2) + l.row * l.words + l.word];
+        rows = half;
+    }
+    __syncthreads();
+}
+
 // Floats of dynamic LDS: sum_rows of 2 W values, or two values a channel.
-inline size_t lds_floats(int c) { return std::max<size_t>((size_t)2 * W * kGroupThreads / 2, (size_t)2 * c); }
+template <int T>
+size_t sum_floats(int c) { return std::max<size_t>((size_t)W * T, (size_t)2 * c); }
 
 // ---- forward -------------------------------------------------------------------------
 
-// A piece's mean and sum of squared deviations, each group.
-template <int DT, bool A>
-__global__ __launch_bounds__(kGroupThreads) void k_group_sums(GroupArgs a) {
-    extern __shared__ float s[];
-    const int number = (int)blockIdx.x;
-    const Piece p = piece_of(a, number);
-    if (!is_sample(a, p) || p.begin >= p.end) return;
-    const Lay l(a.c);
+// Mean and sum of squared deviations of each group over a piece's rows, into out [groups][2] (memory or LDS).
+template <int DT, bool A, int T>
+__device__ __forceinline__ void piece_sums(const GroupArgs& a, const Piece& p, const Lay<T>& l, float* s, float* out) {
     const int c = l.word * W, left = a.c - c;
     float base[W], sum[2 * W];
 #pragma unroll
@@ -151,20 +158,22 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_sums(GroupArgs a) {
             }
         }
     }
-    sum_rows(sum, l.rows, l.words, l.row, l.word, s);
+    sum_rows<T>(sum, l, s);
     const float rows = (float)(p.end - p.begin);
+    float* const s_squares = s + a.c;
     if (l.ok && l.row == 0)
 #pragma unroll
         for (int e = 0; e < W; ++e)
             if (e < left) {
                 const float off = sum[e] / rows;
-                s[c + e] = base[e] + off;                               // the channel's mean
-                s[a.c + c + e] = fmaxf(sum[W + e] - sum[e] * off, 0.f); // and squared deviations
+                s[c + e] = base[e] + off;                                           // the channel's mean
+                s_squares[c + e] = fmaxf(sum[W + e] - sum[e] * off, 0.f);           // and squared deviations
             }
     __syncthreads();
     const int per = a.c / a.groups, lane = threadIdx.x & 63;
-    for (int g = threadIdx.x >> 6; g < a.groups; g += kGroupWaves) {
+    for (int g = threadIdx.x >> 6; g < a.groups; g += T / 64) {
         const float* mean_of = s + g * per;
+        const float* squares_of = s_squares + g * per;
         const float first = mean_of[0];
         float m = 0.f;
         for (int k = lane; k < per; k += 64) m += mean_of[k] - first;
@@ -172,25 +181,34 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_sums(GroupArgs a) {
         float m2 = 0.f;
         for (int k = lane; k < per; k += 64) {
             const float d = mean_of[k] - mean;
-            m2 += mean_of[a.c + k] + rows * (d * d);
+            m2 += squares_of[k] + rows * (d * d);
         }
         m2 = lane_sum<64>(m2);
         if (lane == 0) {
-            float* o = a.by_group + ((int64_t)number * a.groups + g) * 2;
-            o[0] = mean;
-            o[1] = m2;
+            out[2 * g] = mean;
+            out[2 * g + 1] = m2;
         }
     }
 }
 
+template <int DT, bool A, int T>
+__global__ __launch_bounds__(T) void k_group_sums(GroupArgs a) {
+    extern __shared__ float s[];
+    const int number = (int)blockIdx.x;
+    const Piece p = piece_of(a, number);
+    if (!is_sample(a, p) || p.begin >= p.end) return;
+    piece_sums<DT, A>(a, p, Lay<T>(a.c), s, a.by_group + (int64_t)number * a.groups * 2);
+}
+
 // Mean and rstd of each group of a piece's sample, from its pieces, into s_stats
-// [groups][2]. s: 2 x 1024 floats.
+// [groups][2]. s: 2 T floats.
+template <int T>
 __device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float* s_stats) {
     const int first = first_piece(a, p), count = p.run_end > p.run_begin ? last_piece(a, p) - first + 1 : 0;
-    const int per = a.c / a.groups;
-    for (int g0 = 0; g0 < a.groups; g0 += kGroupThreads) {
-        const int wide = min(a.groups - g0, kGroupThreads);
-        const int parts = kGroupThreads / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
+    const int per = a.c / a.groups, cuts = multiples(a, p.run_begin);
+    for (int g0 = 0; g0 < a.groups; g0 += T) {
+        const int wide = min(a.groups - g0, T);
+        const int parts = T / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
         const bool ok = part < parts && count > 0;
         float v[2] = {0.f, 0.f};
         float base = 0.f;
@@ -200,8 +218,8 @@ __device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float*
 #pragma unroll 4
             for (int k = part; k < count; k += parts) {
                 // rows of the piece: the run's, from one multiple to the next
-                const int64_t cut = (int64_t)((p.run_begin >> a.rows_log) + k) << a.rows_log;
-                const float rows = (float)(min((int64_t)p.run_end, cut + ((int64_t)1 << a.rows_log)) -
+                const int64_t cut = (int64_t)(cuts + k) * a.rows_each;
+                const float rows = (float)(min((int64_t)p.run_end, cut + a.rows_each) -
                                            max((int64_t)p.run_begin, cut));
                 const float d = from[(int64_t)k * a.groups * 2] - base;
                 v[0] += rows * d;
@@ -214,12 +232,12 @@ __device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float*
             __syncthreads();
             if (part >= half && part < rows) {
                 s[(part - half) * wide + g] = v[0];
-                s[kGroupThreads + (part - half) * wide + g] = v[1];
+                s[T + (part - half) * wide + g] = v[1];
             }
             __syncthreads();
             if (part + half < rows) {
                 v[0] += s[part * wide + g];
-                v[1] += s[kGroupThreads + part * wide + g];
+                v[1] += s[T + part * wide + g];
             }
             rows = half;
         }
@@ -237,8 +255,8 @@ __device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float*
     }
 }
 
-template <int DT, bool A, int ACT>
-__device__ __forceinline__ void write_rows(const GroupArgs& a, const Piece& p, const Lay& l, const float* s_stats) {
+template <int DT, bool A, int ACT, int T>
+__device__ __forceinline__ void write_rows(const GroupArgs& a, const Piece& p, const Lay<T>& l, const float* s_stats) {
     if (!l.ok) return;
     const int c = l.word * W, left = a.c - c, per = a.c / a.groups;
     float mean[W], scale[W], shift[W];
@@ -260,28 +278,57 @@ __device__ __forceinline__ void write_rows(const GroupArgs& a, const Piece& p, c
     }
 }
 
-template <int DT, bool A>
-__device__ __forceinline__ void write_zeros(const GroupArgs& a, const Piece& p, const Lay& l) {
+template <int DT, bool A, int T>
+__device__ __forceinline__ void write_zeros(const GroupArgs& a, const Piece& p, const Lay<T>& l) {
     if (!l.ok) return;
     const float v[W] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int r = p.begin + l.row; r < p.end; r += l.rows)
         store_16<DT, A>(a.y, (int64_t)r * a.ldy + l.word * W, a.c - l.word * W, v);
 }
 
-template <int DT, bool A>
-__global__ __launch_bounds__(kGroupThreads) void k_group_write(GroupArgs a) {
+template <int DT, bool A, int T>
+__global__ __launch_bounds__(T) void k_group_write(GroupArgs a) {
     extern __shared__ float s[];
     const int number = (int)blockIdx.x;
     const Piece p = piece_of(a, number);
-    const Lay l(a.c);
-    if (!is_sample(a, p)) return write_zeros<DT, A>(a, p, l);
-    float* const s_stats = s + 2 * kGroupThreads;
-    join_pieces(a, p, s, s_stats);
+    const Lay<T> l(a.c);
+    if (!is_sample(a, p)) return write_zeros<DT, A, T>(a, p, l);
+    float* const s_stats = s + 2 * T;
+    join_pieces<T>(a, p, s, s_stats);
     if (a.stats && number == first_piece(a, p)) {
         float* o = a.stats + (int64_t)(a.offsets ? p.run - 1 : 0) * a.groups * 2;
-        for (int i = threadIdx.x; i < 2 * a.groups; i += kGroupThreads) o[i] = s_stats[i];
+        for (int i = threadIdx.x; i < 2 * a.groups; i += T) o[i] = s_stats[i];
     }
-    with_act(a.act, [&](auto act) SMC_INLINE { write_rows<DT, A, decltype(act)::value>(a, p, l, s_stats); });
+    with_act(a.act, [&](auto act) SMC_INLINE { write_rows<DT, A, decltype(act)::value, T>(a, p, l, s_stats); });
+}
+
+// The whole of a small norm: a block for each run.
+template <int DT, bool A, int T>
+__global__ __launch_bounds__(T) void k_group_whole(GroupArgs a) {
+    extern __shared__ float s[];
+    Piece p;
+    p.run = a.offsets ? (int)blockIdx.x : 1;
+    p.begin = p.run_begin = a.offsets ? run_start(a, p.run) : 0;
+    p.end = p.run_end = a.offsets ? max(p.begin, run_start(a, p.run + 1)) : (int)a.n;
+    const Lay<T> l(a.c);
+    if (!is_sample(a, p)) return write_zeros<DT, A, T>(a, p, l);
+    float* const s_stats = s + max(W * T, 2 * a.c);
+    if (p.begin < p.end) piece_sums<DT, A>(a, p, l, s, s_stats);
+    __syncthreads();
+    const float n = (float)(p.end - p.begin) * (float)(a.c / a.groups);
+    for (int g = threadIdx.x; g < a.groups; g += T) {
+        const float mean = p.begin < p.end ? s_stats[2 * g] : 0.f;
+        const float rstd = p.begin < p.end ? inverse_root(s_stats[2 * g + 1] / n + a.eps) : 0.f;
+        s_stats[2 * g] = mean;
+        s_stats[2 * g + 1] = rstd;
+        if (a.stats) {
+            float* o = a.stats + ((int64_t)(p.run - 1) * a.groups + g) * 2;
+            o[0] = mean;
+            o[1] = rstd;
+        }
+    }
+    __syncthreads();
+    with_act(a.act, [&](auto act) SMC_INLINE { write_rows<DT, A, decltype(act)::value, T>(a, p, l, s_stats); });
 }
 
 // ---- backward ----------------------------------------------------------------------
@@ -314,8 +361,8 @@ __device__ __forceinline__ void slope_of(float v, float dy, const Channels& ch, 
 }
 
 // A piece's sums of dz and dz x_hat, each channel; and of a and a x_hat, each group.
-template <int DT, bool A, int ACT>
-__device__ __forceinline__ void gradient_sums(const GroupArgs& a, const Piece& p, const Lay& l, float (&sum)[2 * W]) {
+template <int DT, bool A, int ACT, int T>
+__device__ __forceinline__ void gradient_sums(const GroupArgs& a, const Piece& p, const Lay<T>& l, float (&sum)[2 * W]) {
     const int c = l.word * W, left = a.c - c;
     Channels ch;
     ch.load<DT, A>(a, p, c, left);
@@ -334,19 +381,19 @@ __device__ __forceinline__ void gradient_sums(const GroupArgs& a, const Piece& p
     }
 }
 
-template <int DT, bool A>
-__global__ __launch_bounds__(kGroupThreads) void k_group_gradient_sums(GroupArgs a) {
+template <int DT, bool A, int T>
+__global__ __launch_bounds__(T) void k_group_gradient_sums(GroupArgs a) {
     extern __shared__ float s[];
     const int number = (int)blockIdx.x;
     const Piece p = piece_of(a, number);
-    const Lay l(a.c);
+    const Lay<T> l(a.c);
     const int c = l.word * W, left = a.c - c;
     float sum[2 * W];
 #pragma unroll
     for (int e = 0; e < 2 * W; ++e) sum[e] = 0.f;
     if (l.ok && is_sample(a, p) && p.begin < p.end)
-        with_act(a.act, [&](auto act) SMC_INLINE { gradient_sums<DT, A, decltype(act)::value>(a, p, l, sum); });
-    sum_rows(sum, l.rows, l.words, l.row, l.word, s);
+        with_act(a.act, [&](auto act) SMC_INLINE { gradient_sums<DT, A, decltype(act)::value, T>(a, p, l, sum); });
+    sum_rows<T>(sum, l, s);
     if (l.ok && l.row == 0)
 #pragma unroll
         for (int e = 0; e < W; ++e)
@@ -356,9 +403,9 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_gradient_sums(GroupArgs
             }
     __syncthreads();
     float* o = a.by_channel + (int64_t)number * 2 * a.c;
-    for (int i = threadIdx.x; i < 2 * a.c; i += kGroupThreads) o[i] = s[i];
+    for (int i = threadIdx.x; i < 2 * a.c; i += T) o[i] = s[i];
     const int per = a.c / a.groups, lane = threadIdx.x & 63;
-    for (int g = threadIdx.x >> 6; g < a.groups; g += kGroupWaves) {
+    for (int g = threadIdx.x >> 6; g < a.groups; g += T / 64) {
         float m1 = 0.f, m2 = 0.f;
         for (int k = lane; k < per; k += 64) {
             const float w = to_f32<DT>(static_cast<const uint16_t*>(a.weight)[g * per + k]);
@@ -375,11 +422,12 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_gradient_sums(GroupArgs
 }
 
 // The means of a and a x_hat over a piece's sample, each group.
+template <int T>
 __device__ void join_gradient_pieces(const GroupArgs& a, const Piece& p, float* s, float* s_means) {
     const int first = first_piece(a, p), count = p.run_end > p.run_begin ? last_piece(a, p) - first + 1 : 0;
-    for (int g0 = 0; g0 < a.groups; g0 += kGroupThreads) {
-        const int wide = min(a.groups - g0, kGroupThreads);
-        const int parts = kGroupThreads / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
+    for (int g0 = 0; g0 < a.groups; g0 += T) {
+        const int wide = min(a.groups - g0, T);
+        const int parts = T / wide, part = threadIdx.x / wide, g = threadIdx.x - part * wide;
         float v[2] = {0.f, 0.f};
         if (part < parts) {
             const float* from = a.by_group + ((int64_t)first * a.groups + g0 + g) * 2;
@@ -395,12 +443,12 @@ __device__ void join_gradient_pieces(const GroupArgs& a, const Piece& p, float* 
             __syncthreads();
             if (part >= half && part < rows) {
                 s[(part - half) * wide + g] = v[0];
-                s[kGroupThreads + (part - half) * wide + g] = v[1];
+                s[T + (part - half) * wide + g] = v[1];
             }
             __syncthreads();
             if (part + half < rows) {
                 v[0] += s[part * wide + g];
-                v[1] += s[kGroupThreads + part * wide + g];
+                v[1] += s[T + part * wide + g];
             }
             rows = half;
         }
@@ -413,8 +461,8 @@ __device__ void join_gradient_pieces(const GroupArgs& a, const Piece& p, float* 
     }
 }
 
-template <int DT, bool A, int ACT>
-__device__ __forceinline__ void gradient_rows(const GroupArgs& a, const Piece& p, const Lay& l, const float* s_means) {
+template <int DT, bool A, int ACT, int T>
+__device__ __forceinline__ void gradient_rows(const GroupArgs& a, const Piece& p, const Lay<T>& l, const float* s_means) {
 #pragma clang fp contract(off)
     if (!l.ok) return;
     const int c = l.word * W, left = a.c - c, per = a.c / a.groups;
@@ -442,8 +490,8 @@ __device__ __forceinline__ void gradient_rows(const GroupArgs& a, const Piece& p
     }
 }
 
-// dw and db of 8 channels: every piece's sums, in 64 strided runs joined by a tree.
-template <int DT>
+// dw and db of 8 channels: every piece's sums, in T / 16 strided runs joined by a tree.
+template <int DT, int T>
 __device__ __forceinline__ void sum_channels(const GroupArgs& a, int block, float* s) {
     const int x = threadIdx.x & 15, run = threadIdx.x >> 4;        // 8 channels of db, then of dw
     const int c = block * 8 + (x & 7);
@@ -451,11 +499,11 @@ __device__ __forceinline__ void sum_channels(const GroupArgs& a, int block, floa
     if (c < a.c) {
         const float* from = a.by_channel + (x >> 3) * a.c + c;
 #pragma unroll 8
-        for (int k = run; k < a.pieces; k += 64) v += from[(int64_t)k * 2 * a.c];
+        for (int k = run; k < a.pieces; k += T / 16) v += from[(int64_t)k * 2 * a.c];
     }
     s[run * 17 + x] = v;
     __syncthreads();
-    for (int o = 32; o > 0; o >>= 1) {
+    for (int o = T / 32; o > 0; o >>= 1) {
         if (run < o) s[run * 17 + x] += s[(run + o) * 17 + x];
         __syncthreads();
     }
@@ -463,56 +511,72 @@ __device__ __forceinline__ void sum_channels(const GroupArgs& a, int block, floa
 }
 
 // dx of a piece; the blocks after the pieces' add up dw and db.
-template <int DT, bool A>
-__global__ __launch_bounds__(kGroupThreads) void k_group_gradient_write(GroupArgs a) {
+template <int DT, bool A, int T>
+__global__ __launch_bounds__(T) void k_group_gradient_write(GroupArgs a) {
     extern __shared__ float s[];
     const int number = (int)blockIdx.x;
-    if (number >= a.pieces) return sum_channels<DT>(a, number - a.pieces, s);
+    if (number >= a.pieces) return sum_channels<DT, T>(a, number - a.pieces, s);
     const Piece p = piece_of(a, number);
-    const Lay l(a.c);
-    if (!is_sample(a, p)) return write_zeros<DT, A>(a, p, l);
+    const Lay<T> l(a.c);
+    if (!is_sample(a, p)) return write_zeros<DT, A, T>(a, p, l);
     if (p.begin >= p.end) return;
-    float* const s_means = s + 2 * kGroupThreads;
-    join_gradient_pieces(a, p, s, s_means);
-    with_act(a.act, [&](auto act) SMC_INLINE { gradient_rows<DT, A, decltype(act)::value>(a, p, l, s_means); });
+    float* const s_means = s + 2 * T;
+    join_gradient_pieces<T>(a, p, s, s_means);
+    with_act(a.act, [&](auto act) SMC_INLINE { gradient_rows<DT, A, decltype(act)::value, T>(a, p, l, s_means); });
 }
 
-template <int DT, bool A>
-hipError_t group_norm_t(const GroupArgs& a, hipStream_t s) {
-    launch(k_group_sums<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), lds_floats(a.c) * 4, s, a);
-    launch(k_group_write<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), (2 * kGroupThreads + 2 * (size_t)a.groups) * 4, s, a);
-    return hipGetLastError();
+template <int DT, bool A, int T>
+void group_norm_t(const GroupArgs& a, hipStream_t s) {
+    if (a.whole)
+        return launch(k_group_whole<DT, A, T>, dim3((unsigned)(a.offsets ? a.samples + 2 : 1)), dim3(T),
+                      (sum_floats<T>(a.c) + 2 * (size_t)a.groups) * 4, s, a);
+    launch(k_group_sums<DT, A, T>, dim3((unsigned)a.pieces), dim3(T), sum_floats<T>(a.c) * 4, s, a);
+    launch(k_group_write<DT, A, T>, dim3((unsigned)a.pieces), dim3(T), (2 * T + 2 * (size_t)a.groups) * 4, s, a);
 }
 
-template <int DT, bool A>
-hipError_t group_norm_backward_t(const GroupArgs& a, hipStream_t s) {
-    launch(k_group_gradient_sums<DT, A>, dim3((unsigned)a.pieces), dim3(kGroupThreads), lds_floats(a.c) * 4, s, a);
-    launch(k_group_gradient_write<DT, A>, dim3((unsigned)(a.pieces + (a.c + 7) / 8)), dim3(kGroupThreads),
-           (2 * kGroupThreads + 2 * (size_t)a.groups) * 4, s, a);
+template <int DT, bool A, int T>
+void group_norm_backward_t(const GroupArgs& a, hipStream_t s) {
+    launch(k_group_gradient_sums<DT, A, T>, dim3((unsigned)a.pieces), dim3(T), sum_floats<T>(a.c) * 4, s, a);
+    launch(k_group_gradient_write<DT, A, T>, dim3((unsigned)(a.pieces + (a.c + 7) / 8)), dim3(T),
+           (2 * T + 2 * (size_t)a.groups) * 4, s, a);
+}
+
+template <int DT>
+hipError_t group_norm_of(const GroupArgs& a, bool backward, hipStream_t s) {
+    const bool wide = a.c > kThreads * W;
+#define SMC_GO(A, T) backward ? group_norm_backward_t<DT, A, T>(a, s) : group_norm_t<DT, A, T>(a, s)
+    if (a.vec) wide ? (SMC_GO(true, kThreadsWide)) : (SMC_GO(true, kThreads));
+    else wide ? (SMC_GO(false, kThreadsWide)) : (SMC_GO(false, kThreads));
+#undef SMC_GO
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Rows of a piece: one piece a CU, but no fewer than give each thread 4 words.
+// Rows of a piece: two pieces a compute unit, but no fewer rows than give each thread 4 words. (One
+// or four pieces a compute unit: 40,000 x 512 in four samples 32.3 or 30.3 us for 28.2, its backward
+// 64.1 or 53.4 for 47.0; 91,000 x 128 in one sample 21.3 or 25.3 for 22.1.) Whole steps of a
+// block: 91,000 x 128 in six samples 22.1 us for 25.0.
+//
+// One launch up to 4 words a thread: a single row 10.0 us a call for 12.7; the rows of 64 words a
+// thread would take 24 for 12.5, one block's loads waiting for each other.
 void group_plan(GroupArgs& a) {
-    const int64_t words = (a.c + W - 1) / W;
-    const int64_t rows = std::max<int64_t>((a.n + device_cus() - 1) / device_cus(), 4 * kGroupThreads / words);
-    a.rows_log = 0;
-    while (((int64_t)1 << a.rows_log) < rows) ++a.rows_log;
-    a.pieces = (int)((a.n + ((int64_t)1 << a.rows_log) - 1) >> a.rows_log);
+    const int64_t words = (a.c + W - 1) / W, blocks = 2 * (int64_t)device_cus();
+    a.rows_each = (int)std::max<int64_t>((a.n + blocks - 1) / blocks, std::max<int64_t>(1, 4 * kThreads / words));
+    const int64_t step = std::max<int64_t>(1, kThreads / words);
+    a.rows_each = (int)((a.rows_each + step - 1) / step * step);
+    a.pieces = (int)((a.n + a.rows_each - 1) / a.rows_each);
     if (a.offsets) a.pieces += a.samples + 2;
     a.pieces = std::max(a.pieces, 1);
+    a.whole = a.n * words <= (int64_t)4 * kThreads;
 }
 
 hipError_t launch_group_norm(const GroupArgs& a, int dt, hipStream_t s) {
-    if (dt == kF16) return a.vec ? group_norm_t<kF16, true>(a, s) : group_norm_t<kF16, false>(a, s);
-    return a.vec ? group_norm_t<kBF16, true>(a, s) : group_norm_t<kBF16, false>(a, s);
+    return dt == kF16 ? group_norm_of<kF16>(a, false, s) : group_norm_of<kBF16>(a, false, s);
 }
 
 hipError_t launch_group_norm_backward(const GroupArgs& a, int dt, hipStream_t s) {
-    if (dt == kF16) return a.vec ? group_norm_backward_t<kF16, true>(a, s) : group_norm_backward_t<kF16, false>(a, s);
-    return a.vec ? group_norm_backward_t<kBF16, true>(a, s) : group_norm_backward_t<kBF16, false>(a, s);
+    return dt == kF16 ? group_norm_of<kF16>(a, true, s) : group_norm_of<kBF16>(a, true, s);
 }
 
 }  // namespace smc

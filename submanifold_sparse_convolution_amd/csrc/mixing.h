@@ -26,8 +26,9 @@ struct GroupArgs {
     void* dweight = nullptr;
     void* dbias = nullptr;
     // by group_plan
-    int rows_log = 0;               // rows of a piece (log2)
-    int pieces = 0;                 // see k_group_sums
+    int rows_each = 1;              // rows of a piece
+    int pieces = 0;                 // see Piece
+    bool whole = false;             // forward: one launch
     float* by_group = nullptr;      // [pieces][groups][2]
     float* by_channel = nullptr;    // backward: [pieces][2][c]
     int vec = 0;                    // 16-byte loads and stores are possible
@@ -35,7 +36,7 @@ struct GroupArgs {
 constexpr int kMaxGroupChannels = 8192;         // a block's threads hold a row
 constexpr int kMaxGroupsOfNorm = 4096;         // their statistics lie in LDS
 constexpr int kMaxSamples = 1 << 16;
-void group_plan(GroupArgs& a);                  // rows_log and pieces, from n, c, samples and offsets
+void group_plan(GroupArgs& a);                  // rows_each and pieces, from n, c, samples and offsets
 hipError_t launch_group_norm(const GroupArgs& a, int dt, hipStream_t s);
 hipError_t launch_group_norm_backward(const GroupArgs& a, int dt, hipStream_t s);
 

@@ -9,14 +9,23 @@ namespace {
 
 constexpr int W = 8;        // elements of a word
 
-// A word of a row as float32: elements i .. i + 7, of which `left` exist (all of
-// them where ALIGNED, which also means that the address is a multiple of 16).
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void load_f32(const void* p, int64_t i, int left, float (&v)[W]) {
+// A word of a row: elements i .. i + 7, of which `left` exist (all of them where
+// ALIGNED, which also means that the address is a multiple of 16).
+template <bool ALIGNED>
+__device__ __forceinline__ u32x4 load_word(const void* p, int64_t i, int left) {
     const uint16_t* e0 = static_cast<const uint16_t*>(p) + i;
-    const u32x4 u = ALIGNED ? *reinterpret_cast<const u32x4*>(e0) : left >= W ? load_unaligned(e0) : load_tail(e0, left);
+    return ALIGNED ? *reinterpret_cast<const u32x4*>(e0) : left >= W ? load_unaligned(e0) : load_tail(e0, left);
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(u32x4 u, float (&v)[W]) {
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] = to_f32<DT>((u[e >> 1] >> ((e & 1) * 16)) & 0xffffu);
+}
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void load_f32(const void* p, int64_t i, int left, float (&v)[W]) {
+    unpack<DT>(load_word<ALIGNED>(p, i, left), v);
 }
 
 template <int DT, bool ALIGNED>
