@@ -733,9 +733,10 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  *   bias_ij = sum over the axes of bias[axis][reach + clamp(c_i - c_j, -reach, reach)][h]
  * with c the rows' cells. Head h reads head h / (heads / kv_heads) of k and v. Rows of no
  * window come out as zeros, and so does a row whose scores are all -inf. Windows do not
- * reach each other, also where values are not finite. Infinite entries of bias count as the
- * type's largest values; a NaN in it reaches every row of its head that lies at that
- * distance from a cell of the window's extent.
+ * reach each other, also where values are not finite. Entries of bias count as at most 2^14
+ * in size, infinities too (a mask; a row that it leaves nothing weighs the keys whose masks
+ * are alike by the rest of their scores, as far as float32 holds that beside them); a NaN in it
+ * reaches every row of its head that lies at that distance from a cell of the window's extent.
  * lse (or NULL): log sum_j exp(s_ij), float32 [heads, n] by place (not by row), -inf for
  * zeros' rows; the backward pass reads it. Scores, softmax and sums are float32; P is
  * rounded to dtype for its product with v. out may not overlap q, k or v.
@@ -745,7 +746,7 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  *   delta_i = dout_i . out_i,  dS = P (dout v^T - delta),  dq = scale dS k,
  *   dk = scale dS^T q,  dv = P^T dout (sums over the heads that share them),
  *   dbias[axis][b][h] = sum of dS over the pairs of the bucket, all windows and rows.
- * P and dS are rounded to dtype as operands of products (f16: dS times a power of two found
+ * P and dS are rounded to dtype as operands of products, but not for dbias (f16: dS times a power of two found
  * on the device, so that finite gradients that fit f16 come out finite). Gradients of rows
  * of no window are zeros. dq, dk and dv may be columns of one buffer; they may not overlap
  * an input or each other. workspace: smc_window_attention_backward_workspace(args) bytes,

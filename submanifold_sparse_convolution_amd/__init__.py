@@ -900,8 +900,9 @@ class Windows:
     [windows + 1] CUDA tensor); places of no window may be left at both ends. For a
     relative position bias: coords, the rows' int32 [N, 4] (b, x, y, z) or [N, 3]
     coordinates, and extent, how many cells a window spans along x, y and z at most (each
-    rounded up to a multiple of 4, 128 in all). SmconvError where a row is listed twice, an offset or row is out of range or
-    a window is larger than that."""
+    rounded up to a multiple of 4, 128 in all). SmconvError where a row is listed twice, an
+    offset or row is out of range or a window is larger than that. The tensors are not read
+    again; the object has to outlive the calls that it is used in on other streams."""
 
     def __init__(self, offsets, n: int, order=None, coords=None, extent=None, stream=None):
         import torch

@@ -14,8 +14,10 @@
 // at x_j; the axes' cells lie side by side in the contraction, each axis at a multiple of 4. Table entries are exact in
 // the rows' type, so the sum is float32's. The gradient of B is dS E, by the same tiles.
 // (Looking entries up costs three LDS reads and nine vector operations a score, more than
-// the rest of the softmax.) Infinities would make 0 x inf: they count as the type's
-// largest values, whose exponentials are the same.
+// the rest of the softmax.) Entries count as at most 2^14 in size: infinities
+// would make 0 x inf, and where a mask of such entries leaves a row nothing, log sum exp of
+// far larger scores would lose the sum, and the gradients' probabilities with it (at 3 2^14 a
+// float's step is 2^-8). Scores below the largest by that much have no share either way.
 #pragma once
 
 #include <algorithm>
@@ -117,12 +119,13 @@ struct TableLoads {
         }
     }
     __device__ __forceinline__ void commit(const AttentionArgs& a, uint16_t* s_table) const {
-        const uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80;
+        const uint16_t inf = DT == kF16 ? 0x7c00 : 0x7f80, most = DT == kF16 ? 0x7400 : 0x4680;    // 2^14
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             const int i = k * THREADS + threadIdx.x;
             if (i >= 2 * EXT) continue;
-            const uint16_t e = (v[k] & 0x7fff) == inf ? v[k] - 1 : v[k];
+            const uint16_t size = v[k] & 0x7fff;
+            const uint16_t e = size > most && size <= inf ? (v[k] & 0x8000) | most : v[k];
             s_table[i] = e;
             s_table[kTableEntries<EXT> + i + 1] = e;
         }

@@ -10,13 +10,16 @@
 // dB = dS E comes out as sums over the cells of a key for each query; a block adds
 // them up by distance and writes its buckets, k_table_sum adds the blocks.
 //
-// P and dS are rounded to the rows' type as operands (half an ulp of each term). dS follows
+// P and dS are rounded to the rows' type as operands (half an ulp of each term). Not so for the
+// table's gradient, whose sums over all windows cancel: it takes what the rounding leaves of dS as
+// a second operand (without it up to 1.6 times float32's error; 15,000 x 512 in windows of 1,024
+// 236 us for 226, 91,000 rows in 2,905 windows 180.4 for 179.8). dS follows
 // the gradient's size, which in f16 may leave the type's range where dq and dk do not,
 // so in f16 it is taken times a power of two: |dP - delta| <= 2 dim max |dout| max |v| over
 // the window (finite values), brought to [2^14, 2^15]; k_attention_range finds the maxima.
 // delta is taken from out, which was rounded: an error of half an ulp of each out term, over the
-// window's mean of k on its way into dq. Where a window's keys fit one tile delta is the sum of P dP
-// itself instead (long windows average the error away; blocks of 128 queries have no registers for it).
+// window's mean of k on its way into dq. Where a window's keys fit one tile delta is the mean of dP
+// under P itself instead (long windows average the error away; blocks of 128 queries have no registers for it).
 #pragma once
 
 #include "attention.h"
@@ -194,14 +197,19 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[u][e] = exp2_of(s[u][e] * to_log2 - base[u]);
         };
-        auto slope = [&](const f32x4& p, const f32x4& dp, int u, u32x4& g, int b) SMC_INLINE {
+        // dS, and with a table what its rounding leaves
+        auto slope = [&](const f32x4& p, const f32x4& dp, int u, u32x4& g, u32x4& rest, int b) SMC_INLINE {
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = p[e] * fmaf(dp[e], keep, -(delta[u] * keep));
-            g[2 * (b & 1)] = pack2<DT>(v[0], v[1]);
-            g[2 * (b & 1) + 1] = pack2<DT>(v[2], v[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w = pack2<DT>(v[2 * i], v[2 * i + 1]);
+                g[2 * (b & 1) + i] = w;
+                if (EXT) rest[2 * (b & 1) + i] = pack2<DT>(v[2 * i] - to_f32<DT>(w & 0xffffu), v[2 * i + 1] - to_f32<DT>(w >> 16));
+            }
         };
-        auto products = [&](int h, const u32x4 (&g)[NQ]) SMC_INLINE {
+        auto products = [&](int h, const u32x4 (&g)[NQ], const u32x4 (&rest)[NQ]) SMC_INLINE {
 #pragma unroll
             for (int d = 0; d < DT16; ++d) {
                 const u32x4 f = at.across(s_k, d, 32 * h);
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
                 for (int d = 0; d < ET16; ++d) {
                     const u32x4 f = at_cells.across(s_e, d, 32 * h);
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u) db[u][d] = mfma16<DT>(f, g[u], db[u][d]);
+                    for (int u = 0; u < NQ; ++u) db[u][d] = mfma16<DT>(f, g[u], mfma16<DT>(f, rest[u], db[u][d]));
                 }
         };
         if constexpr (kOwnDelta) {
@@ -230,36 +238,40 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
             if (one)
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) {
-                    float v = 0.f;
+                    float v = 0.f, total = 0.f;         // (over the sum of P: lse of large scores has few digits)
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v += s[b][u][e] * dp[b][u][e];
-                    delta[u] = quad_sum(v);
+                        for (int e = 0; e < 4; ++e) {
+                            v += s[b][u][e] * dp[b][u][e];
+                            total += s[b][u][e];
+                        }
+                    total = quad_sum(total);
+                    delta[u] = total == 0.f ? 0.f : quad_sum(v) / total;
                 }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (B::kSkips && 32 * h >= left) continue;
-                u32x4 g[NQ];
+                u32x4 g[NQ], rest[NQ];
 #pragma unroll
                 for (int u = 0; u < NQ; ++u)
 #pragma unroll
-                    for (int b = 2 * h; b < 2 * h + 2; ++b) slope(s[b][u], dp[b][u], u, g[u], b);
-                products(h, g);
+                    for (int b = 2 * h; b < 2 * h + 2; ++b) slope(s[b][u], dp[b][u], u, g[u], rest[u], b);
+                products(h, g, rest);
             }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {           // 32 keys at a time
                 if (B::kSkips && 32 * h >= left) continue;
-                u32x4 g[NQ];
+                u32x4 g[NQ], rest[NQ];
 #pragma unroll
                 for (int b = 2 * h; b < 2 * h + 2; ++b) {
                     f32x4 s[NQ], dp[NQ];
                     pair(b, s, dp);
 #pragma unroll
-                    for (int u = 0; u < NQ; ++u) slope(s[u], dp[u], u, g[u], b);
+                    for (int u = 0; u < NQ; ++u) slope(s[u], dp[u], u, g[u], rest[u], b);
                 }
-                products(h, g);
+                products(h, g, rest);
             }
         }
     };

@@ -1,9 +1,9 @@
 // Window attention, forward: out_i = sum over the window's keys j of P_ij v_j, P the softmax of
 // s_ij = scale q_i k_j + bias_ij, and lse_i = log sum_j exp(s_ij).
 //
-// A block takes a tile of one window's queries and one head; it walks the window's keys 64
-// at a time, keys and values through LDS with the next 64 on their way in registers, and
-// keeps the running maximum and sum of the softmax.
+// A block takes a tile of one window's queries and a head, or two after each other; it walks
+// the window's keys 64 at a time, keys and values through LDS with the next 64 on their way in
+// registers, and keeps the running maximum and sum of the softmax.
 // P is at most 1 and is rounded to the rows' type for its product with v (half an
 // ulp of each term, beside half an ulp of the sum); the sum of P is taken before
 // the rounding.
@@ -66,9 +66,9 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
             if (EXT) table_words<EXT>(a, s_table[head - first_head], own[u].cells, q, fb[u]);
         }
     };
-    // A step's 16 KB keys from 16 b0 on, of which `left` are the window's: scores, then softmax and out
+    // The scores of a step's 16 KB keys from 16 b0 on
     constexpr int KB = B::kHalves ? 2 : 4;
-    auto scores = [&](f32x4 (&s)[KB][NQ], int b0, int left, const char* s_k, const char* s_e) SMC_INLINE {
+    auto scores = [&](f32x4 (&s)[KB][NQ], int b0, const char* s_k, const char* s_e) SMC_INLINE {
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
 #pragma unroll
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
     };
     auto step = [&](int b0, int left, const char* s_k, const char* s_v, const char* s_e) SMC_INLINE {
         f32x4 s[KB][NQ];
-        scores(s, b0, left, s_k, s_e);
+        scores(s, b0, s_k, s_e);
         if (left < 16 * KB) cut(s, left);
         maxima(s);
         products(s, b0, s_v);

@@ -227,6 +227,8 @@ bool attention_words(const smc_attention_t* a, bool backward) {
                           words16(a->dv, a->ld_dv)));
 }
 
+bool short_windows(const smc_windows_t* w) { return w->windows > 0 && w->n / w->windows < 40; }
+
 // Blocks by the windows' lengths: short where they are short on average, long where the rows are mostly in
 // long ones (pairs / rows) and there are blocks for the device. Forward / backward in us, short, mid and long:
 //   40,000 rows x 4 heads of 32, cells, windows of 24   13.8, 17.0, 29.4 / 61.4, 79.9, 114.5
@@ -242,7 +244,7 @@ bool attention_words(const smc_attention_t* a, bool backward) {
 int window_lengths(const smc_attention_t* a, bool backward) {
     const smc_windows_t* w = a->windows;
     if (!attention_words(a, backward) || w->windows < 1) return kMidWindows;
-    if (w->n / w->windows < 40) return kShortWindows;
+    if (short_windows(w)) return kShortWindows;
     return w->pairs / w->n < 96 || (int64_t)w->tiles128 * a->heads < device_cus() ? kMidWindows : kLongWindows;
 }
 
@@ -293,13 +295,14 @@ int attention(const smc_attention_t* a, void* stream) {
                       "smc_window_attention");
 }
 
-// Scratch of a backward pass: delta, the blocks' buckets, and f16's maxima.
+// Scratch of a backward pass: delta, the blocks' buckets, and f16's maxima. For the more tiles of those that
+// window_lengths may choose, whatever the alignment.
 struct AttentionScratch {
     size_t delta = 0, part = 0, range = 0, bytes = 0;       // offsets
     explicit AttentionScratch(const smc_attention_t* a) {
         const smc_windows_t* w = a->windows;
         part = round_up((size_t)a->heads * w->n * 4);
-        const int64_t tiles = tiles_of(w, window_lengths(a, true));
+        const int64_t tiles = short_windows(w) ? w->tiles32 : w->tiles64;
         range = part + (a->bias ? round_up((size_t)tiles * a->heads * 3 * (2 * a->reach + 1) * 4) : 0);
         bytes = range + (a->dtype == SMC_DTYPE_F16 ? round_up((size_t)w->tiles64 * (a->heads + a->kv_heads) * 4) : 0);
     }

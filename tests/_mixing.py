@@ -21,10 +21,10 @@ U = ro.U
 
 
 def chain(n, c, groups):
-    """Longest chain of additions: 1024 threads a block, 256 blocks."""
+    """Longest chain of additions: 512 threads a block, 512 blocks and one more a sample."""
     words = -(-c // 8)
     a_thread = 2 * max(n * words / 2.0 ** 18, 4) + 2
-    return int(a_thread + 10 + (c // groups) / 64 + 7 + 258 * (groups + 1023) / 1024 + 11) + 8
+    return int(a_thread + 10 + (c // groups) / 64 + 7 + 516 * (groups + 511) / 512 + 11) + 8
 
 
 def runs(offsets, n):
