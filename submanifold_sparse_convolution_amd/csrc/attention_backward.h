@@ -8,12 +8,14 @@
 // NK keys and a head of k and v and walks the queries of that head's group, for dk and dv. Both
 // compute S and dP: 7 products a pair where 5 would do, but dq needs no sum over blocks.
 // dB = dS E comes out as sums over the cells of a key for each query; a block adds
-// them up by distance and writes its buckets, k_table_sum adds the blocks.
+// them up by distance and writes its buckets, k_table_sum adds the blocks. 91,000 rows in 2,905
+// windows: queries 93.6 us, keys 68.3, sums 9.8; 15,000 x 512 in windows of 1,024: 127, 111 and 4.7.
+// (Distances looked up for each entry of dB in place of rows shifted by the query's cell: 107.2 and 134.)
 //
 // P and dS are rounded to the rows' type as operands (half an ulp of each term). Not so for the
 // table's gradient, whose sums over all windows cancel: it takes what the rounding leaves of dS as
 // a second operand (without it up to 1.6 times float32's error; 15,000 x 512 in windows of 1,024
-// 236 us for 226, 91,000 rows in 2,905 windows 180.4 for 179.8). dS follows
+// 236 us for 226 a call, 91,000 rows in 2,905 windows 180.4 for 179.8). dS follows
 // the gradient's size, which in f16 may leave the type's range where dq and dk do not,
 // so in f16 it is taken times a power of two: |dP - delta| <= 2 dim max |dout| max |v| over
 // the window (finite values), brought to [2^14, 2^15]; k_attention_range finds the maxima.
@@ -89,7 +91,7 @@ __device__ __forceinline__ float gradient_scale(const AttentionArgs& a, const Wi
 __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_queries(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, DP <= 32 && EXT <= 32 ? 3 : DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_queries(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16, ET16 = EXT / 16;
     constexpr int NQ = B::kColumns, TH = B::kThreads, kBins = EXT ? EXT / 32 : 1;
     constexpr bool kOwnDelta = B::kRows <= 64;          // (see the top)
@@ -97,7 +99,8 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
     __shared__ __align__(16) typename Keys::Memory s_keys;
     __shared__ __align__(16) uint16_t s_table[B::kHeads][EXT ? 2 * kTableEntries<EXT> : 2];
     // dB of 16 queries a wave (rows 4 floats longer than their cells), then the waves' sums by distance
-    __shared__ __align__(16) float s_db[EXT ? B::kWaves * 16 * (EXT + 4) : 1];
+    constexpr int kRow = 2 * EXT + 5, kRowsOf = EXT <= 32 ? 16 : 8;      // entries by distance, five more for other banks; rows at a time
+    __shared__ __align__(16) float s_db[EXT ? B::kWaves * kRowsOf * kRow : 1];
     int tile, head;
     if (!tile_and_head(a.n_tiles, a.heads, a.heads_each, tile, head)) return;
     const WindowTile t = a.tiles[tile];
@@ -285,41 +288,50 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
                                  own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dq + head * a.dim, a.dim, lane);
         }
         if constexpr (EXT > 0) {
-            // 16 queries at a time: dB to LDS, then each lane adds what lies at its distances (64 a
-            // word of bins, as load_table counts them), query after query
+            // A few queries at a time: a query's dB to a row of LDS at its own distances (as load_table counts the
+            // entries), zeros around it, and the rows added, a lane for each 64th entry
             const Cells cells(a.extent);
-            float* const mine = s_db + wave * 16 * (EXT + 4);
+            float* const mine = s_db + wave * kRowsOf * kRow;
             float bins[kBins];
 #pragma unroll
             for (int i = 0; i < kBins; ++i) bins[i] = 0.f;
             if (active)
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) {
-                    const int rows = min(16, t.count - (wave * NQ + u) * 16);
-                    if (rows <= 0) continue;
-                    __builtin_amdgcn_wave_barrier();
+                    int at[3];          // the entry of element 0
 #pragma unroll
-                    for (int d = 0; d < ET16; ++d) *reinterpret_cast<f32x4*>(mine + col * (EXT + 4) + 16 * d + 4 * q) = db[u][d];
-                    __builtin_amdgcn_wave_barrier();
+                    for (int d = 0; d < 3; ++d)
+                        at[d] = 2 * cells.first[d] + cells.up[d] - (int)((own[u].cells >> (8 * d)) & 255u);
 #pragma unroll
-                    for (int i = 0; i < kBins; ++i) {
-                        const int bin = 64 * i + lane, axis = cells.axis_of_entry(bin), first = cells.pick(cells.first, axis);
-                        const int away = cells.pick(cells.up, axis) - (bin - 2 * first), extent = cells.pick(a.extent, axis);
-                        float v = 0.f;
-                        if (64 * i < 2 * cells.all())
-                            for (int r = 0; r < rows; ++r) {
-                                const uint32_t seen = (uint32_t)__builtin_amdgcn_readlane((int)own[u].cells, r);
-                                const int c = (int)((seen >> (8 * axis)) & 255u) - away;      // the key's cell
-                                const bool in = c >= first && c < first + extent;
-                                const float x = mine[r * (EXT + 4) + (in ? c : 0)];
-                                v += in ? x : 0.f;
+                    for (int half = 0; half < 16 / kRowsOf; ++half) {
+                        if (t.count <= (wave * NQ + u) * 16 + 8 * half) continue;
+                        __builtin_amdgcn_wave_barrier();
+                        // (one set of rows keeps its places from head to head)
+                        if (NQ > 1 || kRowsOf < 16 || head == first_head)
+                            for (int i = lane; i < kRowsOf * kRow; i += 64) mine[i] = 0.f;
+                        __builtin_amdgcn_wave_barrier();
+                        if (col / kRowsOf == half && own[u].row >= 0)
+#pragma unroll
+                            for (int d = 0; d < ET16; ++d) {
+                                const int e = 16 * d + 4 * q;
+                                float* to = mine + (col & (kRowsOf - 1)) * kRow + e;
+                                to += e < cells.first[1] ? at[0] : e < cells.first[2] ? at[1] : at[2];
+                                if (e < cells.all())
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) to[k] = db[u][d][k];
                             }
-                        bins[i] += bin < 2 * cells.all() ? v : 0.f;
+                        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                        for (int i = 0; i < kBins; ++i) {
+                            float v = 0.f;
+#pragma unroll
+                            for (int r = 0; r < kRowsOf; ++r) v += mine[r * kRow + 64 * i + lane];
+                            bins[i] += v;
+                        }
                     }
                 }
             // the waves' sums, then buckets: the outermost ones hold every distance beyond them
-            float* const s_by = s_db;                       // [wave][64 kBins]
-            static_assert(64 * kBins <= 16 * (EXT + 4), "room");
+            __shared__ float s_by[B::kWaves * 64 * kBins];
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kBins; ++i) s_by[(wave * kBins + i) * 64 + lane] = bins[i];
@@ -559,20 +571,23 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
     }
 }
 
-// dtable = the blocks' buckets: 16 buckets a block, 64 strided runs of tiles joined by a tree.
+// dtable = the blocks' buckets: 4 buckets a block, 256 strided runs of tiles joined by a tree.
+// (16 buckets of 64 runs, whose loads are 64 bytes each but 74 after each other: 11.9 us for 9.8 at
+// 4,756 tiles of 4 heads and 69 buckets.)
+constexpr int kBucketsOf = 4, kRunsOf = 1024 / kBucketsOf;
 template <int DT>
 __global__ __launch_bounds__(1024) void k_table_sum(AttentionArgs a) {
-    __shared__ float s[64][17];
-    const int buckets = 3 * (2 * a.reach + 1), x = threadIdx.x & 15, run = threadIdx.x >> 4;
-    const int i = blockIdx.x * 16 + x, head = blockIdx.y;
+    __shared__ float s[kRunsOf][kBucketsOf + 1];
+    const int buckets = 3 * (2 * a.reach + 1), x = threadIdx.x % kBucketsOf, run = threadIdx.x / kBucketsOf;
+    const int i = blockIdx.x * kBucketsOf + x, head = blockIdx.y;
     float v = 0.f;
     if (i < buckets) {
 #pragma unroll 8
-        for (int k = run; k < a.n_tiles; k += 64) v += a.part[((int64_t)k * a.heads + head) * buckets + i];
+        for (int k = run; k < a.n_tiles; k += kRunsOf) v += a.part[((int64_t)k * a.heads + head) * buckets + i];
     }
     s[run][x] = v;
     __syncthreads();
-    for (int o = 32; o > 0; o >>= 1) {
+    for (int o = kRunsOf / 2; o > 0; o >>= 1) {
         if (run < o) s[run][x] += s[run + o][x];
         __syncthreads();
     }
@@ -596,7 +611,7 @@ hipError_t attention_backward_t(const AttentionArgs& a, hipStream_t s) {
                s, b);
     }
     if (EXT)
-        launch(k_table_sum<DT>, dim3((unsigned)((3 * (2 * a.reach + 1) + 15) / 16), (unsigned)a.heads), dim3(1024), 0, s, a);
+        launch(k_table_sum<DT>, dim3((unsigned)((3 * (2 * a.reach + 1) + kBucketsOf - 1) / kBucketsOf), (unsigned)a.heads), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

@@ -240,6 +240,8 @@ bool short_windows(const smc_windows_t* w) { return w->windows > 0 && w->n / w->
 //                                                 100   22.2, 18.7, 18.1 / 62.7, 58.8, 54.7
 //                                                 400   45.5, 34.1, 31.4 / 135.8, 108.1, 97.5
 //   91,000 x 4 of 32, cells, 2,905 windows of 1 .. 160  50.5, 48.9, 67.5 / 172.2, 186.6, 227.4
+// (A few long windows among many short ones stay with short blocks, whose starts cost least: 20,000 windows of a row
+// and 20 of 1,000, 4 heads of 32: short 256 / 726, long 345 / 841; 2,000 of 10 and 40 of 500, 8 of 64: 204 / 579, 253 / 853.)
 // Rows that are no whole 16-byte words have mid blocks only.
 int window_lengths(const smc_attention_t* a, bool backward) {
     const smc_windows_t* w = a->windows;

@@ -38,7 +38,8 @@ BLOCKS = {
     "two long heads": dict(lengths=[200] * 270, heads=8, kv=4, dim=16),
     "two heads and one": dict(lengths=[20, 70, 41] * 160, heads=5, kv=1, dim=16, extent=(4, 4, 4)),
     "two short heads": dict(lengths=[9, 33, 4, 64, 65] * 160, heads=7, kv=7, dim=16, dt=F16, extent=(5, 8, 3), reach=2),
-    "short and one long": dict(lengths=[2] * 300 + [900], heads=2, kv=2, dim=40, extent=(10, 10, 10), reach=5),
+    "short and one of 300": dict(lengths=[2] * 2000 + [300], heads=2, kv=1, dim=32, extent=(10, 4, 10), reach=5),
+    "rows alone and one of 900": dict(lengths=[2] * 300 + [900], heads=2, kv=2, dim=40, extent=(10, 10, 10), reach=5),
 }
 
 
