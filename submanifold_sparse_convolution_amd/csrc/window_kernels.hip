@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void k_windows_cells(WindowArgs a, WindowPlace
 // and their running sum. Offsets out of order are told by the way.
 __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile* tiles32, WindowTile* tiles64,
                                                         WindowTile* tiles128) {
-    __shared__ int s_sum[3][1024];
+    __shared__ long long s_sum[3][1024];        // (offsets out of order could pass 32 bits)
     __shared__ int s_longest, s_bad;
     __shared__ unsigned long long s_pairs;
     if (threadIdx.x == 0) {
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(1024) void k_windows_tiles(WindowArgs a, WindowTile
         }
         __syncthreads();
         for (int o = 1; o < 1024; o <<= 1) {
-            int before[3] = {0, 0, 0};
+            long long before[3] = {0, 0, 0};
             if (threadIdx.x >= o)
                 for (int k = 0; k < 3; ++k) before[k] = s_sum[k][threadIdx.x - o];
             __syncthreads();
