@@ -4,9 +4,14 @@
 // A block takes a tile of one window's queries and a head, or two after each other; it walks
 // the window's keys 64 at a time, keys and values through LDS with the next 64 on their way in
 // registers, and keeps the running maximum and sum of the softmax.
-// P is at most 1 and is rounded to the rows' type for its product with v (half an
+// P, at most 2^8 (see `maxima`), is rounded to the rows' type for its product with v (half an
 // ulp of each term, beside half an ulp of the sum); the sum of P is taken before
 // the rounding.
+//
+// 15,000 x 512 in four windows of 3,750, 8 heads of 64: 177 us a call for a floor of 77 (products at
+// 1.5 PFLOP/s), vector units 51 % busy, matrix units 26 %: a score's exponential, scale, sum and rounding
+// stand beside 256 operations of products. 91,000 x 128 in 2,905 windows of 31 rows, 4 heads, cells: 47.2 us
+// for 18.4 (bytes), where blocks wait for their first loads (places, then rows) half of the time.
 #pragma once
 
 #include "attention.h"

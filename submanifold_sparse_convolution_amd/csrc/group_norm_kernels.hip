@@ -10,9 +10,9 @@
 // blocks add up the pieces of their sample first (a kernel between the two for that would
 // cost its launch). x (and dy) are read twice, the second time largely from the caches.
 //
-// 91,000 x 128 bf16 in six samples: 10.0 us of sums and 13.8 of outputs, 22.1 us a call (70 MB:
-// 9.1 at the rate of a large copy, x counted once); backward, 95,000 x 128 in two: 15.0 and 18.0,
-// 32.3 a call. A thread's rows are few there (192 x 16 words on 512 threads: 6), and what bounds
+// 91,000 x 128 bf16 in six samples: 10.1 us of sums and 13.5 of outputs, 21.9 us a call (70 MB:
+// 9.1 at the rate of a large copy, x counted once); backward, 95,000 x 128 in two: 15.6 and 17.4,
+// 32.4 a call. A thread's rows are few there (192 x 16 words on 512 threads: 6), and what bounds
 // the kernels is latency: the loads', the tree's over a block's rows, the joining of pieces.
 // Without gain: six rows of a thread fetched before the pieces are joined (23.1 us); columns
 // summed by a thread each in place of the tree (25.7 for 24.2).
