@@ -215,6 +215,23 @@ def test_windows_of_one_row_have_no_gradient():
         assert torch.equal(dv.cpu(), c.dout.float().view(90, kv, 4 // kv, 32).sum(2).reshape(90, -1).to(dt))
 
 
+def test_more_windows_than_a_grid_has_blocks():
+    """70,000 windows of a row between 70,000 of none, with cells: out is v."""
+    n = 70000
+    g = gen(15)
+    offsets = torch.arange(n + 1).repeat_interleave(2)[:-1].int().cuda()
+    coords = torch.randint(-2 ** 20, 2 ** 20, (n, 3), generator=g).int().cuda()
+    order = torch.randperm(n, generator=g).int().cuda()
+    w = smc.Windows(offsets, n, order=order, coords=coords, extent=(1, 1, 1))
+    q, k, v = (normal(g, (n, 64)).cuda() for _ in range(3))
+    table = normal(g, (3, 3, 2)).cuda()
+    out, lse = smc.window_attention(q, k, v, w, 2, bias=table, lse=True)
+    assert w.longest == 1 and torch.equal(out, v)
+    dout = normal(g, (n, 64)).cuda()
+    dq, dk, dv, dbias = smc.window_attention_backward(dout, q, k, v, out, lse, w, 2, bias=table)
+    assert torch.equal(dv, dout) and (dq == 0).all() and (dk == 0).all() and (dbias == 0).all()
+
+
 @pytest.mark.parametrize("size", [2.0 ** -14, 1.0, 2.0 ** 12])
 @pytest.mark.parametrize("lengths", [[20, 33, 9], [200, 64, 65]])
 def test_f16_gradients_of_any_size(size, lengths):
