@@ -40,59 +40,73 @@ __device__ __forceinline__ uint32_t word_most(u32x4 w, uint32_t most) {
     return most;
 }
 
-// f16: largest |dout| of each head and |v| of each of its heads in a tile of 64 places; a wave a head.
+// f16: largest |dout| of each head and |v| of each of its heads in a tile of 64 places. The block's threads
+// take the tile's words in order, so that loads are whole lines.
 template <int DT, bool A>
 __global__ __launch_bounds__(256) void k_attention_range(AttentionArgs a) {
+    __shared__ uint32_t s_most[256];
+    __shared__ int s_row[64];
     if (block_number() >= a.n_tiles64) return;
     const WindowTile t = a.tiles64[block_number()];
-    const int lane = threadIdx.x & 63, all = a.heads + a.kv_heads;
-    const int row = lane < t.count ? a.places[t.first + lane].row : -1;
-    for (int h = threadIdx.x >> 6; h < all; h += 4) {
-        const bool of_v = h >= a.heads;
-        const void* base = of_v ? a.v : a.dout;
-        const int64_t at = (int64_t)row * (of_v ? a.ldv : a.ld_dout) + (of_v ? h - a.heads : h) * a.dim;
-        uint32_t most = 0;
-        if (row >= 0)
-            for (int c = 0; c < a.dim; c += W) most = word_most<DT>(row_word<A>(base, at + c, a.dim - c), most);
-        most = lane_max<64>(most);
-        if (lane == 0) reinterpret_cast<uint32_t*>(a.range)[block_number() * all + h] = most;
+    const int all = a.heads + a.kv_heads, per = (a.dim + W - 1) / W;
+    if (threadIdx.x < 64) s_row[threadIdx.x] = threadIdx.x < t.count ? a.places[t.first + threadIdx.x].row : -1;
+    for (int h0 = 0; h0 < all; h0 += 256) {
+        const int heads = min(all - h0, 256), words = heads * per, n = t.count * words;
+        __syncthreads();
+        s_most[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i0 = threadIdx.x; i0 < n; i0 += 4 * 256) {
+            u32x4 w[4];
+            int head[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = min(i0 + 256 * k, n - 1), r = i / words, x = i - r * words;
+                head[k] = x / per;
+                const int c = (x - head[k] * per) * W, h = h0 + head[k];
+                const bool of_v = h >= a.heads;
+                w[k] = row_word<A>(of_v ? a.v : a.dout, (int64_t)s_row[r] * (of_v ? a.ldv : a.ld_dout) +
+                                   (int64_t)(of_v ? h - a.heads : h) * a.dim + c, a.dim - c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) atomicMax(&s_most[head[k]], word_most<DT>(w[k], 0u));
+        }
+        __syncthreads();
+        if (threadIdx.x < heads)
+            reinterpret_cast<uint32_t*>(a.range)[block_number() * all + h0 + threadIdx.x] = s_most[threadIdx.x];
     }
 }
 
-// The power of two that dS is taken times in tile t's window, for a head and its head of v.
-template <int THREADS>
-__device__ __forceinline__ float gradient_scale(const AttentionArgs& a, const WindowTile& t, int head, int kv) {
-    __shared__ uint32_t s_most[2][THREADS / 64];
-    const int count = (t.end - t.begin + 63) / 64, all = a.heads + a.kv_heads;
-    uint32_t most[2] = {0u, 0u};
-    for (int i = threadIdx.x; i < count; i += THREADS) {
-        const uint32_t* r = reinterpret_cast<const uint32_t*>(a.range) + (int64_t)(t.first64 + i) * all;
-        most[0] = max(most[0], r[head]);
-        most[1] = max(most[1], r[a.heads + kv]);
+// The maxima of tile t's window, for a head and its head of v: each lane's share of them. Every wave takes them
+// for itself, before its rows are loaded (by the block, between barriers, 91,000 f16 rows in windows of 31 took
+// 120.6 us a backward call; so 105.4; bf16, which needs none of it, 81.5).
+struct WindowMost {
+    uint32_t most[2];
+    __device__ __forceinline__ void load(const AttentionArgs& a, const WindowTile& t, int head, int kv) {
+        const int count = (t.end - t.begin + 63) / 64, all = a.heads + a.kv_heads;
+        most[0] = most[1] = 0u;
+        for (int i = threadIdx.x & 63; i < count; i += 64) {
+            const uint32_t* r = reinterpret_cast<const uint32_t*>(a.range) + (int64_t)(t.first64 + i) * all;
+            most[0] = max(most[0], r[head]);
+            most[1] = max(most[1], r[a.heads + kv]);
+        }
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        most[k] = lane_max<64>(most[k]);
-        if ((threadIdx.x & 63) == 0) s_most[k][threadIdx.x >> 6] = most[k];
+    // The power of two that dS is taken times, of whole waves.
+    __device__ __forceinline__ float scale(int dim) const {
+        const float bound = 2.f * (float)dim * __uint_as_float(lane_max<64>(most[0])) * __uint_as_float(lane_max<64>(most[1]));
+        // bound is within 2^-46 and 2^40
+        const uint32_t by = (uint32_t)(127 + 14 - ((int)(__float_as_uint(bound) >> 23) - 127)) << 23;
+        return __uint_as_float(__builtin_amdgcn_readfirstlane(bound > 0.f ? by : __float_as_uint(1.f)));
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int w = 0; w < THREADS / 64; ++w) most[k] = max(most[k], s_most[k][w]);
-    const float bound = 2.f * (float)a.dim * __uint_as_float(most[0]) * __uint_as_float(most[1]);
-    if (!(bound > 0.f)) return 1.f;
-    // bound is within 2^-46 and 2^40
-    return __uint_as_float((uint32_t)(127 + 14 - ((int)(__float_as_uint(bound) >> 23) - 127)) << 23);
-}
+};
 
 // lse as an exponent's base: where there is no key P is 0.
 __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// (waves a SIMD by what the registers take; 91,000 rows at three 93.8 us, at two 120)
+// (waves a SIMD by what the registers take; 91,000 rows at three 93.8 us, at two 120; 16,000 x 8 heads of 64 in windows
+// of 60, a backward call with three 40.1 us, with two 42.7)
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads, DP <= 32 && EXT <= 32 ? 3 : DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_queries(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, (DP <= 32 && EXT <= 32) || (DP == 64 && EXT == 0 && B::kRows == 64) ? 3 : DP <= 64 && DP + EXT <= 160 ? 2 : 1)
+void k_attention_queries(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16, ET16 = EXT / 16;
     constexpr int NQ = B::kColumns, TH = B::kThreads, kBins = EXT ? EXT / 32 : 1;
     constexpr bool kOwnDelta = B::kRows <= 64;          // (see the top)
@@ -133,13 +147,21 @@ __global__ __launch_bounds__(B::kThreads, DP <= 32 && EXT <= 32 ? 3 : DP <= 64 &
             }
         }
     };
+    WindowMost most[B::kHeads];
+    if (DT == kF16)
+#pragma unroll
+        for (int h = 0; h < B::kHeads; ++h)
+            if (h < heads) most[h].load(a, t, head + h, (head + h) / share);
     load_queries(head, fq, fo, base);
     keys.point(a.k, a.v, head / share * a.dim);
     keys.load(a, a.ldk, a.ldv);
     if (!one) keys.places(a, t, 1);
+    float grows[B::kHeads];
+#pragma unroll
+    for (int h = 0; h < B::kHeads; ++h) grows[h] = DT == kF16 && h < heads ? most[h].scale(a.dim) : 1.f;
     f32x4 dq[NQ][DT16], db[NQ][ET16 ? ET16 : 1];
     auto begin_head = [&]() SMC_INLINE {
-        if (DT == kF16) grow = gradient_scale<TH>(a, t, head, head / share);
+        if (DT == kF16) grow = grows[B::kHeads > 1 && head > first_head];
         keep = length == 1 ? 0.f : grow;        // a window of one row: P is 1 whatever q, k and the bias are
 #pragma unroll
         for (int u = 0; u < NQ; ++u) {
@@ -432,8 +454,12 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
     f32x4 dk[NK][DT16], dv[NK][DT16];
     auto begin_keys = [&]() SMC_INLINE {
         if (DT == kF16) {                       // the smallest factor of the heads that share them serves all
-            grow = gradient_scale<TH>(a, t, head, kv);
-            for (int h = 1; h < share; ++h) grow = fminf(grow, gradient_scale<TH>(a, t, head + h, kv));
+            grow = INFINITY;
+            for (int h = 0; h < share; ++h) {
+                WindowMost most;
+                most.load(a, t, head + h, kv);
+                grow = fminf(grow, most.scale(a.dim));
+            }
         }
         keep = length == 1 ? 0.f : grow;        // a window of one row: P is 1 whatever q, k and the bias are
 #pragma unroll
