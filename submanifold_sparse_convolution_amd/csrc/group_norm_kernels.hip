@@ -137,6 +137,9 @@ size_t sum_floats(int c) { return std::max<size_t>((size_t)W * T, (size_t)2 * c)
 
 // ---- forward -------------------------------------------------------------------------
 
+// What roundings left below zero counts as zero; a NaN stays.
+__device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
+
 // Mean and sum of squared deviations of each group over a piece's rows, into out [groups][2] (memory or LDS).
 template <int DT, bool A, int T>
 __device__ __forceinline__ void piece_sums(const GroupArgs& a, const Piece& p, const Lay<T>& l, float* s, float* out) {
@@ -167,7 +170,7 @@ __device__ __forceinline__ void piece_sums(const GroupArgs& a, const Piece& p, c
             if (e < left) {
                 const float off = sum[e] / rows;
                 s[c + e] = base[e] + off;                                           // the channel's mean
-                s_squares[c + e] = fmaxf(sum[W + e] - sum[e] * off, 0.f);           // and squared deviations
+                s_squares[c + e] = not_negative(sum[W + e] - sum[e] * off);           // and squared deviations
             }
     __syncthreads();
     const int per = a.c / a.groups, lane = threadIdx.x & 63;
@@ -246,7 +249,7 @@ __device__ void join_pieces(const GroupArgs& a, const Piece& p, float* s, float*
             if (count > 0) {
                 const float n = (float)(p.run_end - p.run_begin), off = v[0] / n;
                 mean = base + off;
-                rstd = inverse_root(fmaxf(v[1] - v[0] * off * (float)per, 0.f) / (n * (float)per) + a.eps);
+                rstd = inverse_root(not_negative(v[1] - v[0] * off * (float)per) / (n * (float)per) + a.eps);
             }
             s_stats[(g0 + g) * 2] = mean;
             s_stats[(g0 + g) * 2 + 1] = rstd;
