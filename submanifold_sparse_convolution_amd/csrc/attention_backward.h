@@ -122,7 +122,8 @@ void k_attention_queries(AttentionArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
     const int share = a.heads / a.kv_heads, first_head = head, heads = min(a.heads_each, a.heads - head);
     const int length = t.end - t.begin;
-    const bool active = wave * NQ * 16 < t.count, one = length <= kKeys;    // one step a head
+    // (rows of no window walk none: products of what they hold with zeros need not be zero)
+    const bool active = wave * NQ * 16 < t.count && length > 0, one = length <= kKeys;      // one: one step a head
     const float to_log2 = EXT ? kLog2e : a.scale * kLog2e;
     const TileLane<RW> at(lane);
     const TileLane<RE> at_cells(lane);
@@ -427,7 +428,8 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
     const int share = a.heads / a.kv_heads, end_head = min(kv + a.heads_each, a.kv_heads) * share;
     const int length = t.end - t.begin;
-    const bool active = wave * NK * 16 < t.count, one = length <= kKeys;    // one step a head
+    // (rows of no window walk none: products of what they hold with zeros need not be zero)
+    const bool active = wave * NK * 16 < t.count && length > 0, one = length <= kKeys;      // one: one step a head
     const float to_log2 = EXT ? kLog2e : a.scale * kLog2e;
     const TileLane<RW> at(lane);
     const TileLane<RE> at_cells(lane);
