@@ -263,8 +263,9 @@ __device__ __forceinline__ WindowPlace place_at(const AttentionArgs& a, int at, 
 
 // Two tiles of a window's rows (keys and values, or queries and dout) and their one-hot cells, 64 rows
 // a step: a step's rows are loaded while the one before is worked on, and go to LDS after it, with two
-// buffers without waiting for the other waves' reads of it.
-template <int DT, int DP, int EXT, bool A, class B, int NB>
+// buffers without waiting for the other waves' reads of it. Places past the window's end are zeros; where REPEATS
+// the first tile has the window's last row there, so that its products with infinities are no others than the window's.
+template <int DT, int DP, int EXT, bool A, class B, int NB, bool REPEATS = false>
 struct Walk {
     static constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, TH = B::kThreads;
     static constexpr int kWords = kKeys * RW / TH, kCells = EXT ? kKeys * RE / TH : 1;      // a thread's
@@ -273,7 +274,7 @@ struct Walk {
     };
     u32x4 wx[kWords], wy[kWords];
     const char *px, *py;        // this thread's word of row 0, of the head whose rows are loaded
-    int rows[kWords];           // of the step to load
+    int rows[kWords];           // of the step to load; negative past the end (REPEATS: ~ of the last row)
     uint32_t cells[kCells], held[kCells];       // of that step, and of the step loaded
     bool whole;                 // the step to load has 64 rows, of DP elements
 
@@ -295,7 +296,15 @@ struct Walk {
             return;
         }
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) rows[i] = place_at(a, first + (i * TH + (int)threadIdx.x) / RW, t.end).row;
+        for (int i = 0; i < kWords; ++i) {
+            const int at = first + (i * TH + (int)threadIdx.x) / RW;
+            if (REPEATS) {
+                const int row = a.places[max(min(at, t.end - 1), 0)].row;
+                rows[i] = at < t.end ? row : ~row;
+            } else {
+                rows[i] = place_at(a, at, t.end).row;
+            }
+        }
         if (EXT)
 #pragma unroll
             for (int i = 0; i < kCells; ++i) cells[i] = place_at(a, first + (i * TH + (int)threadIdx.x) / RE, t.end).cells;
@@ -312,7 +321,8 @@ struct Walk {
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 const int left = rows[i] < 0 ? 0 : a.dim - word();
-                wx[i] = row_word<A>(px + (uint64_t)(uint32_t)rows[i] * bx, 0, left);
+                const int x = REPEATS && rows[i] < 0 ? ~rows[i] : rows[i];
+                wx[i] = row_word<A>(px + (uint64_t)(uint32_t)x * bx, 0, REPEATS ? a.dim - word() : left);
                 wy[i] = row_word<A>(py + (uint64_t)(uint32_t)rows[i] * by, 0, left);
             }
         }

@@ -418,7 +418,8 @@ template <int DT, int DP, int EXT, bool A, class B>
 __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_keys(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NK = B::kColumns, TH = B::kThreads;
-    typedef Walk<DT, DP, EXT, A, B, 1> Queries;
+    // (places past the end have a base of inf, P and dS of 0, also beside k of infinities)
+    typedef Walk<DT, DP, EXT, A, B, 1, true> Queries;
     __shared__ __align__(16) typename Queries::Memory s_queries;
     __shared__ __align__(16) float s_base[kKeys], s_delta[kKeys];
     __shared__ __align__(16) uint16_t s_table[EXT ? 2 * kTableEntries<EXT> : 2];

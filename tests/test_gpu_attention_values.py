@@ -1,4 +1,4 @@
-"""Window attention: rows that belong to no window may hold anything."""
+"""Window attention: values that are not finite in rows of no window and in masked keys."""
 import math
 
 import pytest
@@ -36,3 +36,29 @@ def test_rows_of_no_window_may_hold_anything(lengths, dim, bad, cells, dt):
         if a is not None:
             assert torch.equal(a, b), label
     assert all((t[outside] == 0).all() for t in (want[0], *want[2:5]))
+
+
+@pytest.mark.parametrize("length,dim", [(30, 32), (64, 32), (100, 32), (500, 32), (30, 33), (100, 128)])
+@pytest.mark.parametrize("cells", [False, True])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_a_key_that_is_masked_by_infinity(length, dim, cells, dt):
+    """A key whose scores are all -inf in one head has no share there, as where they are merely far below the
+    others: the same bits of out, dk (zeros for the key) and dv, also beside places that hold no query."""
+    c = Case([length, 7], heads=4, kv=2, dim=dim, dt=dt, extent=(8, 8, 8) if cells else None, reach=3, order=False, seed=21)
+    c.q[:, ::dim] = c.q[:, ::dim].abs() + 1
+    c.k[5, 0] = -1e4
+    q, k, v, table = (t if t is None else t.contiguous() for t in c.device())
+    dout = c.dout.cuda()
+
+    def run():
+        out, lse = smc.window_attention(q, k, v, c.windows, 4, bias=table, lse=True)
+        return (out, lse, *smc.window_attention_backward(dout, q, k, v, out, lse, c.windows, 4, bias=table))
+
+    want = run()
+    k[5, 0] = -math.inf
+    got = run()
+    for label, i in (("out", 0), ("lse", 1), ("dk", 3), ("dv", 4)):
+        assert torch.equal(got[i], want[i]), label
+    assert (got[3][5, :dim] == 0).all() and (got[4][5, :dim] == 0).all()
+    if cells:
+        assert torch.equal(got[5], want[5])
