@@ -18,7 +18,9 @@
 // 236 us for 226 a call, 91,000 rows in 2,905 windows 180.4 for 179.8). dS follows
 // the gradient's size, which in f16 may leave the type's range where dq and dk do not,
 // so in f16 it is taken times a power of two: |dP - delta| <= 2 dim max |dout| max |v| over
-// the window (finite values), brought to [2^14, 2^15]; k_attention_range finds the maxima.
+// the window (finite values), brought to [2^14, 2^15]; k_attention_range finds the maxima. P, for dv, is taken times
+// 2^14 there: in windows of more than some 16,000 rows the mean P is below f16's normal numbers (2^-14), and so are
+// keys of little weight in any (with it 95,000 rows of equal scores lost 0.2 % of dv).
 // delta is taken from out, which was rounded: an error of half an ulp of each out term, over the
 // window's mean of k on its way into dq. Where a window's keys fit one tile delta is the mean of dP
 // under P itself instead (long windows average the error away; blocks of 128 queries have no registers for it).
@@ -418,6 +420,7 @@ template <int DT, int DP, int EXT, bool A, class B>
 __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_keys(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NK = B::kColumns, TH = B::kThreads;
+    constexpr float kLift = DT == kF16 ? 14.f : 0.f;            // P is times 2^kLift, by its base
     // (places past the end have a base of inf, P and dS of 0, also beside k of infinities)
     typedef Walk<DT, DP, EXT, A, B, 1, true> Queries;
     __shared__ __align__(16) typename Queries::Memory s_queries;
@@ -464,7 +467,7 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
                 grow = fminf(grow, most.scale(a.dim));
             }
         }
-        keep = length == 1 ? 0.f : grow;        // a window of one row: P is 1 whatever q, k and the bias are
+        keep = length == 1 ? 0.f : grow * exp2f(-kLift);        // a window of one row: P is 1 whatever q, k and the bias are
 #pragma unroll
         for (int u = 0; u < NK; ++u)
 #pragma unroll
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
         for (int u = 0; u < NK; ++u) {
             const int c0 = kv * a.dim;
             store_row<DT, DP, A>(dk[u], f, a.dk, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dk + c0, a.dim, lane);
-            store_row<DT, DP, A>(dv[u], 1.f, a.dv, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dv + c0, a.dim, lane);
+            store_row<DT, DP, A>(dv[u], exp2f(-kLift), a.dv, own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dv + c0, a.dim, lane);
         }
     };
     auto load = [&](int h, int step) SMC_INLINE {
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) v
     auto commit = [&](bool first) SMC_INLINE {      // (first: of a head)
         __syncthreads();
         if (threadIdx.x < kKeys) {
-            s_base[threadIdx.x] = lse_base(base);
+            s_base[threadIdx.x] = lse_base(base) - kLift;
             s_delta[threadIdx.x] = delta * keep;
         }
         if (EXT && first) table.commit(a, s_table);

@@ -1,9 +1,11 @@
-"""Window attention: values that are not finite in rows of no window and in masked keys."""
+"""Window attention: values that are not finite in rows of no window and in masked keys,
+probabilities below f16's normal numbers."""
 import math
 
 import pytest
 import torch
 
+import _rowops as ro
 import submanifold_sparse_convolution_amd as smc
 from test_gpu_attention import BF16, F16, Case
 
@@ -62,3 +64,34 @@ def test_a_key_that_is_masked_by_infinity(length, dim, cells, dt):
     assert (got[3][5, :dim] == 0).all() and (got[4][5, :dim] == 0).all()
     if cells:
         assert torch.equal(got[5], want[5])
+
+
+def test_f16_gradient_of_values_in_a_window_of_many_rows():
+    """95,001 rows whose scores are alike: P is 1 / 95,001, below f16's normal numbers. With dout 1 every dv is 1.
+    Half an ulp for P as an operand and one for dv, the additions of a step each, an exponential (2^-21), and lse, log 95,001."""
+    n = 95001
+    w = smc.Windows(torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    zero, one = (torch.full((n, 32), f, dtype=F16, device="cuda") for f in (0.0, 1.0))
+    out, lse = smc.window_attention(zero, zero, one, w, 1, lse=True)
+    _, _, dv, _ = smc.window_attention_backward(one, zero, zero, one, out, lse, w, 1)
+    tol = 2 * 2.0 ** -11 + ro.gamma(n // 32 + 40) + 2.0 ** -21 + 4 * ro.U * math.log(n)
+    assert ((dv.double() - 1).abs() <= tol).all()
+
+
+def test_f16_gradient_of_values_with_little_weight():
+    """Every query the same, keys' weights over a range of e^8 in a window of 20,000 rows: dv_j = n P_j, each to its own
+    half ulps, down to P of 10^-8. Scores are exact products below 16 (their rounding and lse's: 4 u |s| each)."""
+    n = 20000
+    g = torch.Generator()
+    g.manual_seed(22)
+    w = smc.Windows(torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    q, k = torch.zeros(n, 32, dtype=F16), torch.zeros(n, 32, dtype=F16)
+    q[:, 0] = 1
+    k[:, 0] = (-8 * torch.rand(n, generator=g)).to(F16)
+    v, one = (torch.full((n, 32), 1.0, dtype=F16, device="cuda") for _ in range(2))
+    q, k = q.cuda(), k.cuda()
+    out, lse = smc.window_attention(q, k, v, w, 1, scale=1.0, lse=True)
+    _, _, dv, _ = smc.window_attention_backward(one, q, k, v, out, lse, w, 1, scale=1.0)
+    want = n * torch.softmax(k[:, 0].double(), 0)
+    tol = 2 * 2.0 ** -11 + ro.gamma(n // 32 + 40) + 2.0 ** -21 + 8 * ro.U * 16
+    assert ((dv.double() - want[:, None]).abs() <= tol * want[:, None] + 2.0 ** -25).all()
