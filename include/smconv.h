@@ -655,7 +655,8 @@ int smc_weight_quantize(const void* w, int64_t ldw, int c_in, int c_out, int dty
  * rows of no sample come out as zeros, and so do their gradients. stats (or NULL):
  * mean and 1 / sqrt(var + eps) of each sample and group, zeros for an empty sample; a
  * variance of zero with eps = 0 counts as 1 / sqrt 0 = 0.
- * y may be x (equal addresses and row distances); other overlaps are refused.
+ * y may be x (equal addresses and row distances); other overlaps of an output with
+ * an argument of the call are refused (SMC_ERR_ARG), in the backward pass too.
  *
  * Backward, from x and the stats that the forward call wrote: with z = x_hat weight + bias,
  * dz = dy act'(z) and means over the sample and group
@@ -739,7 +740,8 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  * reaches every row of its head that lies at that distance from a cell of the window's extent.
  * lse (or NULL): log sum_j exp(s_ij), float32 [heads, n] by place (not by row), -inf for
  * zeros' rows; the backward pass reads it. Scores, softmax and sums are float32; P is
- * rounded to dtype for its product with v. out may not overlap q, k or v.
+ * rounded to dtype for its product with v. out and lse may not overlap each other, q, k, v or bias
+ * (SMC_ERR_ARG).
  *
  * Backward, from the same inputs and what the forward call wrote to out and lse, for the
  * gradient dout of out; P is computed again:
@@ -748,8 +750,9 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  *   dbias[axis][b][h] = sum of dS over the pairs of the bucket, all windows and rows.
  * P and dS are rounded to dtype as operands of products, but not for dbias (f16: dS times a power of two found
  * on the device, so that finite gradients that fit f16 come out finite). Gradients of rows
- * of no window are zeros. dq, dk and dv may be columns of one buffer; they may not overlap
- * an input or each other. workspace: smc_window_attention_backward_workspace(args) bytes,
+ * of no window are zeros. dq, dk and dv may be columns of one buffer; they and dbias may not overlap
+ * an input or each other (SMC_ERR_ARG), but dbias may be bias. workspace:
+ * smc_window_attention_backward_workspace(args) bytes,
  * 16-byte aligned; the query reads windows, heads, kv_heads, dtype, bias and reach.
  */
 typedef struct smc_attention_s {

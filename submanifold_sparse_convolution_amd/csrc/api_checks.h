@@ -56,6 +56,23 @@ inline bool share_memory(const void* p, int64_t ldp, int esp, const void* q, int
     return apart < wp || apart + wq > pitch;
 }
 
+// Do the `bytes` bytes at v lie over the tensor at p (16-bit rows of cols elements, ld elements apart)?
+inline bool over_rows(const void* v, size_t bytes, const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    if (!v || !p || rows <= 0 || bytes == 0) return false;
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)v;
+    const uint64_t pitch = (uint64_t)ld * 2, width = (uint64_t)cols * 2;
+    if (b + bytes <= a || b >= a + (uint64_t)(rows - 1) * pitch + width) return false;
+    if (b < a) return true;
+    const uint64_t into = (b - a) % pitch;             // bytes of b's row that lie before it
+    return into < width || into + bytes > pitch;        // (b lies before the last row's end, so another row follows)
+}
+
+// Do the bytes at v lie over those at w?
+inline bool over_bytes(const void* v, size_t bytes, const void* w, size_t others) {
+    const uintptr_t a = (uintptr_t)v, b = (uintptr_t)w;
+    return v && w && bytes > 0 && others > 0 && a < b + others && b < a + bytes;
+}
+
 inline int check_common(int64_t n, int64_t c, const char* cname, int dtype) {
     if (n < 0 || n > kMaxRows) return bad(SMC_ERR_ARG, "n = %lld", (long long)n);
     if (c < 1 || c > kMaxDim) return bad(SMC_ERR_ARG, "%s = %lld outside [1, 2^21]", cname, (long long)c);

@@ -9,6 +9,24 @@ namespace {
 
 bool odd(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
+// Arguments that may not share memory.
+struct Rows {
+    const char* name;
+    const void* p;
+    int64_t ld, cols;
+};
+struct Vector {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+int apart(const Vector& v, const Rows& r, int64_t n) {
+    return over_rows(v.p, v.bytes, r.p, r.ld, n, r.cols) ? bad(SMC_ERR_ARG, "%s shares memory with %s", v.name, r.name) : SMC_OK;
+}
+int apart(const Vector& v, const Vector& w) {
+    return over_bytes(v.p, v.bytes, w.p, w.bytes) ? bad(SMC_ERR_ARG, "%s shares memory with %s", v.name, w.name) : SMC_OK;
+}
+
 // ---- group norm --------------------------------------------------------------------
 
 int check_group(const smc_group_norm_t* a, bool backward) {
@@ -33,10 +51,20 @@ int check_group(const smc_group_norm_t* a, bool backward) {
     auto over = [&](const void* p, int64_t ldp, const void* q, int64_t ldq) {
         return (p != q || ldp != ldq) && share_memory(p, ldp, 2, q, ldq, 2, a->n, a->c, a->c);
     };
+    // and some blocks write theirs while others still read the vectors and statistics
+    const size_t row = (size_t)a->c * 2, kept = (size_t)a->samples * a->groups * 8;
+    const Vector in[] = {{"weight", a->weight, row}, {"bias", a->bias, row}, {"offsets", a->offsets, ((size_t)a->samples + 1) * 4}};
+    const Vector stats = {"stats", a->stats, kept};
     if (!backward) {
         CHECK(check_rows("y", a->y, a->n, a->c, a->ldy));
         if (over(a->y, a->ldy, a->x, a->ldx)) return bad(SMC_ERR_ARG, "y shares memory with x");
-        return SMC_OK;
+        const Rows x = {"x", a->x, a->ldx, a->c}, y = {"y", a->y, a->ldy, a->c};
+        for (const Vector& v : in) {
+            CHECK(apart(v, y, a->n));
+            CHECK(apart(stats, v));
+        }
+        CHECK(apart(stats, x, a->n));
+        return apart(stats, y, a->n);
     }
     if (!a->stats) return bad(SMC_ERR_ARG, "stats is NULL");
     CHECK(check_rows("dy", a->dy, a->n, a->c, a->ld_dy));
@@ -45,7 +73,16 @@ int check_group(const smc_group_norm_t* a, bool backward) {
     if (!a->dbias || odd(a->dbias, 2)) return bad(SMC_ERR_ARG, "dbias is NULL or misaligned");
     if (over(a->dx, a->ld_dx, a->x, a->ldx)) return bad(SMC_ERR_ARG, "dx shares memory with x");
     if (over(a->dx, a->ld_dx, a->dy, a->ld_dy)) return bad(SMC_ERR_ARG, "dx shares memory with dy");
-    return SMC_OK;
+    const Rows rows[] = {{"x", a->x, a->ldx, a->c}, {"dy", a->dy, a->ld_dy, a->c}, {"dx", a->dx, a->ld_dx, a->c}};
+    const Vector to[] = {{"dweight", a->dweight, row}, {"dbias", a->dbias, row}};
+    for (const Vector& t : to) {
+        for (const Vector& v : in) CHECK(apart(t, v));
+        CHECK(apart(t, stats));
+        for (const Rows& r : rows) CHECK(apart(t, r, a->n));
+    }
+    for (const Vector& v : in) CHECK(apart(v, rows[2], a->n));
+    CHECK(apart(stats, rows[2], a->n));
+    return apart(to[0], to[1]);
 }
 
 GroupArgs group_args(const smc_group_norm_t* a) {
@@ -186,7 +223,14 @@ int check_attention(const smc_attention_t* a, bool backward) {
         if (a->windows->ex < 1) return bad(SMC_ERR_STATE, "a bias needs windows with cells");
         if (a->reach < 1 || a->reach > kMaxReach) return bad(SMC_ERR_ARG, "reach = %d outside [1, %d]", a->reach, kMaxReach);
     }
+    const Vector lse = {"lse", a->lse, (size_t)a->heads * n * 4};
+    const Vector table = {"bias", a->bias, a->bias ? (size_t)3 * (2 * a->reach + 1) * a->heads * 2 : 0};
+    const Rows in[] = {{"q", a->q, a->ldq, c}, {"k", a->k, a->ldk, ckv}, {"v", a->v, a->ldv, ckv},
+                       {"out", a->out, a->ld_out, c}, {"dout", a->dout, a->ld_dout, c}};
     if (!backward) {
+        CHECK(apart(table, in[3], n));
+        CHECK(apart(lse, table));
+        for (int i = 0; i < 4; ++i) CHECK(apart(lse, in[i], n));
         // other blocks read the inputs' rows again
         if (share_memory(a->out, a->ld_out, 2, a->q, a->ldq, 2, n, c, c) ||
             share_memory(a->out, a->ld_out, 2, a->k, a->ldk, 2, n, c, ckv) ||
@@ -200,13 +244,6 @@ int check_attention(const smc_attention_t* a, bool backward) {
     CHECK(check_rows("dk", a->dk, n, ckv, a->ld_dk));
     CHECK(check_rows("dv", a->dv, n, ckv, a->ld_dv));
     if (a->bias && (!a->dbias || odd(a->dbias, 2))) return bad(SMC_ERR_ARG, "dbias is NULL or misaligned");
-    struct Rows {
-        const char* name;
-        const void* p;
-        int64_t ld, cols;
-    };
-    const Rows in[] = {{"q", a->q, a->ldq, c}, {"k", a->k, a->ldk, ckv}, {"v", a->v, a->ldv, ckv},
-                       {"out", a->out, a->ld_out, c}, {"dout", a->dout, a->ld_dout, c}};
     const Rows to[] = {{"dq", a->dq, a->ld_dq, c}, {"dk", a->dk, a->ld_dk, ckv}, {"dv", a->dv, a->ld_dv, ckv}};
     auto shared = [n](const Rows& x, const Rows& y) {
         return share_memory(x.p, x.ld, 2, y.p, y.ld, 2, n, x.cols, y.cols);
@@ -216,6 +253,15 @@ int check_attention(const smc_attention_t* a, bool backward) {
             if (shared(to[i], r)) return bad(SMC_ERR_ARG, "%s shares memory with %s", to[i].name, r.name);
         for (int j = 0; j < i; ++j)
             if (shared(to[i], to[j])) return bad(SMC_ERR_ARG, "%s shares memory with %s", to[i].name, to[j].name);
+    }
+    // (dbias is written by the last kernel: it may be bias)
+    const Vector to_table = {"dbias", a->dbias, table.bytes};
+    CHECK(apart(to_table, lse));
+    for (const Rows& r : in) CHECK(apart(to_table, r, n));
+    for (const Rows& r : to) {
+        CHECK(apart(table, r, n));
+        CHECK(apart(lse, r, n));
+        CHECK(apart(to_table, r, n));
     }
     return SMC_OK;
 }
