@@ -760,7 +760,7 @@ typedef struct smc_attention_s {
     int32_t heads, kv_heads;  /* kv_heads divides heads */
     int32_t head_dim;         /* 1 .. 128 */
     int32_t dtype;            /* SMC_DTYPE_BF16 or _F16 */
-    float scale;              /* > 0 */
+    float scale;              /* > 0, at most 2^126 */
     int32_t reach;            /* 1 .. 127 with bias */
     const void* bias;         /* [3, 2 reach + 1, heads] or NULL */
     const void* q;            /* [n, heads * head_dim] */

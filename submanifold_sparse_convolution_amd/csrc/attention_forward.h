@@ -117,7 +117,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) m = fmaxf(m, s[b][u][e]);
             most[u] = quad_max(m);
-            grows |= most[u] > top[u] + 8.f / to_log2;
+            grows |= (most[u] - top[u]) * to_log2 > 8.f;       // (of two -inf: no)
         }
         if (any_lane(grows))
 #pragma unroll

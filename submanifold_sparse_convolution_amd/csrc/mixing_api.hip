@@ -212,7 +212,8 @@ int check_attention(const smc_attention_t* a, bool backward) {
     CHECK(check_common(n, c, "heads * head_dim", a->dtype));
     if ((int64_t)a->windows->tiles32 * a->heads >= (int64_t)1 << 31)
         return bad(SMC_ERR_UNSUPPORTED, "%d tiles of %d heads: 2^31 or more", a->windows->tiles32, a->heads);
-    if (!(a->scale > 0.f) || a->scale > 3.4e38f) return bad(SMC_ERR_ARG, "scale = %g", (double)a->scale);
+    if (!(a->scale > 0.f) || a->scale > 0x1p126f)      // (its product with log2 e is finite)
+        return bad(SMC_ERR_ARG, "scale = %g", (double)a->scale);
     CHECK(check_rows("q", a->q, n, c, a->ldq));
     CHECK(check_rows("k", a->k, n, ckv, a->ldk));
     CHECK(check_rows("v", a->v, n, ckv, a->ldv));

@@ -1,10 +1,11 @@
 """Window attention: values that are not finite in rows of no window and in masked keys,
-probabilities below f16's normal numbers."""
+probabilities below f16's normal numbers, scales at float32's lower end."""
 import math
 
 import pytest
 import torch
 
+import _mixing as mx
 import _rowops as ro
 import submanifold_sparse_convolution_amd as smc
 from test_gpu_attention import BF16, F16, Case
@@ -95,3 +96,17 @@ def test_f16_gradient_of_values_with_little_weight():
     want = n * torch.softmax(k[:, 0].double(), 0)
     tol = 2 * 2.0 ** -11 + ro.gamma(n // 32 + 40) + 2.0 ** -21 + 8 * ro.U * 16
     assert ((dv.double() - want[:, None]).abs() <= tol * want[:, None] + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-38, 2.0 ** -100])
+@pytest.mark.parametrize("cells", [False, True])
+def test_scales_at_the_lower_end_of_float32(scale, cells):
+    """Every score is the bias alone: out the mean of v under the softmax of the bias, lse with it."""
+    c = Case([50, 130, 9], heads=4, kv=2, dim=32, extent=(8, 8, 8) if cells else None, reach=3, seed=23)
+    q, k, v, table = c.device()
+    args = list(c.formula())
+    args[9] = 0.0
+    want, bound, wl, el = mx.attention(*args)
+    out, lse = smc.window_attention(q, k, v, c.windows, 4, bias=table, scale=scale, lse=True)
+    ro.check(out, want, bound, "out")
+    ro.check(lse, wl, el, "lse")

@@ -1,5 +1,5 @@
 """Group norm and window attention refuse outputs that lie over what other blocks of the call still read
-or write. Addresses only: every call here is refused before any GPU work."""
+or write, and scales that float32 does not hold. Addresses only: every call here is refused before any GPU work."""
 import ctypes
 
 import pytest
@@ -98,3 +98,12 @@ def test_attention_neighbours_are_taken():
         a = attention(**changed)
         a.workspace_bytes = 0
         assert "workspace" in message(smc.lib().smc_window_attention_backward, a)
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf"), 3e38])
+def test_scales(scale):
+    """Above 2^126 the scale's product with log2 e is no float32 number."""
+    a = attention()
+    a.scale = scale
+    for call in (smc.lib().smc_window_attention, smc.lib().smc_window_attention_backward):
+        assert "scale" in message(call, a)
