@@ -943,7 +943,7 @@ def _attention_args(q, k, v, windows, heads, bias, scale):
         raise TypeError("windows must be a Windows")
     if windows.device != dev or windows.n != n:
         raise ValueError(f"windows are of {windows.n} rows on {windows.device}, q has {n} on {dev}")
-    if heads < 1 or c % heads:
+    if heads < 1 or c < 1 or c % heads:
         raise ValueError(f"{c} channels in {heads} heads")
     dim = c // heads
     if k.dim() != 2 or k.shape[1] < dim or k.shape[1] % dim or heads % (k.shape[1] // dim):

@@ -314,7 +314,7 @@ void k_attention_queries(AttentionArgs a) {
                                  own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ld_dq + head * a.dim, a.dim, lane);
         }
         if constexpr (EXT > 0) {
-            // A few queries at a time: a query's dB to a row of LDS at its own distances (as load_table counts the
+            // A few queries at a time: a query's dB to a row of LDS at its own distances (as TableLoads counts the
             // entries), zeros around it, and the rows added, a lane for each 64th entry
             const Cells cells(a.extent);
             float* const mine = s_db + wave * kRowsOf * kRow;

@@ -59,7 +59,7 @@ struct Cells {
         }
     }
     __host__ __device__ int all() const { return first[2] + up[2]; }
-    // twice as many entries by distance (see load_table)
+    // twice as many entries by distance (see TableLoads)
     __host__ __device__ int axis_of_entry(int i) const { return (i >= 2 * first[1]) + (i >= 2 * first[2]); }
     __host__ __device__ static int pick(const int (&v)[3], int axis) { return axis == 0 ? v[0] : axis == 1 ? v[1] : v[2]; }
     __host__ __device__ uint32_t lowest() const { return (uint32_t)first[1] << 8 | (uint32_t)first[2] << 16; }
@@ -112,7 +112,6 @@ struct AttentionArgs {
     float scale = 0.f;
     const void *q = nullptr, *k = nullptr, *v = nullptr;
     int64_t ldq = 0, ldk = 0, ldv = 0;
-    const char* plan = nullptr;
     const WindowPlace* places = nullptr;
     const WindowTile* tiles = nullptr;
     int n_tiles = 0;

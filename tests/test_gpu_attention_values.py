@@ -110,3 +110,10 @@ def test_scales_at_the_lower_end_of_float32(scale, cells):
     out, lse = smc.window_attention(q, k, v, c.windows, 4, bias=table, scale=scale, lse=True)
     ro.check(out, want, bound, "out")
     ro.check(lse, wl, el, "lse")
+
+
+def test_rows_without_channels_are_refused():
+    w = smc.Windows(torch.tensor([0, 4], dtype=torch.int32, device="cuda"), 4)
+    none = torch.empty(4, 0, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="channels"):
+        smc.window_attention(none, none, none, w, 2)
