@@ -654,7 +654,8 @@ int smc_weight_quantize(const void* w, int64_t ldw, int c_in, int c_out, int dty
  * [0, n] (others are read as if cut to it, and give wrong results). Samples may be empty;
  * rows of no sample come out as zeros, and so do their gradients. stats (or NULL):
  * mean and 1 / sqrt(var + eps) of each sample and group, zeros for an empty sample; a
- * variance of zero with eps = 0 counts as 1 / sqrt 0 = 0.
+ * variance of zero with eps = 0 counts as 1 / sqrt 0 = 0. A value that is not finite makes rstd and the rows of its
+ * sample and group NaN, and no others (differences of a group's values count: bf16 beyond 2^127 apart are infinite).
  * y may be x (equal addresses and row distances); other overlaps of an output with
  * an argument of the call are refused (SMC_ERR_ARG), in the backward pass too.
  *

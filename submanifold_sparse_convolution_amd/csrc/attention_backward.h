@@ -9,7 +9,7 @@
 // compute S and dP: 7 products a pair where 5 would do, but dq needs no sum over blocks.
 // dB = dS E comes out as sums over the cells of a key for each query; a block adds
 // them up by distance and writes its buckets, k_table_sum adds the blocks. 91,000 rows in 2,905
-// windows: queries 93.6 us, keys 68.3, sums 9.8; 15,000 x 512 in windows of 1,024: 127, 111 and 4.7.
+// windows: queries 93.9 us, keys 68.1, sums 9.8; 15,000 x 512 in windows of 1,024: 131, 118 and 4.8.
 // (Distances looked up for each entry of dB in place of rows shifted by the query's cell: 107.2 and 134.)
 //
 // P and dS are rounded to the rows' type as operands (half an ulp of each term). Not so for the

@@ -8,9 +8,9 @@
 // ulp of each term, beside half an ulp of the sum); the sum of P is taken before
 // the rounding.
 //
-// 15,000 x 512 in four windows of 3,750, 8 heads of 64: 177 us a call for a floor of 77 (products at
+// 15,000 x 512 in four windows of 3,750, 8 heads of 64: 182 us a call for a floor of 77 (products at
 // 1.5 PFLOP/s), vector units 51 % busy, matrix units 26 %: a score's exponential, scale, sum and rounding
-// stand beside 256 operations of products. 91,000 x 128 in 2,905 windows of 31 rows, 4 heads, cells: 47.2 us
+// stand beside 256 operations of products. 91,000 x 128 in 2,905 windows of 31 rows, 4 heads, cells: 48.0 us
 // for 18.4 (bytes), where blocks wait for their first loads (places, then rows) half of the time.
 #pragma once
 
@@ -228,12 +228,13 @@ void attention_t(AttentionArgs a, hipStream_t s) {
     launch(k_attention<DT, DP, EXT, A, B>, attention_grid(a.n_tiles, a.heads, a.heads_each), dim3(B::kThreads), 0, s, a);
 }
 
-// Rows that are no whole 16-byte words take one kernel a width: their loads cost more than a better
-// fitting block or contraction would save.
+// Rows that are no whole 16-byte words take one kernel a width, which keeps the library small and costs most where
+// there is a bias (128 cells): 91,000 x 4 heads of 32 in windows of 31, forward / backward in us, 53 / 260 for 24 / 87
+// aligned, without a bias 25.7 / 76.6 for 23.8 / 65.8.
 template <int DT, int DP>
 hipError_t attention_by_cells(const AttentionArgs& a, int lengths, hipStream_t s) {
     const int cells = a.table ? Cells(a.extent).all() : 0;
-    #define SMC_GO(EXT, A, B) attention_t<DT, DP, EXT, A, B>(a, s)
+#define SMC_GO(EXT, A, B) attention_t<DT, DP, EXT, A, B>(a, s)
 #define SMC_CELLS(EXT)                                                         \
     do {                                                                       \
         if (lengths == kShortWindows) SMC_GO(EXT, true, BlockShort);       \

@@ -10,9 +10,9 @@
 // blocks add up the pieces of their sample first (a kernel between the two for that would
 // cost its launch). x (and dy) are read twice, the second time largely from the caches.
 //
-// 91,000 x 128 bf16 in six samples: 10.1 us of sums and 13.5 of outputs, 21.9 us a call (70 MB:
-// 9.1 at the rate of a large copy, x counted once); backward, 95,000 x 128 in two: 15.6 and 17.4,
-// 32.4 a call. A thread's rows are few there (192 x 16 words on 512 threads: 6), and what bounds
+// 91,000 x 128 bf16 in six samples: 10.8 us of sums and 13.2 of outputs, 22.4 us a call (70 MB:
+// 9.1 at the rate of a large copy, x counted once); backward, 95,000 x 128 in two: 15.0 and 18.3,
+// 32.5 a call. A thread's rows are few there (192 x 16 words on 512 threads: 6), and what bounds
 // the kernels is latency: the loads', the tree's over a block's rows, the joining of pieces.
 // Without gain: six rows of a thread fetched before the pieces are joined (23.1 us); columns
 // summed by a thread each in place of the tree (25.7 for 24.2).
@@ -21,7 +21,8 @@
 // far and the sum of squared deviations from it (as Welford, of differences from the piece's first row,
 // which keep the mean's digits), and threads, channels and pieces are joined by theirs (as Chan, Golub and
 // LeVeque). (Sums of the differences and of their squares, whose parts from that row to the mean are taken off
-// at the end, lose the variance where it lies far off: 3 % of it in 1,000,000 rows behind one of 1,000 sigma.)
+// at the end, lose digits where it lies far off: 1,000,000 rows of mean 1,000 and spread 1 behind a row of zeros
+// 6 % of the variance; so 10^-7.)
 #include <algorithm>
 
 #include "mixing.h"
@@ -595,13 +596,13 @@ hipError_t group_norm_of(const GroupArgs& a, bool backward, hipStream_t s) {
 
 }  // namespace
 
-// Rows of a piece: two pieces a compute unit, but no fewer rows than give each thread 4 words. (One
-// or four pieces a compute unit: 40,000 x 512 in four samples 32.3 or 30.3 us for 28.2, its backward
-// 64.1 or 53.4 for 47.0; 91,000 x 128 in one sample 21.3 or 25.3 for 22.1.) Whole steps of a
-// block: 91,000 x 128 in six samples 22.1 us for 25.0.
+// Rows of a piece: two pieces a compute unit, but no fewer rows than give each thread 4 words; the same in both passes.
+// (One or four pieces a compute unit: 40,000 x 512 in four samples 30.2 or 40.6 us for 30.5, its backward 49.7 or 53.7
+// for 46.1; 91,000 x 128 in one sample 23.0 or 30.5 for 25.3, its backward 34.9 or 37.3 for 32.1.) Whole steps of a
+// block: 91,000 x 128 in six samples 22.4 us for 25.3.
 //
-// One launch up to 4 words a thread: a single row 10.0 us a call for 12.7; the rows of 64 words a
-// thread would take 24 for 12.5, one block's loads waiting for each other.
+// One launch up to 4 words a thread: a single row 12.0 us a call for 14.6; the rows of 64 words a
+// thread would take 43 for 14.7, one block's loads waiting for each other.
 void group_plan(GroupArgs& a) {
     const int64_t words = (a.c + W - 1) / W, blocks = 2 * (int64_t)device_cus();
     a.rows_each = (int)std::max<int64_t>((a.n + blocks - 1) / blocks, std::max<int64_t>(1, 4 * kThreads / words));
