@@ -6,7 +6,8 @@
 // registers, and keeps the running maximum and sum of the softmax.
 // P, at most 2^8 (see `maxima`), is rounded to the rows' type for its product with v (half an
 // ulp of each term, beside half an ulp of the sum); the sum of P is taken before
-// the rounding.
+// the rounding. In f16 it is times 2^7 more, within its range: keys of little weight, of which a long window may have
+// enough to count, would be below its normal numbers (95,000 of 5 10^-6 beside one of 1 came out 0.55 % off).
 //
 // 15,000 x 512 in four windows of 3,750, 8 heads of 64: 182 us a call for a floor of 77 (products at
 // 1.5 PFLOP/s), vector units 51 % busy, matrix units 26 %: a score's exponential, scale, sum and rounding
@@ -26,6 +27,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
     // two buffers cost registers (addresses): us for windows of 1,000, 16,000 x 8 heads of 64 without and 40,000 x 4 of 32
     // with cells, one and two: long 73.4, 67.9 and 78.6, 85.2; mid 86.5, 76.6 and 90.1, 82.1
     constexpr int kBuffers = B::kWaves > 2 && (NQ == 1 || EXT == 0) ? 2 : 1;
+    constexpr float kLift = DT == kF16 ? 7.f : 0.f;
     typedef Walk<DT, DP, EXT, A, B, kBuffers> Keys;
     __shared__ __align__(16) typename Keys::Memory s_keys;
     __shared__ __align__(16) uint16_t s_table[B::kHeads][EXT ? 2 * kTableEntries<EXT> : 2];
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
 #pragma unroll
                 for (int d = 0; d < DT16; ++d) o[u][d] *= shrink;
                 top[u] = m;
-                base[u] = next;
+                base[u] = next - kLift;
             }
     };
     auto products = [&](f32x4 (&s)[KB][NQ], int b0, const char* s_v) SMC_INLINE {
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
                                  own[u].row < 0 ? -1 : (int64_t)own[u].row * a.ldo + head * a.dim, a.dim, lane);
             if (a.lse && q == 0 && own[u].row >= 0)
                 a.lse[(int64_t)head * a.n + t.first + (wave * NQ + u) * 16 + col] =
-                    total == 0.f ? -INFINITY : top[u] * (EXT ? 1.f : a.scale) + logf(total);
+                    total == 0.f ? -INFINITY : top[u] * (EXT ? 1.f : a.scale) + logf(total * exp2f(-kLift));
         }
     };
     int i = 0, buf = 0;                 // the step of the head, and its buffer

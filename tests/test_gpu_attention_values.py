@@ -117,3 +117,19 @@ def test_rows_without_channels_are_refused():
     none = torch.empty(4, 0, dtype=BF16, device="cuda")
     with pytest.raises(ValueError, match="channels"):
         smc.window_attention(none, none, none, w, 2)
+
+
+@pytest.mark.parametrize("first", [0, 50000, 95000])
+def test_f16_output_of_many_keys_with_little_weight(first):
+    """One key stands 12.16 above 95,000 others, whose weights of 5 10^-6 beside its own add up to half of it: out is their
+    share. Half an ulp for P as an operand and one for out, the additions of a step each for the products and of four
+    lanes for their sum, two exponentials (2^-21 each)."""
+    n, top = 95001, 12.1640625
+    w = smc.Windows(torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    q, k, v = (torch.zeros(n, 32, dtype=F16, device="cuda") for _ in range(3))
+    q[:, 0], v[:] = 1, 1
+    k[first, 0], v[first] = top, 0
+    out = smc.window_attention(q, k, v, w, 1, scale=1.0)
+    others = (n - 1) * math.exp(-top)
+    tol = 2 * 2.0 ** -11 + ro.gamma(n // 32 + 80) + ro.gamma(n // 4 + 80) + 2 * 2.0 ** -21 + 8 * ro.U * top
+    assert ((out.double() * (1 + others) / others - 1).abs() <= tol).all()
