@@ -135,6 +135,7 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
     };
     auto products = [&](f32x4 (&s)[KB][NQ], int b0, const char* s_v) SMC_INLINE {
         u32x4 p[NQ][KB / 2];
+        float part[NQ];         // of the step: little weights after a large one are not added to it one by one
         // values before the exponentials, which cover their latency (else read two at a time, when they are needed)
         constexpr bool kEarly = DP <= 64 && EXT == 0;
         u32x4 fv[kEarly ? KB / 2 : 1][DT16];
@@ -152,11 +153,13 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[b][u][e] = exp2_of(s[b][u][e] * to_log2 - base[u]);
-                    sum[u] += s[b][u][e];
+                    part[u] = b + e == 0 ? s[b][u][e] : part[u] + s[b][u][e];
                 }
                 p[u][b >> 1][2 * (b & 1)] = pack2<DT>(s[b][u][0], s[b][u][1]);
                 p[u][b >> 1][2 * (b & 1) + 1] = pack2<DT>(s[b][u][2], s[b][u][3]);
             }
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) sum[u] += part[u];
 #pragma unroll
         for (int h = 0; h < KB / 2; ++h)
 #pragma unroll

@@ -133,3 +133,20 @@ def test_f16_output_of_many_keys_with_little_weight(first):
     others = (n - 1) * math.exp(-top)
     tol = 2 * 2.0 ** -11 + ro.gamma(n // 32 + 80) + ro.gamma(n // 4 + 80) + 2 * 2.0 ** -21 + 8 * ro.U * top
     assert ((out.double() * (1 + others) / others - 1).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("cells", [False, True])
+def test_lse_of_many_keys_with_little_weight(dt, cells):
+    """As above, the sum itself: weights are added up over a step (64 keys, 16 a lane), then to those before: n / 64 + 16
+    additions after each other, and four lanes; half as many keys a step in short windows' blocks."""
+    n, top = 95001, 12.0
+    at = dict(coords=torch.zeros(n, 4, dtype=torch.int32, device="cuda"), extent=(1, 1, 1)) if cells else {}
+    w = smc.Windows(torch.tensor([0, n], dtype=torch.int32, device="cuda"), n, **at)
+    table = torch.zeros(3, 3, 1, dtype=dt, device="cuda") if cells else None
+    q, k, v = (torch.zeros(n, 32, dtype=dt, device="cuda") for _ in range(3))
+    q[:, 0], k[0, 0] = 1, top
+    _, lse = smc.window_attention(q, k, v, w, 1, bias=table, scale=1.0, lse=True)
+    others = (n - 1) * math.exp(-top)
+    tol = ro.gamma(n // 32 + 80) + 2.0 ** -21 + 8 * ro.U * top
+    assert ((lse.double() - top - math.log1p(others)).abs() <= tol).all()
