@@ -741,7 +741,7 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  * reaches every row of its head that lies at that distance from a cell of the window's extent.
  * lse (or NULL): log sum_j exp(s_ij), float32 [heads, n] by place (not by row), -inf for
  * zeros' rows; the backward pass reads it. Scores, softmax and sums are float32; P is
- * rounded to dtype for its product with v. out and lse may not overlap each other, q, k, v or bias
+ * rounded to dtype for its product with v (f16: times a power of two, here and for dv, so that little weights keep their digits). out and lse may not overlap each other, q, k, v or bias
  * (SMC_ERR_ARG).
  *
  * Backward, from the same inputs and what the forward call wrote to out and lse, for the
@@ -751,7 +751,7 @@ int smc_windows_build(smc_windows_t* windows, void* stream);
  *   dbias[axis][b][h] = sum of dS over the pairs of the bucket, all windows and rows.
  * P and dS are rounded to dtype as operands of products, but not for dbias (f16: dS times a power of two found
  * on the device, so that finite gradients that fit f16 come out finite). Gradients of rows
- * of no window are zeros. dq, dk and dv may be columns of one buffer; they and dbias may not overlap
+ * of no window are zeros, whatever these rows hold. dq, dk and dv may be columns of one buffer; they and dbias may not overlap
  * an input or each other (SMC_ERR_ARG), but dbias may be bias. workspace:
  * smc_window_attention_backward_workspace(args) bytes,
  * 16-byte aligned; the query reads windows, heads, kv_heads, dtype, bias and reach.

@@ -1,5 +1,5 @@
 """Window attention: values that are not finite in rows of no window and in masked keys,
-probabilities below f16's normal numbers, scales at float32's lower end."""
+probabilities below f16's normal numbers, scales at float32's lower end, rows without channels."""
 import math
 
 import pytest
