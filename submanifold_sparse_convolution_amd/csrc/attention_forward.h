@@ -6,7 +6,7 @@
 // registers, and keeps the running maximum and sum of the softmax.
 // P, at most 2^8 (see `maxima`), is rounded to the rows' type for its product with v (half an
 // ulp of each term, beside half an ulp of the sum); the sum of P is taken before
-// the rounding. In f16 it is times 2^7 more, within its range: keys of little weight, of which a long window may have
+// the rounding. In f16 it is times 2^7, at most 2^15: keys of little weight, of which a long window may have
 // enough to count, would be below its normal numbers (95,000 of 5 10^-6 beside one of 1 came out 0.55 % off).
 //
 // 15,000 x 512 in four windows of 3,750, 8 heads of 64: 182 us a call for a floor of 77 (products at
@@ -20,14 +20,16 @@
 namespace smc {
 namespace {
 
+// (waves a SIMD by what the registers take; left at three, f16's long blocks of heads up to 32 with up to 32 cells take 132:
+// 40,000 x 4 heads in windows of 100 19.1 us for 18.0)
 template <int DT, int DP, int EXT, bool A, class B>
-__global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 2 : 1) void k_attention(AttentionArgs a) {
+__global__ __launch_bounds__(B::kThreads, DP <= 32 && EXT <= 32 ? 4 : DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 2 : 1) void k_attention(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NQ = B::kColumns, TH = B::kThreads;
     // two buffers cost registers (addresses): us for windows of 1,000, 16,000 x 8 heads of 64 without and 40,000 x 4 of 32
     // with cells, one and two: long 73.4, 67.9 and 78.6, 85.2; mid 86.5, 76.6 and 90.1, 82.1
     constexpr int kBuffers = B::kWaves > 2 && (NQ == 1 || EXT == 0) ? 2 : 1;
-    constexpr float kLift = DT == kF16 ? 7.f : 0.f;
+    constexpr float kLift = DT == kF16 ? 7.f : 0.f, kSlack = DT == kF16 ? 7.f : 8.f;     // powers of two (see `maxima`)
     typedef Walk<DT, DP, EXT, A, B, kBuffers> Keys;
     __shared__ __align__(16) typename Keys::Memory s_keys;
     __shared__ __align__(16) uint16_t s_table[B::kHeads][EXT ? 2 * kTableEntries<EXT> : 2];
@@ -106,8 +108,9 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
 #pragma unroll
                 for (int u = 0; u < NQ; ++u) s[b][u][e] = 16 * b + 4 * q + e < left ? s[b][u][e] : -INFINITY;
     };
-    // The base of the exponentials follows the maximum only where that is 2^8 above it: P then stays below 2^8,
-    // as exact as below 1, and out and the sums are seldom rescaled.
+    // The base of the exponentials follows the maximum only where that is 2^kSlack above it: P then stays below 2^8
+    // (f16: 2^15, as a base beyond 2^24 may be rounded 8 down where it was meant to be kLift), as exact as below 1, and
+    // out and the sums are seldom rescaled.
     auto maxima = [&](const f32x4 (&s)[KB][NQ]) SMC_INLINE {
         float most[NQ];
         bool grows = false;
@@ -119,18 +122,18 @@ __global__ __launch_bounds__(B::kThreads, DP + EXT <= 64 ? 3 : DP + EXT < 192 ? 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) m = fmaxf(m, s[b][u][e]);
             most[u] = quad_max(m);
-            grows |= (most[u] - top[u]) * to_log2 > 8.f;       // (of two -inf: no)
+            grows |= (most[u] - top[u]) * to_log2 > kSlack;    // (of two -inf: no)
         }
         if (any_lane(grows))
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
-                const float m = fmaxf(top[u], most[u]), next = m == -INFINITY ? 0.f : m * to_log2;     // (every score -inf so far)
-                const float shrink = exp2_of(top[u] * to_log2 - next);
+                const float m = fmaxf(top[u], most[u]), next = (m == -INFINITY ? 0.f : m * to_log2) - kLift;   // (every score -inf so far)
+                const float shrink = top[u] == -INFINITY ? 0.f : exp2_of(base[u] - next);
                 sum[u] *= shrink;
 #pragma unroll
                 for (int d = 0; d < DT16; ++d) o[u][d] *= shrink;
                 top[u] = m;
-                base[u] = next - kLift;
+                base[u] = next;
             }
     };
     auto products = [&](f32x4 (&s)[KB][NQ], int b0, const char* s_v) SMC_INLINE {

@@ -150,3 +150,44 @@ def test_lse_of_many_keys_with_little_weight(dt, cells):
     others = (n - 1) * math.exp(-top)
     tol = ro.gamma(n // 32 + 80) + 2.0 ** -21 + 8 * ro.U * top
     assert ((lse.double() - top - math.log1p(others)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("length", [30, 100, 700])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 12, 2.0 ** 15])
+@pytest.mark.parametrize("cells", [False, True])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_scores_of_any_size(length, size, cells, dt):
+    """Scores up to 2^35, whose neighbours in float32 are 2^12 apart: the largest takes all, wherever it stands among the
+    keys, and the window's rows get its values to the bit."""
+    g = torch.Generator()
+    g.manual_seed(25)
+    n = 4 * length
+    at = dict(coords=torch.zeros(n, 4, dtype=torch.int32, device="cuda"), extent=(1, 1, 1)) if cells else {}
+    w = smc.Windows(torch.arange(5, dtype=torch.int32, device="cuda") * length, n, **at)
+    table = torch.full((3, 3, 2), 1.5, dtype=dt, device="cuda") if cells else None
+    q = torch.full((n, 64), size, dtype=dt)
+    k = torch.full((n, 64), size / 2, dtype=dt)
+    top = torch.arange(4) * length + torch.tensor([0, length // 2, length - 1, 7])
+    k[top] = size
+    v = torch.randn(n, 64, generator=g).to(dt)
+    out, lse = smc.window_attention(q.cuda(), k.cuda(), v.cuda(), w, 2, bias=table, scale=1.0, lse=True)
+    assert torch.equal(out.cpu(), v[top].repeat_interleave(length, 0))
+    want = 32 * size * size + (4.5 if cells else 0.0)
+    assert ((lse.double() - want).abs() <= 4 * ro.U * want).all()
+
+
+@pytest.mark.parametrize("first", [32768.0, 16384.0, 8192.0])
+@pytest.mark.parametrize("length", [100, 700])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_a_key_little_above_large_scores(first, length, dt):
+    """Scores of 2^25 (2^24, 2^23), scale log 2: a key of the window's last step stands 8 (powers of two) above one of its
+    first, all others have no share. Exponents are exact but for the base's rounding, the same for both."""
+    w = smc.Windows(torch.tensor([0, length], dtype=torch.int32, device="cuda"), length)
+    q, k, v = (torch.zeros(length, 32, dtype=dt, device="cuda") for _ in range(3))
+    q[:, 0], q[:, 1] = 1024, 8
+    k[3, 0], k[3, 1], v[3] = first, 8, 1
+    k[length - 2, 0], k[length - 2, 1], v[length - 2] = first, 9, 3
+    out = smc.window_attention(q, k, v, w, 1, scale=math.log(2.0))
+    want = (3 * 256 + 1) / 257
+    tol = 2 * ro.HALF_ULP[dt] + ro.gamma(100) + 2 * 2.0 ** -21
+    assert ((out.double() - want).abs() <= tol * want).all()
