@@ -19,8 +19,9 @@
 // the gradient's size, which in f16 may leave the type's range where dq and dk do not,
 // so in f16 it is taken times a power of two: |dP - delta| <= 2 dim max |dout| max |v| over
 // the window (finite values), brought to [2^14, 2^15]; k_attention_range finds the maxima. P, for dv, is taken times
-// 2^14 there: in windows of more than some 16,000 rows the mean P is below f16's normal numbers (2^-14), and so are
-// keys of little weight in any (with it 95,000 rows of equal scores lost 0.2 % of dv).
+// 2^12 there: in windows of more than some 16,000 rows the mean P is below f16's normal numbers (2^-14), and so are
+// keys of little weight in any (with it 95,000 rows of equal scores lost 0.2 % of dv). (12 taken off a base is exact up
+// to 2^26; beyond, P is off by the base's half ulp, 4 powers of two and more, and may leave f16.)
 // delta is taken from out, which was rounded: an error of half an ulp of each out term, over the
 // window's mean of k on its way into dq. Where a window's keys fit one tile delta is the mean of dP
 // under P itself instead (long windows average the error away; blocks of 128 queries have no registers for it).
@@ -420,7 +421,7 @@ template <int DT, int DP, int EXT, bool A, class B>
 __global__ __launch_bounds__(B::kThreads, DP <= 64 && DP + EXT <= 160 ? 2 : 1) void k_attention_keys(AttentionArgs a) {
     constexpr int RW = DP / 8, RE = EXT ? EXT / 8 : 4, CK = DP / 32, CE = EXT / 32, DT16 = DP / 16;
     constexpr int NK = B::kColumns, TH = B::kThreads;
-    constexpr float kLift = DT == kF16 ? 14.f : 0.f;            // P is times 2^kLift, by its base
+    constexpr float kLift = DT == kF16 ? 12.f : 0.f;            // P is times 2^kLift, by its base
     // (places past the end have a base of inf, P and dS of 0, also beside k of infinities)
     typedef Walk<DT, DP, EXT, A, B, 1, true> Queries;
     __shared__ __align__(16) typename Queries::Memory s_queries;

@@ -191,3 +191,21 @@ def test_a_key_little_above_large_scores(first, length, dt):
     want = (3 * 256 + 1) / 257
     tol = 2 * ro.HALF_ULP[dt] + ro.gamma(100) + 2 * 2.0 ** -21
     assert ((out.double() - want).abs() <= tol * want).all()
+
+
+@pytest.mark.parametrize("first", [32768.0, 16384.0, 1024.0])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_gradients_beside_large_scores(first, dt):
+    """One key above all others at scores of 2^25 (2^24, 2^20): P is 1 but for the rounding of its base, log2 e of the score,
+    whose half ulp is 2 (1, 2^-5) powers of two, and as much again for lse. dv is that of the sum of dout, no infinity."""
+    length = 100
+    w = smc.Windows(torch.tensor([0, length], dtype=torch.int32, device="cuda"), length)
+    q, k, v = (torch.zeros(length, 32, dtype=dt, device="cuda") for _ in range(3))
+    q[:, 0] = 1024
+    k[3, 0], v[3] = first, 1
+    dout = torch.full_like(q, 2.0 ** -4)
+    out, lse = smc.window_attention(q, k, v, w, 1, scale=1.0, lse=True)
+    assert (out == 1).all()
+    _, _, dv, _ = smc.window_attention_backward(dout, q, k, v, out, lse, w, 1, scale=1.0)
+    off = (dv[3].double() / (length * 2.0 ** -4)).log2()
+    assert (off.abs() <= {32768.0: 4, 16384.0: 2, 1024.0: 2.0 ** -4}[first] + 2 * ro.HALF_ULP[dt] * 1.5).all(), off
